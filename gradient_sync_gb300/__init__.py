@@ -32,6 +32,8 @@ ORDERS = {"ring": AR_ORDER_RING, "rank": AR_ORDER_RANK, "tree": AR_ORDER_TREE, "
 DTYPES = {"f32": AR_F32, "bf16": AR_BF16}
 COLLECTIVES = {"allreduce": AR_ALLREDUCE, "reduce_scatter": AR_REDUCE_SCATTER, "allgather": AR_ALLGATHER}
 KERNELS = {"auto": AR_KERNEL_AUTO, "loads": AR_KERNEL_LOADS, "bulk": AR_KERNEL_BULK}
+LOSS_MEANS = {"token": 0, "sequence": 1}
+PREFERENCE_FORMS = {"sigmoid": 0, "square": 1}
 KERNEL_NAMES = {v: k for k, v in KERNELS.items()}
 
 
@@ -319,6 +321,147 @@ def ar_compressed_allreduce(grads, block: int, dtype="f32", residuals=None, scal
     o = _ptrs(outs) if outs is not None else None
     _check(_lib.load().ar_compressed_allreduce(n, int(count), int(block), DTYPES.get(dtype, dtype), _ptrs(grads),
                                                res, float(scale), o, _stream(stream)), "ar_compressed_allreduce")
+
+
+# ---------------------------------------------------------------- losses
+
+
+def _dtype_of(t) -> int:
+    """The library's type of a torch tensor; TypeError for any other type."""
+    name = str(t.dtype).replace("torch.", "")
+    if name not in ("float32", "bfloat16"):
+        raise TypeError(f"float32 or bfloat16 wanted, got {t.dtype}")
+    return AR_F32 if name == "float32" else AR_BF16
+
+
+def _dense(t, dtype: str, shape, what: str):
+    """Check a contiguous device tensor of one type and shape."""
+    if str(t.dtype) != "torch." + dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{what}: a contiguous {dtype} CUDA tensor of shape {tuple(shape)} wanted, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _row_major(t, what: str):
+    """Check a 2-D device tensor whose rows are contiguous (any row stride)."""
+    if t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: a 2-D CUDA tensor with contiguous rows wanted, got shape {tuple(t.shape)}, "
+                         f"strides {t.stride()} on {t.device}")
+    return max(t.stride(0), t.shape[1])
+
+
+def _logits(logits, labels, temperature):
+    ld = _row_major(logits, "logits")
+    _dense(labels, "int64", logits.shape[:1], "labels")
+    return _lib.ArLogits(_ptr(logits), logits.shape[0], logits.shape[1], ld, _dtype_of(logits), _ptr(labels),
+                         float(temperature))
+
+
+def _gradient(logits, dlogits, grad: bool):
+    """(tensor or None, row stride) of the gradient of the logits."""
+    import torch
+
+    if dlogits is None:
+        if not grad:
+            return None, 0
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
+        raise ValueError("dlogits: the logits' type and shape wanted")
+    return dlogits, _row_major(dlogits, "dlogits")
+
+
+def _output(t, shape, like, what: str):
+    import torch
+
+    if t is None:
+        return torch.empty(shape, dtype=torch.float32, device=like.device)
+    return _dense(t, "float32", shape, what)
+
+
+def ar_loss_workspace(rows: int, n_seq: int) -> int:
+    """Device bytes that the two losses need for `rows` tokens in `n_seq` sequences."""
+    b = _lib.c_size_t()
+    _check(_lib.load().ar_loss_workspace(int(rows), int(n_seq), b), "ar_loss_workspace")
+    return b.value
+
+
+def _loss_workspace(workspace, rows, n_seq, like):
+    need = ar_loss_workspace(rows, n_seq)
+    if workspace is None:
+        import torch
+
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+    if workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace: {need} bytes wanted")
+    return workspace
+
+
+def ar_token_logp(logits, labels, temperature: float = 1.0, logp=None, stream=None):
+    """Log-probabilities of the labelled tokens, [rows] fp32 (0 where the label
+    is negative). `logits` [rows, vocab] fp32 or bf16, any row stride; `labels` int64."""
+    d = _logits(logits, labels, temperature)
+    logp = _output(logp, logits.shape[:1], logits, "logp")
+    _check(_lib.load().ar_token_logp(d, _ptr(logp), _stream(stream)), "ar_token_logp")
+    return logp
+
+
+def ar_policy_loss(logits, labels, old_logp, advantages, seq_start=None, ref_logp=None, clip_low: float = 0.2,
+                   clip_high: float = 0.2, kl_coef: float = 0.0, temperature: float = 1.0, reduction="token",
+                   denominator: float = 0.0, grad_scale: float = 1.0, grad: bool = True, stats=None, logp=None,
+                   dlogits=None, workspace=None, stream=None):
+    """Clipped policy loss with a KL term, and its gradient (see include/ar.h).
+
+    Per-token `old_logp`, `advantages` and optional `ref_logp` are fp32 [rows];
+    `seq_start` int64 [n_seq + 1] row offsets (None: one sequence). `dlogits`
+    may be the logits themselves. Returns (stats [loss, surrogate, kl, clipped
+    share], logp, dlogits or None)."""
+    d = _logits(logits, labels, temperature)
+    rows = logits.shape[0]
+    for t, what in ((old_logp, "old_logp"), (advantages, "advantages"), (ref_logp, "ref_logp")):
+        if t is not None or what != "ref_logp":
+            _dense(t, "float32", (rows,), what)
+    n_seq = 1
+    if seq_start is not None:
+        n_seq = seq_start.numel() - 1
+        _dense(seq_start, "int64", (n_seq + 1,), "seq_start")
+    dlogits, dld = _gradient(logits, dlogits, grad)
+    stats = _output(stats, (4,), logits, "stats")
+    logp = _output(logp, (rows,), logits, "logp")
+    workspace = _loss_workspace(workspace, rows, max(n_seq, 0), logits)
+    desc = _lib.ArPolicyDesc(float(clip_low), float(clip_high), float(kl_coef), LOSS_MEANS.get(reduction, reduction),
+                             float(denominator), float(grad_scale))
+    _check(_lib.load().ar_policy_loss(d, _ptr(old_logp), _ptr(ref_logp), _ptr(advantages), _ptr(seq_start), n_seq,
+                                      desc, _ptr(stats), _ptr(logp), _ptr(dlogits), dld, _ptr(workspace),
+                                      _stream(stream)), "ar_policy_loss")
+    return stats, logp, dlogits
+
+
+def ar_preference_loss(logits, labels, ref_logp, seq_start, beta: float = 0.1, label_smoothing: float = 0.0,
+                       loss="sigmoid", target: float = 0.5, length_normalized: bool = False,
+                       temperature: float = 1.0, denominator: float = 0.0, grad_scale: float = 1.0,
+                       grad: bool = True, stats=None, ratios=None, logp=None, dlogits=None, workspace=None,
+                       stream=None):
+    """Preference loss over paired log ratios, and its gradient (see include/ar.h).
+
+    Sequences 2i and 2i + 1 of `seq_start` (int64 [n_seq + 1]) are the chosen
+    and the rejected answer of pair i; `ref_logp` fp32 [rows]. Returns (stats
+    [loss, chosen reward, rejected reward, accuracy], ratios, logp, dlogits or
+    None)."""
+    d = _logits(logits, labels, temperature)
+    rows, n_seq = logits.shape[0], seq_start.numel() - 1
+    _dense(ref_logp, "float32", (rows,), "ref_logp")
+    _dense(seq_start, "int64", (n_seq + 1,), "seq_start")
+    dlogits, dld = _gradient(logits, dlogits, grad)
+    stats = _output(stats, (4,), logits, "stats")
+    ratios = _output(ratios, (max(n_seq, 0),), logits, "ratios")
+    logp = _output(logp, (rows,), logits, "logp")
+    workspace = _loss_workspace(workspace, rows, max(n_seq, 0), logits)
+    desc = _lib.ArPreferenceDesc(float(beta), PREFERENCE_FORMS.get(loss, loss), float(label_smoothing), float(target),
+                                 int(bool(length_normalized)), float(denominator), float(grad_scale))
+    _check(_lib.load().ar_preference_loss(d, _ptr(ref_logp), _ptr(seq_start), n_seq, desc, _ptr(stats), _ptr(ratios),
+                                          _ptr(logp), _ptr(dlogits), dld, _ptr(workspace), _stream(stream)),
+           "ar_preference_loss")
+    return stats, ratios, logp, dlogits
 
 
 # ---------------------------------------------------------------- status

@@ -29,6 +29,21 @@ class ArFabric(ctypes.Structure):
                 ("ranks_per_server", c_int), ("in_network", c_int), ("shared_memory", c_int)]
 
 
+class ArLogits(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("dtype", c_int), ("labels", c_void_p), ("temperature", c_float)]
+
+
+class ArPolicyDesc(ctypes.Structure):
+    _fields_ = [("clip_low", c_float), ("clip_high", c_float), ("kl_coef", c_float), ("mean", c_int),
+                ("denominator", c_float), ("grad_scale", c_float)]
+
+
+class ArPreferenceDesc(ctypes.Structure):
+    _fields_ = [("beta", c_float), ("form", c_int), ("label_smoothing", c_float), ("target", c_float),
+                ("length_normalized", c_int), ("denominator", c_float), ("grad_scale", c_float)]
+
+
 # name -> (restype, argtypes), in the order of include/ar.h
 SIGNATURES = {
     "ar_plan": (c_int, [ctypes.POINTER(ArDesc), ctypes.POINTER(c_void_p)]),
@@ -56,6 +71,14 @@ SIGNATURES = {
     "ar_compressed_reduce": (c_int, [c_int, c_size_t, c_int, VOIDPP, VOIDPP, c_float, c_int, VOIDPP, c_void_p]),
     "ar_compressed_allreduce": (c_int, [c_int, c_size_t, c_int, c_int, VOIDPP, VOIDPP, c_float, VOIDPP,
                                         c_void_p]),
+    "ar_token_logp": (c_int, [ctypes.POINTER(ArLogits), c_void_p, c_void_p]),
+    "ar_loss_workspace": (c_int, [ctypes.c_int64, ctypes.c_int64, SIZEP]),
+    "ar_policy_loss": (c_int, [ctypes.POINTER(ArLogits), c_void_p, c_void_p, c_void_p, c_void_p, ctypes.c_int64,
+                               ctypes.POINTER(ArPolicyDesc), c_void_p, c_void_p, c_void_p, ctypes.c_int64, c_void_p,
+                               c_void_p]),
+    "ar_preference_loss": (c_int, [ctypes.POINTER(ArLogits), c_void_p, c_void_p, ctypes.c_int64,
+                                   ctypes.POINTER(ArPreferenceDesc), c_void_p, c_void_p, c_void_p, c_void_p,
+                                   ctypes.c_int64, c_void_p, c_void_p]),
     "ar_device_status": (c_int, [c_int]),
     "ar_plan_query": (c_int, [c_void_p]),
     "ar_selftest_wait_timeout": (c_int, [ctypes.c_uint, c_void_p]),

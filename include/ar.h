@@ -533,6 +533,107 @@ ar_status ar_compressed_reduce(int n_ranks, size_t count, int block, const void*
 ar_status ar_compressed_allreduce(int n_ranks, size_t count, int block, ar_dtype dtype, const void* const* grads,
                                   void* const* residuals, float scale, void* const* outs, void* stream);
 
+/* ---------------------------------------------------------------- losses
+ * The losses in front of the gradient exchange: what a post-training step
+ * differentiates to get the gradients that the collectives sum. Each reads a
+ * language model's logits and, where asked, writes the gradient of the logits
+ * in the same call. With x = logits row t, tau = temperature, y = label:
+ *   lp_t = x_y / tau - log sum_j exp(x_j / tau)
+ *   dL/dx_j = dL/dlp_t * ([j = y] - exp(x_j / tau) / sum) / tau
+ * Sums are fp32 or wider; gradients are rounded once, into the logits' type.
+ *
+ * Conventions of the three calls:
+ *  - a row with a negative label is not part of the loss and is not read:
+ *    its log-probability is 0 and its gradient row is zeros, whatever its
+ *    logits and per-token inputs hold. A label >= vocab makes its row's
+ *    outputs, and the statistics, NaN. So does a row of -inf alone; single
+ *    entries of -inf (tokens that are ruled out) have probability 0.
+ *  - sequences are given by n_seq + 1 non-decreasing row offsets in device
+ *    memory; sequence s is rows [seq_start[s], seq_start[s+1]), and may be
+ *    empty or have no labelled row. Rows outside every sequence do not count.
+ *  - device pointers are aligned to their element; rows of logits and of
+ *    gradients may lie further apart than vocab. The gradient may be written
+ *    over the logits (same address and row stride); otherwise outputs must
+ *    not overlap inputs.
+ *  - results do not depend on timing: sums run in a fixed order.             */
+typedef struct {
+  const void* data;      /* device; row t at data + t * ld elements */
+  int64_t rows;          /* tokens, >= 0 */
+  int64_t vocab;         /* >= 1 */
+  int64_t ld;            /* row stride in elements, >= vocab */
+  ar_dtype dtype;
+  const int64_t* labels; /* device, [rows] */
+  float temperature;     /* > 0 */
+} ar_logits;
+
+/* Log-probabilities of the labelled tokens: logp[t] = lp_t. The old and
+ * reference log-probabilities of the two losses below are made by this call.
+ * AR_EINVAL: a NULL or misaligned pointer, a bad size, type or temperature;
+ * AR_EUNSUPPORTED: rows >= 2^31. */
+ar_status ar_token_logp(const ar_logits* logits, float* logp, void* stream);
+
+/* Device bytes (16-byte aligned) that ar_policy_loss and ar_preference_loss
+ * need for `rows` tokens in n_seq sequences. AR_EINVAL: NULL, negative sizes. */
+ar_status ar_loss_workspace(int64_t rows, int64_t n_seq, size_t* bytes);
+
+typedef enum {
+  AR_MEAN_TOKENS = 0,   /* w_t = 1 / labelled tokens */
+  AR_MEAN_SEQUENCES = 1 /* w_t = 1 / (labelled tokens of its sequence *
+                           sequences with any) */
+} ar_loss_mean;
+
+typedef struct {
+  float clip_low, clip_high; /* the ratio is clipped to [1 - low, 1 + high] */
+  float kl_coef;             /* beta >= 0; > 0 needs ref_logp */
+  ar_loss_mean mean;
+  float denominator;         /* > 0: replaces the counted denominator of the
+                                mean (labelled tokens or sequences), e.g. by
+                                the count over all data-parallel ranks */
+  float grad_scale;          /* multiplies the gradient only */
+} ar_policy_desc;
+
+/* The clipped policy loss with a KL term, and its gradient:
+ *   r_t = exp(lp_t - old_logp[t])
+ *   s_t = -min(r_t A_t, clip(r_t, 1 - low, 1 + high) A_t)
+ *   k_t = exp(b) - b - 1, b = ref_logp[t] - lp_t
+ *   L   = sum_t w_t (s_t + beta k_t)
+ *   dL/dlp_t = w_t ([r_t A_t <= clip(r_t) A_t] (-r_t A_t) + beta (1 - exp(b)))
+ * stats[4] (device): L, sum w s, sum w k, and the weighted share of tokens
+ * whose ratio the clip holds. logp [rows] and dlogits (row stride dld; NULL:
+ * no gradient) are outputs. ref_logp may be NULL (no KL term: sum w k is 0).
+ * seq_start NULL: one sequence of all rows (n_seq must be 1). With no labelled
+ * token the statistics and the gradient are 0. */
+ar_status ar_policy_loss(const ar_logits* logits, const float* old_logp, const float* ref_logp,
+                         const float* advantages, const int64_t* seq_start, int64_t n_seq,
+                         const ar_policy_desc* desc, float* stats, float* logp, void* dlogits, int64_t dld,
+                         void* workspace, void* stream);
+
+typedef enum {
+  AR_PREFER_SIGMOID = 0, /* -(1 - e) log sigmoid(z) - e log sigmoid(-z) */
+  AR_PREFER_SQUARE = 1   /* (z - target)^2 */
+} ar_preference_form;
+
+typedef struct {
+  float beta;              /* z = beta (rho_chosen - rho_rejected) */
+  ar_preference_form form;
+  float label_smoothing;   /* e in [0, 0.5], sigmoid form */
+  float target;            /* square form */
+  int length_normalized;   /* rho_s is divided by its labelled tokens */
+  float denominator;       /* > 0: replaces the number of pairs of the mean */
+  float grad_scale;        /* multiplies the gradient only */
+} ar_preference_desc;
+
+/* The preference loss over paired log ratios, and its gradient. Sequence 2i
+ * is the chosen and 2i + 1 the rejected answer of pair i (n_seq even, >= 2):
+ *   rho_s = sum over labelled t of s: lp_t - ref_logp[t]
+ *   L = mean over pairs of the form above
+ * stats[4] (device): L, the means of beta rho_chosen and beta rho_rejected,
+ * and the share of pairs with rho_chosen > rho_rejected. ratios [n_seq] are
+ * the rho_s; logp and dlogits as in ar_policy_loss. */
+ar_status ar_preference_loss(const ar_logits* logits, const float* ref_logp, const int64_t* seq_start,
+                             int64_t n_seq, const ar_preference_desc* desc, float* stats, float* ratios,
+                             float* logp, void* dlogits, int64_t dld, void* workspace, void* stream);
+
 /* ---------------------------------------------------------------- status */
 
 /* Every device-side wait in the library is bounded. One that runs out (for

@@ -34,6 +34,9 @@ COLLECTIVES = {"allreduce": AR_ALLREDUCE, "reduce_scatter": AR_REDUCE_SCATTER, "
 KERNELS = {"auto": AR_KERNEL_AUTO, "loads": AR_KERNEL_LOADS, "bulk": AR_KERNEL_BULK}
 LOSS_MEANS = {"token": 0, "sequence": 1}
 PREFERENCE_FORMS = {"sigmoid": 0, "square": 1}
+PRECISIONS = {"auto": 0, "half": 1, "split": 2}
+ADJUSTS = {"none": 0, "shape": 1, "rms": 2}
+AR_MAX_MATRICES = 192
 KERNEL_NAMES = {v: k for k, v in KERNELS.items()}
 
 
@@ -462,6 +465,109 @@ def ar_preference_loss(logits, labels, ref_logp, seq_start, beta: float = 0.1, l
                                           _ptr(logp), _ptr(dlogits), dld, _ptr(workspace), _stream(stream)),
            "ar_preference_loss")
     return stats, ratios, logp, dlogits
+
+
+# ---------------------------------------------------------------- optimiser
+
+
+class OrthoPlan:
+    """An ar_ortho_plan_t*; destroyed with the object."""
+
+    def __init__(self, handle: int, shapes, in_dtype: int, out_dtype: int):
+        self.handle, self.shapes, self.in_dtype, self.out_dtype = handle, shapes, in_dtype, out_dtype
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h:
+            try:
+                _lib.load().ar_ortho_plan_destroy(h)
+            except Exception:
+                pass
+
+
+def ar_ortho_plan(shapes, in_dtype="f32", out_dtype="f32", steps: int = 5, coefficients=None, eps: float = 1e-7,
+                  precision="auto") -> OrthoPlan:
+    """Plan the orthogonalised update of matrices of the given (rows, cols).
+
+    `in_dtype`: matrices or gradients; `out_dtype`: results or weights.
+    `coefficients`: `steps` triples (a, b, c), default the quintic of the Muon
+    optimiser; see include/ar.h."""
+    shapes = [(int(r), int(c)) for r, c in shapes]
+    n = len(shapes)
+    dims = [(ctypes.c_int64 * max(1, n))(*[s[d] for s in shapes]) for d in (0, 1)]
+    coef = None
+    if coefficients is not None:
+        flat = [float(v) for row in coefficients for v in row]
+        if len(flat) != 3 * steps:
+            raise ValueError(f"coefficients: {steps} triples wanted")
+        coef = (_lib.c_float * len(flat))(*flat)
+    ins, outs = DTYPES.get(in_dtype, in_dtype), DTYPES.get(out_dtype, out_dtype)
+    d = _lib.ArOrthoDesc(n, dims[0], dims[1], ins, outs, int(steps), coef, float(eps),
+                         PRECISIONS.get(precision, precision))
+    h = _lib.c_void_p()
+    _check(_lib.load().ar_ortho_plan(d, h), "ar_ortho_plan")
+    return OrthoPlan(h.value, shapes, ins, outs)
+
+
+def ar_ortho_workspace(plan: OrthoPlan) -> int:
+    """Device bytes that a call with the plan needs."""
+    b = _lib.c_size_t()
+    _check(_lib.load().ar_ortho_workspace(plan.handle, b), "ar_ortho_workspace")
+    return b.value
+
+
+def _matrices(plan: OrthoPlan, tensors, dtype: int, what: str):
+    if tensors is None:
+        return None
+    if len(tensors) != len(plan.shapes):
+        raise ValueError(f"{what}: {len(plan.shapes)} matrices wanted, got {len(tensors)}")
+    arr = (_lib.ArMatrix * max(1, len(tensors)))()
+    for i, (t, shape) in enumerate(zip(tensors, plan.shapes)):
+        ld = _row_major(t, f"{what}[{i}]")
+        if tuple(t.shape) != shape or _dtype_of(t) != dtype:
+            raise ValueError(f"{what}[{i}]: the plan has {shape} of type {dtype}, got {tuple(t.shape)} {t.dtype}")
+        arr[i].data, arr[i].ld = _ptr(t), ld
+    return arr
+
+
+def _ortho_room(plan: OrthoPlan, workspace, like):
+    need = ar_ortho_workspace(plan)
+    if workspace is None:
+        import torch
+
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+    if workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace: {need} bytes wanted")
+    return workspace
+
+
+def ar_orthogonalize(plan: OrthoPlan, matrices, outs=None, workspace=None, stream=None):
+    """Newton-Schulz orthogonalisation of every matrix of the plan; returns `outs`
+    (new tensors by default; may be `matrices` themselves where the types agree)."""
+    if outs is None:
+        import torch
+
+        kind = torch.bfloat16 if plan.out_dtype == AR_BF16 else torch.float32
+        outs = [torch.empty(m.shape, dtype=kind, device=m.device) for m in matrices]
+    a, b = _matrices(plan, matrices, plan.in_dtype, "matrices"), _matrices(plan, outs, plan.out_dtype, "outs")
+    workspace = _ortho_room(plan, workspace, matrices[0])
+    _check(_lib.load().ar_orthogonalize(plan.handle, a, b, _ptr(workspace), _stream(stream)), "ar_orthogonalize")
+    return outs
+
+
+def ar_muon_step(plan: OrthoPlan, params, grads, momenta, lr: float, momentum: float = 0.95, weight_decay: float = 0.0,
+                 nesterov: bool = True, adjust="shape", grad_scale: float = 1.0, params_out=None, momenta_out=None,
+                 workspace=None, stream=None):
+    """One step of the orthogonalised optimiser on every matrix of the plan (see
+    include/ar.h); `params` and `momenta` (fp32) are updated in place unless
+    `params_out` / `momenta_out` are given."""
+    p, g = _matrices(plan, params, plan.out_dtype, "params"), _matrices(plan, grads, plan.in_dtype, "grads")
+    m = _matrices(plan, momenta, AR_F32, "momenta")
+    po, mo = _matrices(plan, params_out, plan.out_dtype, "params_out"), _matrices(plan, momenta_out, AR_F32, "momenta_out")
+    workspace = _ortho_room(plan, workspace, params[0])
+    d = _lib.ArMuonDesc(float(lr), float(momentum), float(weight_decay), int(bool(nesterov)),
+                        ADJUSTS.get(adjust, adjust), float(grad_scale))
+    _check(_lib.load().ar_muon_step(plan.handle, d, p, g, m, po, mo, _ptr(workspace), _stream(stream)), "ar_muon_step")
 
 
 # ---------------------------------------------------------------- status

@@ -44,6 +44,23 @@ class ArPreferenceDesc(ctypes.Structure):
                 ("length_normalized", c_int), ("denominator", c_float), ("grad_scale", c_float)]
 
 
+class ArOrthoDesc(ctypes.Structure):
+    _fields_ = [("n_matrices", c_int), ("rows", ctypes.POINTER(ctypes.c_int64)),
+                ("cols", ctypes.POINTER(ctypes.c_int64)), ("in_dtype", c_int), ("out_dtype", c_int), ("steps", c_int),
+                ("coefficients", ctypes.POINTER(c_float)), ("eps", c_float), ("precision", c_int)]
+
+
+class ArMatrix(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("ld", ctypes.c_int64)]
+
+
+class ArMuonDesc(ctypes.Structure):
+    _fields_ = [("lr", c_float), ("momentum", c_float), ("weight_decay", c_float), ("nesterov", c_int),
+                ("adjust", c_int), ("grad_scale", c_float)]
+
+
+MATRIXP = ctypes.POINTER(ArMatrix)
+
 # name -> (restype, argtypes), in the order of include/ar.h
 SIGNATURES = {
     "ar_plan": (c_int, [ctypes.POINTER(ArDesc), ctypes.POINTER(c_void_p)]),
@@ -79,6 +96,12 @@ SIGNATURES = {
     "ar_preference_loss": (c_int, [ctypes.POINTER(ArLogits), c_void_p, c_void_p, ctypes.c_int64,
                                    ctypes.POINTER(ArPreferenceDesc), c_void_p, c_void_p, c_void_p, c_void_p,
                                    ctypes.c_int64, c_void_p, c_void_p]),
+    "ar_ortho_plan": (c_int, [ctypes.POINTER(ArOrthoDesc), ctypes.POINTER(c_void_p)]),
+    "ar_ortho_plan_destroy": (None, [c_void_p]),
+    "ar_ortho_workspace": (c_int, [c_void_p, SIZEP]),
+    "ar_orthogonalize": (c_int, [c_void_p, MATRIXP, MATRIXP, c_void_p, c_void_p]),
+    "ar_muon_step": (c_int, [c_void_p, ctypes.POINTER(ArMuonDesc), MATRIXP, MATRIXP, MATRIXP, MATRIXP, MATRIXP,
+                             c_void_p, c_void_p]),
     "ar_device_status": (c_int, [c_int]),
     "ar_plan_query": (c_int, [c_void_p]),
     "ar_selftest_wait_timeout": (c_int, [ctypes.c_uint, c_void_p]),

@@ -17,15 +17,6 @@ namespace ar {
 // Bits of the status word.
 enum : unsigned int { kStatusTimeout = 1u };
 
-// The library's sticky per-device status word (read by ar_device_status).
-// Defined here: only one translation unit (fused_tma.cu) includes this file.
-__device__ unsigned int g_ar_status_word;
-
-// Host-visible copy of the status word: one word of page-locked, mapped host
-// memory per device, which the host reads without synchronising. Null until
-// the host has published it (the first executing call on the device).
-__device__ unsigned int* g_ar_status_host;
-
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -63,17 +54,25 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return done != 0;
 }
 
+// Where a device records a wait that ran out: the address of its status word
+// and of the pointer to the host-visible copy (for kernels outside the
+// translation unit that defines them).
+struct StatusRef {
+  unsigned int* word;
+  unsigned int* const* host;
+};
+
 // Wait for the phase with the given parity to complete, at most `limit`
 // polls; stop early if *abort becomes non-zero. Returns false on timeout or
 // abort (and records a timeout).
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32_t limit,
-                                          volatile int* abort) {
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32_t limit, volatile int* abort,
+                                          const StatusRef& status) {
   for (uint32_t i = 0; i < limit; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
   }
-  atomicOr(&g_ar_status_word, kStatusTimeout);
-  if (unsigned int* h = g_ar_status_host) {
+  atomicOr(status.word, kStatusTimeout);
+  if (unsigned int* h = *status.host) {
     // Only one bit exists, so a plain store of it loses nothing to racing
     // writers; the fence makes it visible to the host before the kernel ends.
     *reinterpret_cast<volatile unsigned int*>(h) = kStatusTimeout;
@@ -82,6 +81,22 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
   *abort = 1;
   return false;
 }
+
+#ifdef AR_DEFINE_STATUS_WORDS
+// The library's sticky per-device status word (read by ar_device_status).
+// Defined in one translation unit (fused_tma.cu).
+__device__ unsigned int g_ar_status_word;
+
+// Host-visible copy of the status word: one word of page-locked, mapped host
+// memory per device, which the host reads without synchronising. Null until
+// the host has published it (the first executing call on the device).
+__device__ unsigned int* g_ar_status_host;
+
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32_t limit, volatile int* abort) {
+  const StatusRef status = {&g_ar_status_word, &g_ar_status_host};
+  return mbar_wait(bar, parity, limit, abort, status);
+}
+#endif
 
 // Global -> shared bulk copy of `bytes` (multiple of 16, both addresses
 // 16-byte aligned); completion is counted on `bar`.

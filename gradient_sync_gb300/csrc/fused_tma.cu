@@ -29,6 +29,7 @@
 // after its outstanding copies.
 #include <atomic>
 
+#define AR_DEFINE_STATUS_WORDS
 #include "bulk.cuh"
 #include "common.cuh"
 
@@ -862,6 +863,15 @@ cudaError_t host_status_word(int device, volatile unsigned int** word) {
   }
   *word = h;
   return cudaSuccess;
+}
+
+cudaError_t status_ref(unsigned int** word, unsigned int* const** host) {
+  void *w = nullptr, *h = nullptr;
+  cudaError_t err = cudaGetSymbolAddress(&w, g_ar_status_word);
+  if (err == cudaSuccess) err = cudaGetSymbolAddress(&h, g_ar_status_host);
+  *word = static_cast<unsigned int*>(w);
+  *host = static_cast<unsigned int* const*>(h);
+  return err;
 }
 
 cudaError_t read_device_status(unsigned int* value, bool clear) {

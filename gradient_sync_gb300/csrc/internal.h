@@ -275,6 +275,9 @@ cudaError_t read_device_status(unsigned int* value, bool clear);
 // and makes no CUDA call.
 cudaError_t host_status_word(int device, volatile unsigned int** word);
 volatile unsigned int* host_status_word_if_ready(int device);
+// Device addresses of the current device's status word and of its pointer to
+// the host-visible copy, for kernels of other translation units.
+cudaError_t status_ref(unsigned int** word, unsigned int* const** host);
 // The bulk-copy variant of the fused all-reduce (fused_tma.cu).
 bool tma_shape(int n, int& stages, int& tile_bytes);
 cudaError_t launch_fused_tma(const FusedParams& p, ar_dtype dtype, int stages, int tile_bytes, int sm_budget,

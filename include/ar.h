@@ -634,6 +634,96 @@ ar_status ar_preference_loss(const ar_logits* logits, const float* ref_logp, con
                              int64_t n_seq, const ar_preference_desc* desc, float* stats, float* ratios,
                              float* logp, void* dlogits, int64_t dld, void* workspace, void* stream);
 
+/* ---------------------------------------------------------------- optimiser
+ * The update behind the gradient exchange: the orthogonalised (Muon) step for
+ * weight matrices. With U the update of a rows x cols matrix,
+ *   X = U / (|U|_F + eps); `steps` times: A = X X^T,
+ *   X <- a X + (b A + c A A) X
+ * which takes every singular value s of X through a s + b s^3 + c s^5. The
+ * default coefficients (3.4445, -4.7750, 2.0315), five times, bring singular
+ * values from about 0.003 up into [0.68, 1.13] (published with the Muon
+ * optimiser). A tall matrix is handled as its transpose (X^T X on the other
+ * side), so the products have min(rows, cols) rows.
+ *
+ * All matrices of a plan run together, in 2 + 3 * steps kernels.
+ *
+ * Precision. The products are tensor-core products of fp16 operands with
+ * fp32 sums: AR_PRECISION_HALF rounds each operand to fp16 (X itself is kept
+ * to 22 bits); AR_PRECISION_SPLIT keeps operands as two fp16 numbers and
+ * multiplies three of the four combinations, about 22 bits throughout, at
+ * about 3 times the work. AR_PRECISION_AUTO is SPLIT for AR_F32 results and
+ * HALF for AR_BF16 results (whose own rounding is larger than HALF's error).
+ * Momentum is fp32. A zero matrix gives zeros (with eps > 0); a NaN or an infinity anywhere
+ * in a matrix gives NaN throughout that matrix.                             */
+#define AR_MAX_MATRICES 192
+#define AR_MAX_ORTHO_STEPS 16
+
+typedef struct ar_ortho_plan ar_ortho_plan_t;
+
+typedef enum { AR_PRECISION_AUTO = 0, AR_PRECISION_HALF = 1, AR_PRECISION_SPLIT = 2 } ar_precision;
+
+typedef struct {
+  int n_matrices;             /* 1..AR_MAX_MATRICES */
+  const int64_t* rows;        /* host, [n_matrices], each 1..2^20 */
+  const int64_t* cols;
+  ar_dtype in_dtype;          /* matrices to orthogonalise; gradients */
+  ar_dtype out_dtype;         /* results; weights */
+  int steps;                  /* 1..AR_MAX_ORTHO_STEPS */
+  const float* coefficients;  /* host, [3 * steps]: a, b, c of every step;
+                                 NULL: the default ones */
+  float eps;                  /* >= 0 */
+  ar_precision precision;
+} ar_ortho_desc;
+
+/* A matrix in device memory: element (r, c) at data + r * ld + c elements,
+ * ld >= cols. data is aligned to its element. */
+typedef struct {
+  void* data;
+  int64_t ld;
+} ar_matrix;
+
+/* Build a plan (host only; keeps nothing of the descriptor's arrays).
+ * AR_EINVAL: NULL, a bad count, size, type or precision, eps negative or not
+ * finite, a coefficient not finite. AR_EUNSUPPORTED: more than
+ * AR_MAX_MATRICES matrices, or coefficients under which a singular value that
+ * starts in [0, 1] passes 3.5 in some step, or an eigenvalue of b A + c A A
+ * passes 12 (fp16's range). */
+ar_status ar_ortho_plan(const ar_ortho_desc* desc, ar_ortho_plan_t** out);
+void ar_ortho_plan_destroy(ar_ortho_plan_t* plan);
+
+/* Device bytes (16-byte aligned) that a call with the plan needs. Calls that
+ * overlap on the GPU need workspaces of their own. */
+ar_status ar_ortho_workspace(const ar_ortho_plan_t* plan, size_t* bytes);
+
+/* out[i] = the matrix after the steps above, from in[i]. Arrays of
+ * n_matrices (host). out[i] may be in[i] (same address, stride and type). */
+ar_status ar_orthogonalize(const ar_ortho_plan_t* plan, const ar_matrix* in, const ar_matrix* out, void* workspace,
+                           void* stream);
+
+typedef enum {
+  AR_ADJUST_NONE = 0,  /* 1 */
+  AR_ADJUST_SHAPE = 1, /* sqrt(max(1, rows / cols)) */
+  AR_ADJUST_RMS = 2    /* 0.2 * sqrt(max(rows, cols)): the update's rms is
+                          about 0.2 whatever the shape */
+} ar_adjust;
+
+typedef struct {
+  float lr, momentum, weight_decay;
+  int nesterov;
+  ar_adjust adjust;
+  float grad_scale; /* multiplies the gradients, e.g. 1 / ranks after a sum */
+} ar_muon_desc;
+
+/* One optimiser step. Per matrix, with G = grad_scale * gradient (in_dtype),
+ * M the momentum (fp32) and W the weights (out_dtype):
+ *   M' = momentum M + G;  U = nesterov ? G + momentum M' : M'
+ *   W' = (1 - lr weight_decay) W - lr adjust O(U)
+ * params_out and momenta_out may be NULL (in place), or name the inputs
+ * themselves; otherwise no two arrays of the call overlap. */
+ar_status ar_muon_step(const ar_ortho_plan_t* plan, const ar_muon_desc* desc, const ar_matrix* params,
+                       const ar_matrix* grads, const ar_matrix* momenta, const ar_matrix* params_out,
+                       const ar_matrix* momenta_out, void* workspace, void* stream);
+
 /* ---------------------------------------------------------------- status */
 
 /* Every device-side wait in the library is bounded. One that runs out (for
@@ -643,7 +733,8 @@ ar_status ar_preference_loss(const ar_logits* logits, const float* ref_logp, con
  * work has returned, since initiation is non-blocking (Scaling ML Systems,
  * "Collective communication"). From then on the executing calls
  * (ar_execute, ar_execute_host, ar_execute_noalloc, ar_bind,
- * ar_execute_bound, ar_bucket_allreduce) on that device return AR_ETIMEOUT
+ * ar_execute_bound, ar_bucket_allreduce, ar_orthogonalize, ar_muon_step) on
+ * that device return AR_ETIMEOUT
  * and enqueue nothing, until ar_device_status(1) clears the word. */
 
 /* Read (and clear, if clear != 0) the calling device's sticky status word.

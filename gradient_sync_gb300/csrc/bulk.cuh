@@ -54,6 +54,21 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return done != 0;
 }
 
+// The same for a barrier at which the cluster's other CTAs arrive.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Where a device records a wait that ran out: the address of its status word
 // and of the pointer to the host-visible copy (for kernels outside the
 // translation unit that defines them).
@@ -62,15 +77,8 @@ struct StatusRef {
   unsigned int* const* host;
 };
 
-// Wait for the phase with the given parity to complete, at most `limit`
-// polls; stop early if *abort becomes non-zero. Returns false on timeout or
-// abort (and records a timeout).
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32_t limit, volatile int* abort,
-                                          const StatusRef& status) {
-  for (uint32_t i = 0; i < limit; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
-  }
+// Record that a bounded wait ran out, and raise the abort flag.
+__device__ __forceinline__ void report_timeout(volatile int* abort, const StatusRef& status) {
   atomicOr(status.word, kStatusTimeout);
   if (unsigned int* h = *status.host) {
     // Only one bit exists, so a plain store of it loses nothing to racing
@@ -79,6 +87,19 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
     __threadfence_system();
   }
   *abort = 1;
+}
+
+// Wait for the phase with the given parity to complete, at most `limit`
+// polls; stop early if *abort becomes non-zero. Returns false on timeout or
+// abort (and records a timeout).
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32_t limit, volatile int* abort,
+                                          const StatusRef& status) {
+  for (uint32_t i = 0; i < limit; ++i) {
+    if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+  }
+  report_timeout(abort, status);
   return false;
 }
 

@@ -13,6 +13,8 @@ namespace {
 using namespace ar;
 
 constexpr int64_t kMaxDim = 1 << 20;
+// Plans with at least this many 256 x 256 tiles of X run tiles of two CTAs.
+constexpr int64_t kPairTiles = 64;
 constexpr float kDefault[3] = {3.4445f, -4.7750f, 2.0315f};
 
 size_t esize(ar_dtype d) { return d == AR_BF16 ? 2 : 4; }
@@ -81,6 +83,17 @@ bool valid(const ar_matrix& m, int64_t cols, size_t es) {
   return m.data != nullptr && reinterpret_cast<uintptr_t>(m.data) % es == 0 && m.ld >= cols && m.ld <= INT64_MAX / 8 / kMaxDim;
 }
 
+// Whether every access to rows of `cols` elements can be 16 bytes wide, `step` elements at a time.
+bool wide(const void* p, int64_t ld, int64_t step) {
+  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % step == 0);
+}
+void set_access(OrthoIo& q, int64_t cols, size_t out_size) {
+  q.flat = q.g_ld == cols && (q.m == nullptr || (q.m_ld == cols && q.m_out_ld == cols));
+  q.vec_in = cols % 8 == 0 && wide(q.g, q.g_ld, 8) && wide(q.m, q.m_ld, 8) && wide(q.m_out, q.m_out_ld, 8);
+  const int64_t step = int64_t(16 / out_size);
+  q.vec_out = wide(q.w, q.w_ld, step) && wide(q.w_out, q.w_out_ld, step);
+}
+
 bool same(const ar_matrix& a, const ar_matrix& b) { return a.data == b.data && a.ld == b.ld; }
 
 ar_status guard(const void* workspace) {
@@ -123,6 +136,13 @@ ar_status ar_ortho_plan(const ar_ortho_desc* desc, ar_ortho_plan_t** out) try {
   p.out_dtype = desc->out_dtype;
   p.eps = desc->eps;
   p.split = desc->precision == AR_PRECISION_SPLIT || (desc->precision == AR_PRECISION_AUTO && desc->out_dtype == AR_F32);
+  // Tiles of two CTAs read less per product, but pad row blocks to 256.
+  int64_t work = 0;
+  for (int i = 0; i < n; ++i) {
+    const int64_t r = desc->rows[i], c = desc->cols[i], mb = (std::min(r, c) + 127) / 128, nb = (std::max(r, c) + 127) / 128;
+    work += (mb + 1) / 2 * ((nb + 1) / 2);
+  }
+  p.cluster = work >= kPairTiles ? 2 : 1;
   int64_t at = 0, parts = 0, blocks = 0;
   for (int i = 0; i < n; ++i) {
     const int64_t r = desc->rows[i], c = desc->cols[i];
@@ -131,6 +151,7 @@ ar_status ar_ortho_plan(const ar_ortho_desc* desc, ar_ortho_plan_t** out) try {
     m.m = int32_t(std::min(r, c));
     m.n = int32_t(std::max(r, c));
     m.mb = (m.m + 127) / 128;
+    if (p.cluster > 1) m.mb += m.mb % 2;
     m.nb = (m.n + 127) / 128 * 2;
     // entries of X have rms up to 1 / sqrt(n): held as about 16
     m.sx = std::ldexp(16.0f, int(std::ceil(std::log2(double(m.n)) / 2)));
@@ -148,8 +169,10 @@ ar_status ar_ortho_plan(const ar_ortho_desc* desc, ar_ortho_plan_t** out) try {
     p.rows.push_back(r);
     p.cols.push_back(c);
   }
+  if (at / 128 > INT32_MAX) return AR_EUNSUPPORTED;
   p.part_off = at;
-  p.bytes = at + (4 * parts + 255) / 256 * 256;
+  p.sync_off = at + 4 * parts;
+  p.bytes = at + (4 * (parts + 1 + n) + 255) / 256 * 256;
   p.order.resize(n);
   std::iota(p.order.begin(), p.order.end(), 0);
   std::stable_sort(p.order.begin(), p.order.end(), [&](int a, int b) { return p.mats[a].nb > p.mats[b].nb; });
@@ -185,6 +208,7 @@ ar_status ar_orthogonalize(const ar_ortho_plan_t* plan, const ar_matrix* in, con
     io[i].w_out = out[i].data;
     io[i].w_out_ld = out[i].ld;
     io[i].alpha = 1.0f;
+    set_access(io[i], c, oe);
   }
   if (!apart(std::move(ranges))) return AR_EINVAL;
   const ar_status s = device_ready();
@@ -237,6 +261,7 @@ ar_status ar_muon_step(const ar_ortho_plan_t* plan, const ar_muon_desc* desc, co
                           : desc->adjust == AR_ADJUST_RMS ? 0.2 * std::sqrt(std::max(rows, cols))
                                                           : 1.0;
     q.alpha = float(-double(desc->lr) * adjust);
+    set_access(q, c, we);
   }
   if (!apart(std::move(ranges))) return AR_EINVAL;
   const ar_status s = device_ready();

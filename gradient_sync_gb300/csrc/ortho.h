@@ -37,6 +37,9 @@ struct OrthoIo {
   void* w_out;
   int64_t g_ld, m_ld, m_out_ld, w_ld, w_out_ld;
   float alpha;     // factor of the orthogonal matrix in the result
+  bool flat;       // g, m and m_out are contiguous: element e of the matrix is element e of each
+  bool vec_in;     // g, m and m_out can be read eight elements at a time
+  bool vec_out;    // w and w_out can be accessed 16 bytes at a time
 };
 
 struct OrthoHyper {
@@ -58,7 +61,8 @@ struct ar_ortho_plan {
   ar_dtype in_dtype, out_dtype;
   float eps;
   bool split;
-  int64_t part_off, bytes;
+  int cluster;  // CTAs that work on a tile together: 1, or 2 (row blocks padded to an even number)
+  int64_t part_off, sync_off, bytes;  // partial sums of squares; the products' counters
 };
 
 namespace ar {

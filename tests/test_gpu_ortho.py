@@ -171,7 +171,7 @@ def test_many_matrices(g):
 @pytest.mark.parametrize("precision,dst", [("half", "bf16"), ("split", "f32")])
 def test_large(g, precision, dst):
     """Several tiles a CTA, all of the pipelines' phases; the oracle on the device, in 64 bits."""
-    shapes = [(2048, 2048), (1024, 4096), (3000, 1100)]
+    shapes = [(2048, 2048), (1024, 4096), (3000, 1100), (2900, 1290), (100, 4500)]
     gen = torch.Generator(device="cuda").manual_seed(1)
     mats = [torch.randn(s, generator=gen, device="cuda") for s in shapes]
     outs = g.ar_orthogonalize(g.ar_ortho_plan(shapes, "f32", dst, precision=precision), mats)

@@ -156,11 +156,15 @@ __device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* map, 
       : "memory");
 }
 
-// Arrive at the same barrier in CTA `rank` of the cluster.
+// Arrive at the same barrier in CTA `rank` of the cluster; with `publish`, what
+// this thread has written there before is visible to who waits for it (which
+// takes a fence across the cluster, about a thousand clocks).
+template <bool PUBLISH>
 __device__ __forceinline__ void mbar_arrive_remote(uint64_t* bar, uint32_t rank) {
-  asm volatile(
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(bar, rank))
-      : "memory");
+  if (PUBLISH)
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(bar, rank)) : "memory");
+  else
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(bar, rank)) : "memory");
 }
 
 // 16 or 32 consecutive fp32 columns of this warp's 32 accumulator rows, one row a lane.
@@ -531,8 +535,8 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
   constexpr int SEGMENT = SPLIT ? kSegment : 1 << 30;
   extern __shared__ char smem_raw[];
   __shared__ uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], done, old_full[EPI];
-  __shared__ uint64_t item_full[RING], item_free[RING];
-  __shared__ int items[RING][kTileWords];
+  __shared__ uint64_t item_full[RING], item_free[RING], mail_full[RING], mail_free[RING];
+  __shared__ int items[RING][kTileWords], mail[RING][kTileWords];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   volatile int* abort = &abort_flag;
@@ -554,7 +558,9 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
     }
     for (int s = 0; s < RING; ++s) {
       mbar_init(&item_full[s], 1);
-      mbar_init(&item_free[s], CLUSTER * (EPI + 1) + 1);  // epilogues, producers, tensor core
+      mbar_init(&item_free[s], rank == 0 ? EPI + 2 : EPI + 1);  // epilogue, producer, tensor core
+      mbar_init(&mail_full[s], 1);
+      mbar_init(&mail_free[s], 1);
     }
     for (int w = 0; w < EPI; ++w) mbar_init(&old_full[w], 1);
     mbar_init(&done, 1);
@@ -573,38 +579,49 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
 
   // The n-th tile of this worker.
   auto receive = [&](int n, Tile& t) {
-    const bool ok = mbar_wait<PAIR>(&item_full[n % RING], (n / RING) & 1, kWaitPolls, abort, p.status);
+    const bool ok = mbar_wait(&item_full[n % RING], (n / RING) & 1, kWaitPolls, abort, p.status);
     const volatile int* w = items[n % RING];
     t.op = w[0], t.step = w[1], t.i = w[2], t.tm = w[3], t.tn = w[4], t.nu = w[5], t.ks = w[6];
     __syncwarp();
-    if (lane == 0) {
-      if (PAIR) mbar_arrive_remote(&item_free[n % RING], 0);
-      else mbar_arrive(&item_free[n % RING]);
-    }
+    if (lane == 0) mbar_arrive(&item_free[n % RING]);
     return !__any_sync(~0u, !ok) && t.op != kNone;
   };
 
   if (warp == EPI + 2) {
-    // ---- tiles for the worker
-    if (rank == 0 && lane == 0) {
+    // ---- tiles for the worker: the first CTA takes them and passes them on;
+    // each CTA's warps then hear of them from their own CTA only
+    if (lane == 0) {
       const int n_items = p.steps * (p.total[0] + p.total[1] + p.total[2]);
       for (int n = 0; !*abort; ++n) {
-        const int item = int(atomicAdd(queue, 1u));
-        Tile t = {kNone, 0, 0, 0, 0, 0, 0, 0};
-        if (item < n_items) {
-          t = find_tile<S>(p, item);
-          if (t.need > 0 && !tiles_complete(complete + t.i, unsigned(t.need) * S::PER_TILE, abort, p.status)) break;
-        }
-        if (n >= RING && !mbar_wait<PAIR>(&item_free[n % RING], (n / RING + 1) & 1, kWaitPolls, abort, p.status)) break;
-        const int words[7] = {t.op, t.step, t.i, t.tm, t.tn, t.nu, t.ks};
+        const int s = n % RING;
+        const uint32_t reuse = (n / RING + 1) & 1;
+        int words[7];
+        if (rank == 0) {
+          const int item = int(atomicAdd(queue, 1u));
+          Tile t = {kNone, 0, 0, 0, 0, 0, 0, 0};
+          if (item < n_items) {
+            t = find_tile<S>(p, item);
+            if (t.need > 0 && !tiles_complete(complete + t.i, unsigned(t.need) * S::PER_TILE, abort, p.status)) break;
+          }
+          words[0] = t.op, words[1] = t.step, words[2] = t.i, words[3] = t.tm, words[4] = t.tn, words[5] = t.nu;
+          words[6] = t.ks;
+          if (PAIR) {
+            if (n >= RING && !mbar_wait<true>(&mail_free[s], reuse, kWaitPolls, abort, p.status)) break;
 #pragma unroll
-        for (int w = 0; w < 7; ++w) {
-          items[n % RING][w] = words[w];
-          if (PAIR) store_remote(&items[n % RING][w], 1, words[w]);
+            for (int w = 0; w < 7; ++w) store_remote(&mail[s][w], 1, words[w]);
+            mbar_arrive_remote<true>(&mail_full[s], 1);
+          }
+        } else {
+          if (!mbar_wait<true>(&mail_full[s], (n / RING) & 1, kWaitPolls, abort, p.status)) break;
+#pragma unroll
+          for (int w = 0; w < 7; ++w) words[w] = *static_cast<volatile int*>(&mail[s][w]);
+          mbar_arrive_remote<true>(&mail_free[s], 0);
         }
-        mbar_arrive(&item_full[n % RING]);
-        if (PAIR) mbar_arrive_remote(&item_full[n % RING], 1);
-        if (t.op == kNone) break;
+        if (n >= RING && !mbar_wait(&item_free[s], reuse, kWaitPolls, abort, p.status)) break;
+#pragma unroll
+        for (int w = 0; w < 7; ++w) items[s][w] = words[w];
+        mbar_arrive(&item_full[s]);
+        if (words[0] == kNone) break;
       }
     }
   } else if (warp == EPI) {
@@ -651,7 +668,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
       const int mn_from = is_a ? left_mn_from<S>(t) : right_mn_from<S>(t);
       const uint32_t bytes = HALVES * (S::CTAS * kUnit + t.nu * kUnit);
       for (int k = 0; k < t.ks; ++k) {
-        if (!mbar_wait<PAIR>(&empty[s], phase, kWaitPolls, abort, p.status)) break;
+        if (!mbar_wait(&empty[s], phase, kWaitPolls, abort, p.status)) break;
         // the second CTA's copies count on the first one's barrier
         if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
         const int from = k >= mn_from ? at_mn + (k >> 1) * nb * 128 + (k & 1) * 64 : at_k + k * 128;
@@ -688,7 +705,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
       const uint32_t idesc = instr_desc(S::CTAS * 128, t.nu * 128);
       for (int k0 = 0; k0 < t.ks; k0 += SEGMENT, ++part) {
         const int acc = part & 1;
-        if (part >= 2 && __any_sync(~0u, !mbar_wait<PAIR>(&acc_empty[acc], (part / 2 + 1) & 1, kWaitPolls, abort, p.status)))
+        if (part >= 2 && __any_sync(~0u, !mbar_wait(&acc_empty[acc], (part / 2 + 1) & 1, kWaitPolls, abort, p.status)))
           break;
         fence_after();
         const uint32_t d = tmem + acc * 256;
@@ -741,7 +758,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
       fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (PAIR) mbar_arrive_remote(&acc_empty[acc], 0);
+        if (PAIR) mbar_arrive_remote<false>(&acc_empty[acc], 0);
         else mbar_arrive(&acc_empty[acc]);
       }
     };
@@ -764,7 +781,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
     };
     Tile t;
     for (int n = 0;; ++n) {
-      if (!mbar_try_wait(&item_full[n % RING], (n / RING) & 1)) report(false);
+      if (!mbar_test(&item_full[n % RING], (n / RING) & 1)) report(false);
       __syncwarp();
       if (!receive(n, t)) break;
       const OrthoMat& mat = p.mat[t.i];
@@ -779,9 +796,9 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
       uint32_t at = 0;  // this warp's accumulator
       for (int k0 = 0; k0 < t.ks; k0 += SEGMENT, ++part) {
         const int acc = part & 1;
-        if (owed >= 0 && !mbar_try_wait(&acc_full[acc], (part / 2) & 1)) report(false);
+        if (owed >= 0 && !mbar_test(&acc_full[acc], (part / 2) & 1)) report(false);
         __syncwarp();
-        const bool ok = mbar_wait<PAIR>(&acc_full[acc], (part / 2) & 1, kWaitPolls, abort, p.status);
+        const bool ok = mbar_wait(&acc_full[acc], (part / 2) & 1, kWaitPolls, abort, p.status);
         if (__any_sync(~0u, !ok)) {
           landed = false;
           break;

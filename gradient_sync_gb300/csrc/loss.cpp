@@ -5,13 +5,14 @@
 #include <utility>
 #include <vector>
 
+#include "internal.h"
 #include "loss.h"
 
 namespace {
 
 using namespace ar;
 
-constexpr double kLog2e = 1.4426950408889634074, kLn2 = 0.69314718055994530942;
+constexpr double kLog2e = 1.4426950408889634074;
 
 bool aligned(const void* p, size_t a) { return p != nullptr && reinterpret_cast<uintptr_t>(p) % a == 0; }
 size_t esize(ar_dtype d) { return d == AR_BF16 ? 2 : 4; }
@@ -46,7 +47,7 @@ ar_status logits_params(const ar_logits* l, const float* logp, LossParams& p) {
   if (!(l->temperature > 0.0f) || !std::isfinite(l->temperature)) return AR_EINVAL;
   const double k = kLog2e / double(l->temperature);
   if (!std::isfinite(float(k)) || !std::isfinite(1.0f / l->temperature)) return AR_EINVAL;
-  if (l->rows >= (int64_t(1) << 31)) return AR_EUNSUPPORTED;
+  if (l->rows >= (int64_t(1) << 31) || l->vocab > (int64_t(1) << 30)) return AR_EUNSUPPORTED;
   if (l->rows > 0 && l->ld > INT64_MAX / 8 / l->rows) return AR_EINVAL;
   if (l->rows > 0 && (!aligned(l->data, esize(l->dtype)) || !aligned(l->labels, 8) || !aligned(logp, 4)))
     return AR_EINVAL;
@@ -57,7 +58,6 @@ ar_status logits_params(const ar_logits* l, const float* logp, LossParams& p) {
   p.ld = l->ld;
   p.labels = l->labels;
   p.k = float(k);
-  p.to_ln = kLn2;
   p.inv_temp = float(1.0 / double(l->temperature));
   p.logp = const_cast<float*>(logp);
   return AR_OK;
@@ -84,7 +84,6 @@ ar_status loss_params(const ar_logits* l, const float* logp, float* stats, void*
   const LossLayout w = loss_layout(p.rows, n_seq);
   char* base = static_cast<char*>(workspace);
   p.tickets = reinterpret_cast<unsigned int*>(base);
-  p.total = reinterpret_cast<float*>(base + 16);
   p.seq_count = reinterpret_cast<int32_t*>(base + w.seq_count);
   p.row_a = reinterpret_cast<float*>(base + w.row_a);
   p.row_lse = reinterpret_cast<float2*>(base + w.row_lse);
@@ -110,6 +109,15 @@ bool loss_apart(const ar_logits* l, const LossParams& p, std::vector<Range> more
   return apart(outs, ins);
 }
 
+// Refuses while a device-side wait that ran out is recorded.
+ar_status device_ready() {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return AR_ECUDA;
+  volatile unsigned int* word = nullptr;
+  if (host_status_word(dev, &word) != cudaSuccess) return AR_ECUDA;
+  return *word != 0 ? AR_ETIMEOUT : AR_OK;
+}
+
 ar_status from_cuda(cudaError_t e) { return e == cudaSuccess ? AR_OK : AR_ECUDA; }
 
 }  // namespace
@@ -130,6 +138,7 @@ ar_status ar_token_logp(const ar_logits* logits, float* logp, void* stream) {
   if (overlap(o, matrix_range(p.x, p.rows, p.vocab, p.ld, esize(logits->dtype))) ||
       overlap(o, range(p.labels, 8 * p.rows)))
     return AR_EINVAL;
+  if ((s = device_ready()) != AR_OK) return s;
   return from_cuda(launch_token_logp(p, logits->dtype, static_cast<cudaStream_t>(stream)));
 }
 
@@ -160,6 +169,7 @@ ar_status ar_policy_loss(const ar_logits* logits, const float* old_logp, const f
   p.kl = desc->kl_coef;
   p.seq_start = seq_start;
   p.by_sequence = desc->mean == AR_MEAN_SEQUENCES;
+  if ((s = device_ready()) != AR_OK) return s;
   return from_cuda(launch_policy_loss(p, logits->dtype, static_cast<cudaStream_t>(stream)));
 } catch (const std::bad_alloc&) {
   return AR_ENOMEM;
@@ -187,6 +197,7 @@ ar_status ar_preference_loss(const ar_logits* logits, const float* ref_logp, con
   p.square = desc->form == AR_PREFER_SQUARE;
   p.normalize = desc->length_normalized != 0;
   p.ratios = ratios;
+  if ((s = device_ready()) != AR_OK) return s;
   return from_cuda(launch_preference_loss(p, logits->dtype, static_cast<cudaStream_t>(stream)));
 } catch (const std::bad_alloc&) {
   return AR_ENOMEM;

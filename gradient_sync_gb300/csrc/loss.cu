@@ -10,8 +10,8 @@
 // All of it is kept in base 2: with k = log2(e) / tau and any shift c,
 // e_j = 2^(x_j k - c) is one FMA and one exponential, and two partial sums
 // with shifts c1, c2 combine exactly by 2^(c1 - c2). Sums and shifts are fp32;
-// the few operations a row does once (lp itself) are in fp64, so that lp
-// carries no rounding of the shift or of the logarithm's integer part.
+// the few operations a row does once (lp itself) are in pairs of fp32, so that
+// lp carries no rounding of the shift or of the logarithm's integer part.
 // Shifts are integers.
 // Gradients are rounded once, into the logits' type.
 //
@@ -21,12 +21,22 @@
 // type's lowest value alone is uniform.
 #include "loss.h"
 
+#include <algorithm>
+#include <array>
+#include <mutex>
+#include <vector>
+
+#include "bulk.cuh"
 #include "common.cuh"
 
 namespace ar {
 namespace {
 
-constexpr int kRowThreads = 512;
+// What one thread holds of a row: kVecs 16-byte vectors, so that a row is read
+// once, its sum taken, and the gradient written from registers. With 512
+// threads and clusters of up to 8 CTAs a row that is up to 8 x 32768 bf16 or
+// 8 x 16384 fp32 long; longer ones are read twice.
+constexpr int kVecs = 8;
 constexpr double kExpLow = 4.9e-8;
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -56,53 +66,54 @@ __device__ __forceinline__ Lse lse_join(Lse a, Lse b) {
   const float c = fmaxf(a.c, b.c), z = finite_shift(c);
   return {c, a.s * pow2(a.c - z) + b.s * pow2(b.c - z)};
 }
-
-// Sum of one row over the CTA; every thread gets the result. `part` holds one
-// entry per warp.
-template <int THREADS>
-__device__ __forceinline__ Lse lse_block(Lse v, Lse* part) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    v = lse_join(v, {__shfl_xor_sync(~0u, v.c, o), __shfl_xor_sync(~0u, v.s, o)});
-  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
-  __syncthreads();
-  constexpr int W = THREADS / 32;
-  v = part[threadIdx.x % W];
-#pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1)
+__device__ __forceinline__ Lse lse_warp(Lse v, int width) {
+  for (int o = width / 2; o > 0; o >>= 1)
     v = lse_join(v, {__shfl_xor_sync(~0u, v.c, o), __shfl_xor_sync(~0u, v.s, o)});
   return v;
 }
 
-__device__ __forceinline__ double log_prob(const LossParams& p, float x_label, float k, Lse z) {
-  // z.s = f * 2^e with f in [1/2, 1): the integer part of its logarithm is exact
+// A sum of two floats, for the few operations of a row that need more than 24 bits.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+
+// lp = (x_y k - c - log2 s) ln 2. What cancels is subtracted exactly.
+__device__ __forceinline__ Two log_prob(float x, float k, Lse z) {
+  // s = f * 2^e with f in [1/2, 1): the integer part of its logarithm is exact
   int e = 0;
-  const float f = frexpf(z.s, &e);
+  const float f = frexpf(z.s, &e), c = finite_shift(z.c);
+  const float xk = x * k;
+  const Two a = two_sum(xk, -c), b = two_sum(a.hi, -float(e)), d = two_sum(b.hi, -log2f(f));
+  const float lo = fmaf(x, k, -xk) + a.lo + b.lo + d.lo;
   // The hardware's exponential is low by kExpLow of its value in the mean over
   // its fraction (measured over [-20, 0]), hence the sum too, but for the
   // label's own term where that dominates.
-  const float own = exp2_approx(fmaf(x_label, k, -finite_shift(z.c))) / z.s;
-  const double low = kExpLow * double(1.0f - own);
-  const double above = double(x_label) * double(k) - double(finite_shift(z.c));  // first: both may be huge
-  return (above - (double(e) + double(log2f(f)))) * p.to_ln - low;
+  const float own = exp2_approx(fmaf(x, k, -c)) / z.s;
+  constexpr float kLn2 = 0.69314718f, kLn2Low = float(0.69314718055994530942 - double(kLn2));
+  const float r = d.hi * kLn2;
+  float low = fmaf(d.hi, kLn2, -r) + fmaf(d.hi, kLn2Low, lo * kLn2) - float(kExpLow) * (1.0f - own);
+  if (!isfinite(r) || low != low) return {r, 0.0f};  // -inf or NaN as it is
+  return {r, low};
 }
 
 // The range of a row of `n` elements starting at `base`: `head` elements up to
 // the first 16-byte boundary, `vecs` whole 16-byte vectors, the rest.
 template <int W, int ES>
 struct RowSpan {
-  int head;
-  int64_t vecs;
-  int tail;
-  __device__ __forceinline__ RowSpan(const char* base, int64_t n) {
+  int head, vecs, tail;
+  __device__ __forceinline__ RowSpan(const char* base, int n) {
     const int off = int(reinterpret_cast<uintptr_t>(base) % 16) / ES;
     head = off ? W - off : 0;
-    if (head > n) head = int(n);
+    if (head > n) head = n;
     vecs = (n - head) / W;
-    tail = int(n - head - vecs * W);
+    tail = n - head - vecs * W;
   }
   // The element outside the vectors that thread `i` takes (-1: none).
-  __device__ __forceinline__ int64_t edge(int i) const {
+  __device__ __forceinline__ int edge(int i) const {
     if (i < head) return i;
     return i - head < tail ? head + vecs * W + (i - head) : -1;
   }
@@ -121,118 +132,240 @@ __device__ __forceinline__ void store_one(char* base, int64_t e, float v) {
   const float f[1] = {v};
   L::store(base, e, L::narrow(f));
 }
-template <bool BF16>
-__device__ __forceinline__ void load_vec(const char* base, int64_t e, float (&f)[Lane<BF16, true>::W]) {
-  using L = Lane<BF16, true>;
-  L::widen(L::load(base, e), f);
-}
-template <bool BF16>
-__device__ __forceinline__ void store_vec(char* base, int64_t e, const float (&f)[Lane<BF16, true>::W], bool aligned) {
-  using L = Lane<BF16, true>;
-  if (aligned) {
-    L::store(base, e, L::narrow(f));
-  } else {
-#pragma unroll
-    for (int i = 0; i < L::W; ++i) store_one<BF16>(base, e + i, f[i]);
-  }
+
+// A vector of the logits' type (bf16: two conversions an instruction).
+__device__ __forceinline__ uint4 narrow(const float (&f)[4]) { return Lane<false, true>::narrow(f); }
+__device__ __forceinline__ uint4 narrow(const float (&f)[8]) {
+  uint4 r;
+  auto two = [](float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  };
+  r.x = two(f[0], f[1]), r.y = two(f[2], f[3]), r.z = two(f[4], f[5]), r.w = two(f[6], f[7]);
+  return r;
 }
 
-// One row's gradient: d_j = up * [j = y] - up * p_j, p_j = 2^(x_j k - shift) * inv_sum.
+// The part of a row that one CTA of its cluster takes.
 template <bool BF16, int THREADS>
-__device__ __forceinline__ void write_gradient(const LossParams& p, int64_t t, const char* x, int64_t label, float up,
-                                               float k, float shift, float inv_sum) {
-  constexpr int W = Lane<BF16, true>::W, ES = BF16 ? 2 : 4;
-  char* d = static_cast<char*>(p.d) + t * p.dld * ES;
-  const RowSpan<W, ES> span(x, p.vocab);
-  const bool aligned = (reinterpret_cast<uintptr_t>(d) - reinterpret_cast<uintptr_t>(x)) % 16 == 0;
-  const float g = -up * inv_sum;
-  for (int64_t i = threadIdx.x; i < span.vecs; i += THREADS) {
-    const int64_t e = span.head + i * W;
-    float f[W];
-    load_vec<BF16>(x, e, f);
+struct Slice {
+  static constexpr int W = Lane<BF16, true>::W, ES = BF16 ? 2 : 4;
+  static constexpr int kChunk = THREADS * kVecs;  // vectors held at a time
+  const char* x;
+  RowSpan<W, ES> span;
+  int v0, v1;
+  int edge;  // this thread's element outside the vectors, -1: none
+  __device__ __forceinline__ Slice(const char* row, int vocab, int rank, int ranks) : x(row), span(row, vocab) {
+    const int per = (span.vecs + ranks - 1) / ranks;
+    v0 = min(span.vecs, per * rank);
+    v1 = min(span.vecs, v0 + per);
+    edge = rank == 0 ? span.edge(threadIdx.x) : -1;
+  }
+  __device__ __forceinline__ bool held() const { return v1 - v0 <= kChunk; }
+  // Vectors first + threadIdx.x + j THREADS, -inf beyond the slice. `keep`: the
+  // row will be read again soon.
+  __device__ __forceinline__ void load(uint4 (&raw)[kVecs], int first, bool keep) const {
+    const uint32_t none = BF16 ? 0xFF80FF80u : 0xFF800000u;
+    const int v = first + int(threadIdx.x);
+    const uint4* from = reinterpret_cast<const uint4*>(x + span.head * ES) + v;
 #pragma unroll
-    for (int w = 0; w < W; ++w) f[w] = exp2_approx(fmaf(f[w], k, -shift)) * g;
-    if (label >= e && label < e + W) {
-#pragma unroll
-      for (int w = 0; w < W; ++w)
-        if (label == e + w) f[w] += up;
+    for (int j = 0; j < kVecs; ++j) {
+      raw[j] = make_uint4(none, none, none, none);
+      if (v + j * THREADS < v1) raw[j] = keep ? from[j * THREADS] : __ldcs(from + j * THREADS);
     }
-    store_vec<BF16>(d, e, f, aligned);
   }
-  const int64_t e = span.edge(threadIdx.x);
-  if (e >= 0) {
-    const float v = exp2_approx(fmaf(load_one<BF16>(x, e), k, -shift)) * g;
-    store_one<BF16>(d, e, label == e ? v + up : v);
-  }
+};
+
+// (The packed bf16 maximum instruction measured 1.6 times slower over a whole
+// row than widening first.)
+template <bool BF16>
+__device__ __forceinline__ float largest(const uint4& r) {
+  constexpr int W = Lane<BF16, true>::W;
+  float f[W];
+  Lane<BF16, true>::widen(r, f);
+  float m = f[0];
+#pragma unroll
+  for (int w = 1; w < W; ++w) m = fmaxf(m, f[w]);
+  return m;
 }
 
-template <bool BF16, int THREADS>
-__device__ __forceinline__ void write_zeros(const LossParams& p, int64_t t) {
-  constexpr int W = Lane<BF16, true>::W, ES = BF16 ? 2 : 4;
-  char* d = static_cast<char*>(p.d) + t * p.dld * ES;
-  const RowSpan<W, ES> span(d, p.vocab);
-  const float zero[W] = {};
-  for (int64_t i = threadIdx.x; i < span.vecs; i += THREADS) store_vec<BF16>(d, span.head + i * W, zero, true);
-  const int64_t e = span.edge(threadIdx.x);
-  if (e >= 0) store_one<BF16>(d, e, 0.0f);
-}
-
-// The sum of one row.
-template <bool BF16, int THREADS>
-__device__ __forceinline__ Lse row_lse(const LossParams& p, const char* x, float k, Lse* part) {
-  constexpr int W = Lane<BF16, true>::W, ES = BF16 ? 2 : 4;
-  const RowSpan<W, ES> span(x, p.vocab);
-  Lse z = {-INFINITY, 0.0f};
-  for (int64_t i = threadIdx.x; i < span.vecs; i += THREADS) {
+// This thread's share of the row's sum.
+template <bool BF16>
+__device__ __forceinline__ Lse thread_lse(const uint4 (&raw)[kVecs], float k) {
+  constexpr int W = Lane<BF16, true>::W;
+  float top = largest<BF16>(raw[0]);
+#pragma unroll
+  for (int j = 1; j < kVecs; ++j) top = fmaxf(top, largest<BF16>(raw[j]));
+  const float c = fmaxf(-INFINITY, ceilf(top * k)), shift = finite_shift(c);  // (fmaxf: a NaN alone)
+  float s[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
     float f[W];
-    load_vec<BF16>(x, span.head + i * W, f);
-    float top = f[0];
+    Lane<BF16, true>::widen(raw[j], f);
 #pragma unroll
-    for (int w = 1; w < W; ++w) top = fmaxf(top, f[w]);
-    const float c = fmaxf(z.c, ceilf(top * k)), shift = finite_shift(c);
-    float s = z.s * pow2(z.c - shift);
-#pragma unroll
-    for (int w = 0; w < W; ++w) s += exp2_approx(fmaf(f[w], k, -shift));
-    z = {c, s};
+    for (int w = 0; w < W; ++w) s[w & 1] += exp2_approx(fmaf(f[w], k, -shift));
   }
-  const int64_t e = span.edge(threadIdx.x);
-  if (e >= 0) {
-    const float f = load_one<BF16>(x, e), c = ceilf(f * k);
-    z = lse_join(z, {c, exp2_approx(fmaf(f, k, -finite_shift(c)))});
-  }
-  return lse_block<THREADS>(z, part);
+  return {c, s[0] + s[1]};
 }
 
-// The same with the row's scale. Where x k itself is not finite (a row whose
-// largest logit is near the type's lowest or highest value), two logits differ
-// by 0 or by more than any exponent holds, at any scale: k = 1 serves.
-template <bool BF16, int THREADS>
-__device__ __forceinline__ Lse row_lse_scaled(const LossParams& p, const char* x, float& k, Lse* part) {
-  k = p.k;
-  Lse z = row_lse<BF16, THREADS>(p, x, k, part);
-  if (isinf(z.c)) {
-    k = 1.0f;
-    __syncthreads();
-    z = row_lse<BF16, THREADS>(p, x, k, part);
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ void store_peer(void* p, int rank, float2 v) {
+  const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+  asm volatile(
+      "{\n"
+      ".reg .b32 remote;\n"
+      "mapa.shared::cluster.u32 remote, %0, %1;\n"
+      "st.shared::cluster.v2.f32 [remote], {%2, %3};\n"
+      "}\n" ::"r"(a),
+      "r"(rank), "f"(v.x), "f"(v.y)
+      : "memory");
+}
+
+// The same counted (8 bytes) on a barrier of that CTA, which needs no fence between the CTAs.
+__device__ __forceinline__ void send_peer(void* p, uint64_t* bar, int rank, float2 v) {
+  asm volatile(
+      "{\n"
+      ".reg .b32 to, count;\n"
+      "mapa.shared::cluster.u32 to, %0, %2;\n"
+      "mapa.shared::cluster.u32 count, %1, %2;\n"
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [to], {%3, %4}, [count];\n"
+      "}\n" ::"r"(smem_u32(p)),
+      "r"(smem_u32(bar)), "r"(rank), "f"(v.x), "f"(v.y)
+      : "memory");
+}
+
+// One token's part of the policy loss.
+struct PolicyTerm {
+  float terms[3];  // weighted surrogate, KL, whether the clip holds the ratio
+  float up;        // slope of the loss in x_y
+};
+__device__ __forceinline__ PolicyTerm policy_term(const LossParams& p, float lp, float weight, float mean, float adv,
+                                                  float old, float ref) {
+  const float ratio = expf(lp - old), free = ratio * adv;
+  const float held = (ratio < p.lo ? p.lo : ratio > p.hi ? p.hi : ratio) * adv;  // NaN stays NaN
+  const float w = weight * mean;
+  float slope = free <= held ? -free : free > held ? 0.0f : free;
+  PolicyTerm r = {{-w * (free < held || free != free ? free : held), 0.0f, held < free ? w : 0.0f}, 0.0f};
+  if (p.ref_logp != nullptr) {
+    const float back = ref - lp, grow = expm1f(back);
+    r.terms[1] = w * (grow - back);
+    slope -= p.kl * grow;
   }
-  return z;
+  r.up = w * slope * p.grad_scale * p.inv_temp;
+  if (weight == 0.0f) r = {{0.0f, 0.0f, 0.0f}, 0.0f};  // outside every sequence
+  return r;
+}
+
+constexpr int kMaxCluster = 8;
+struct RowShared {
+  Lse warp[16];
+  float2 cta[kMaxCluster];
+};
+
+// The row's sum, from every thread's; the same bits in every thread of the
+// cluster. May be called again after a barrier.
+template <int THREADS>
+__device__ __forceinline__ Lse row_sum(Lse v, RowShared& sh, int rank, int ranks) {
+  constexpr int W = THREADS / 32;
+  v = lse_warp(v, 32);
+  if (threadIdx.x % 32 == 0) sh.warp[threadIdx.x / 32] = v;
+  __syncthreads();
+  v = lse_warp(sh.warp[threadIdx.x % W], W);
+  if (ranks > 1) {
+    if (threadIdx.x < ranks) store_peer(&sh.cta[rank], threadIdx.x, make_float2(v.c, v.s));
+    cluster_barrier();
+    v = {sh.cta[0].x, sh.cta[0].y};
+    for (int r = 1; r < ranks; ++r) v = lse_join(v, {sh.cta[r].x, sh.cta[r].y});
+  }
+  return v;
+}
+
+template <bool BF16, int THREADS>
+__device__ __forceinline__ Lse row_lse(const Slice<BF16, THREADS>& slice, uint4 (&raw)[kVecs], float edge, float k,
+                                       RowShared& sh, int rank, int ranks) {
+  Lse z = {-INFINITY, 0.0f};
+  if (slice.held()) {
+    z = thread_lse<BF16>(raw, k);
+  } else {
+#pragma unroll 1
+    for (int first = slice.v0; first < slice.v1; first += slice.kChunk) {
+      slice.load(raw, first, true);
+      z = lse_join(z, thread_lse<BF16>(raw, k));
+    }
+  }
+  if (slice.edge >= 0) {
+    const float c = fmaxf(-INFINITY, ceilf(edge * k));
+    z = lse_join(z, {c, exp2_approx(fmaf(edge, k, -finite_shift(c)))});
+  }
+  return row_sum<THREADS>(z, sh, rank, ranks);
+}
+
+// The gradient of this CTA's part of a row, from the vectors held:
+// d_j = up * [j = y] - up * p_j, p_j = 2^(x_j k - shift) * inv_sum.
+template <bool BF16, int THREADS>
+__device__ __forceinline__ void write_gradient(const Slice<BF16, THREADS>& slice, char* d, uint4 (&raw)[kVecs], float edge,
+                                               int64_t label, float up, float k, float shift, float inv_sum) {
+  using L = Lane<BF16, true>;
+  constexpr int W = L::W;
+  const bool aligned = (reinterpret_cast<uintptr_t>(d) - reinterpret_cast<uintptr_t>(slice.x)) % 16 == 0;
+  const float g = -up * inv_sum;
+  const int own = int(label) - slice.span.head;  // the label's place among the vectors' elements
+#pragma unroll 1
+  for (int first = slice.v0; first < slice.v1; first += slice.kChunk) {
+    if (!slice.held()) slice.load(raw, first, false);
+    const int v = first + int(threadIdx.x);
+    char* to = d + (slice.span.head + int64_t(v) * W) * slice.ES;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      if (v + j * THREADS >= slice.v1) continue;
+      float f[W];
+      L::widen(raw[j], f);
+#pragma unroll
+      for (int w = 0; w < W; ++w) f[w] = exp2_approx(fmaf(f[w], k, -shift)) * g;
+      const int at = own - (v + j * THREADS) * W;
+      if (unsigned(at) < unsigned(W)) {
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+          if (at == w) f[w] += up;
+      }
+      if (aligned) {
+        L::store(to, j * THREADS * W, narrow(f));
+      } else {
+#pragma unroll
+        for (int w = 0; w < W; ++w) store_one<BF16>(to, j * THREADS * W + w, f[w]);
+      }
+    }
+  }
+  if (slice.edge >= 0) {
+    const float v = exp2_approx(fmaf(edge, k, -shift)) * g;
+    store_one<BF16>(d, slice.edge, label == slice.edge ? v + up : v);
+  }
+}
+
+// Zeros in this CTA's part of a gradient row.
+template <bool BF16, int THREADS>
+__device__ __forceinline__ void write_zeros(char* d, int vocab, int rank, int ranks) {
+  const Slice<BF16, THREADS> slice(d, vocab, rank, ranks);
+  uint4* to = reinterpret_cast<uint4*>(d + slice.span.head * slice.ES);
+  for (int v = slice.v0 + int(threadIdx.x); v < slice.v1; v += THREADS) __stcs(to + v, make_uint4(0, 0, 0, 0));
+  if (slice.edge >= 0) store_one<BF16>(d, slice.edge, 0.0f);
 }
 
 // ---------------------------------------------------------------- sequences
 
-// Labelled tokens of each sequence (one CTA a sequence), the rows' weights,
-// and, by the CTA that finishes last, 1 / (the loss's denominator).
+__device__ __forceinline__ int64_t seq_bound(const LossParams& p, int64_t i) {
+  const int64_t v = p.seq_start == nullptr ? (i == 0 ? 0 : p.rows) : p.seq_start[i];
+  return v < 0 ? int64_t(0) : v > p.rows ? p.rows : v;
+}
+
+// Labelled tokens of each sequence (one CTA a sequence), and the rows' weights
+// before the mean's denominator.
 __global__ void __launch_bounds__(256) count_kernel(LossParams p) {
   grid_dependency_wait();
   grid_dependents_launch();
-  const int64_t s = blockIdx.x;
-  auto bound = [&](int64_t i) {
-    const int64_t v = p.seq_start == nullptr ? (i == 0 ? 0 : p.rows) : p.seq_start[i];
-    return v < 0 ? int64_t(0) : v > p.rows ? p.rows : v;
-  };
-  const int64_t lo = bound(s), hi = bound(s + 1);
+  const int64_t s = blockIdx.x, lo = seq_bound(p, s), hi = seq_bound(p, s + 1);
   __shared__ int warp_sum[8];
-  __shared__ bool last;
   int n = 0;
   for (int64_t t = lo + threadIdx.x; t < hi; t += 256) n += p.labels[t] >= 0;
   n = __reduce_add_sync(~0u, n);
@@ -247,126 +380,555 @@ __global__ void __launch_bounds__(256) count_kernel(LossParams p) {
     for (int64_t t = threadIdx.x; t < lo; t += 256) p.row_a[t] = 0.0f;
   if (s == p.n_seq - 1)
     for (int64_t t = hi + threadIdx.x; t < p.rows; t += 256) p.row_a[t] = 0.0f;
-  if (threadIdx.x == 0) {
-    p.seq_count[s] = n;
-    __threadfence();
-    last = atomicAdd(&p.tickets[0], 1u) == gridDim.x - 1;
-  }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  long long sum = 0;  // labelled tokens, or sequences that have any
-  for (int64_t i = threadIdx.x; i < p.n_seq; i += 256) {
-    const int c = __ldcg(&p.seq_count[i]);
-    sum += p.by_sequence ? (c > 0) : c;
-  }
-  __shared__ long long parts[256];
-  parts[threadIdx.x] = sum;
-  __syncthreads();
-  for (int o = 128; o > 0; o >>= 1) {
-    if (threadIdx.x < o) parts[threadIdx.x] += parts[threadIdx.x + o];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0)
-    p.total[0] = p.denominator > 0.0f ? 1.0f / p.denominator : 1.0f / float(parts[0] > 0 ? parts[0] : 1);
+  if (threadIdx.x == 0) p.seq_count[s] = n;
 }
 
-// Sums `n` entries of four columns (stride `pitch` between columns) in a fixed
-// order, in fp64. Result in thread 0.
-template <int THREADS>
-__device__ void sum_columns(const float* col, int64_t pitch, int64_t n, int columns, double* shared, double (&out)[4]) {
-  for (int c = 0; c < columns; ++c) {
-    double a = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += THREADS) a += double(__ldcg(col + c * pitch + i));
-    __syncthreads();
-    shared[threadIdx.x] = a;
-    __syncthreads();
-    for (int o = THREADS / 2; o > 0; o >>= 1) {
-      if (threadIdx.x < o) shared[threadIdx.x] += shared[threadIdx.x + o];
-      __syncthreads();
-    }
-    out[c] = shared[0];
+// 1 / (the mean's denominator), by one warp.
+__device__ __forceinline__ float mean_scale(const LossParams& p) {
+  if (p.denominator > 0.0f) return 1.0f / p.denominator;
+  int64_t sum = 0;
+  for (int64_t i = threadIdx.x % 32; i < p.n_seq; i += 32) {
+    const int c = p.seq_count[i];
+    sum += p.by_sequence ? (c > 0) : c;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  return 1.0f / float(sum > 0 ? sum : 1);
+}
+
+// Sums `n` entries of each of COLUMNS columns (`pitch` apart) in a fixed order,
+// by the CTA; results in thread 0.
+template <int THREADS, int COLUMNS>
+__device__ __forceinline__ void sum_columns(const float* col, int64_t pitch, int64_t n, double (&out)[COLUMNS]) {
+  __shared__ double warp_sum[COLUMNS][THREADS / 32];
+  float a[COLUMNS];
+#pragma unroll
+  for (int c = 0; c < COLUMNS; ++c) {
+    a[c] = 0.0f;
+    for (int64_t i = threadIdx.x; i < n; i += THREADS) a[c] += __ldcg(col + c * pitch + i);
+  }
+#pragma unroll
+  for (int c = 0; c < COLUMNS; ++c) {
+    double s = double(a[c]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+    if (threadIdx.x % 32 == 0) warp_sum[c][threadIdx.x / 32] = s;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < COLUMNS; ++c) {
+    out[c] = 0.0;
+    if (threadIdx.x == 0)
+      for (int w = 0; w < THREADS / 32; ++w) out[c] += warp_sum[c][w];
   }
 }
 
 // ---------------------------------------------------------------- rows
 
-template <bool BF16, int MODE>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(LossParams p) {
+// One cluster a row.
+template <bool BF16, int MODE, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) rows_kernel(LossParams p) {
   constexpr int ES = BF16 ? 2 : 4;
-  __shared__ Lse part[kRowThreads / 32];
+  __shared__ RowShared sh;
+  __shared__ float mean_shared;
   grid_dependency_wait();
   grid_dependents_launch();
-  const int64_t t = blockIdx.x;
+  const int ranks = p.cluster, rank = int(blockIdx.x) % ranks;
+  // the gradient of a pair's rows starts with the rows that were read last
+  const int64_t at = blockIdx.x / ranks, t = MODE == kPrefBackward ? p.rows - 1 - at : at;
   const char* x = static_cast<const char*>(p.x) + t * p.ld * ES;
+  char* d = p.d == nullptr ? nullptr : static_cast<char*>(p.d) + t * p.dld * ES;
+  if (MODE == kPrefForward && blockIdx.x == 0 && threadIdx.x == 0) p.tickets[0] = 0;
   const int64_t label = p.labels[t];
-  const bool active = label >= 0;
-  if (MODE == kPrefBackward) {
-    if (!active) {
-      write_zeros<BF16, kRowThreads>(p, t);
-      return;
+  if (label < 0) {
+    if ((MODE == kPolicy || MODE == kPrefBackward) && d != nullptr) write_zeros<BF16, THREADS>(d, int(p.vocab), rank, ranks);
+    if (MODE != kPrefBackward && rank == 0 && threadIdx.x == 0) {
+      p.logp[t] = 0.0f;
+      if (MODE == kPolicy)
+        for (int c = 0; c < 3; ++c) p.row_terms[c * p.rows + t] = 0.0f;
     }
-    const float2 z = p.row_lse[t];  // the sign of 1 / sum tells the scale
-    write_gradient<BF16, kRowThreads>(p, t, x, label, p.row_a[t] * p.inv_temp, z.y < 0.0f ? 1.0f : p.k, z.x,
-                                      fabsf(z.y));
     return;
   }
-  float terms[3] = {0.0f, 0.0f, 0.0f};
-  float lp = 0.0f;
-  if (!active) {
-    if (MODE == kPolicy && p.d != nullptr) write_zeros<BF16, kRowThreads>(p, t);
-  } else {
-    const float x_label = label < p.vocab ? load_one<BF16>(x, label) : __int_as_float(0x7fffffff);
-    float k;
-    // (barriers inside: x_label is read before any gradient is written)
-    const Lse z = row_lse_scaled<BF16, kRowThreads>(p, x, k, part);
-    const double exact_lp = log_prob(p, x_label, k, z);
-    lp = float(exact_lp);
-    const float shift = finite_shift(z.c);
-    if (MODE == kPrefForward && threadIdx.x == 0) {
-      // the log ratio before lp is rounded: sequences sum hundreds of them
-      p.row_terms[t] = float(exact_lp - double(p.ref_logp[t]));
-      p.row_lse[t] = make_float2(shift, copysignf(1.0f / z.s, k == p.k ? 1.0f : -1.0f));
-    }
-    const float weight = MODE == kPolicy ? p.row_a[t] : 0.0f;
-    if (MODE == kPolicy && weight == 0.0f) {  // outside every sequence
-      if (p.d != nullptr) write_zeros<BF16, kRowThreads>(p, t);
-    } else if (MODE == kPolicy) {
-      const float adv = p.adv[t];
-      const float ratio = expf(lp - p.old_logp[t]);
-      const float free = ratio * adv;
-      const float held = (ratio < p.lo ? p.lo : ratio > p.hi ? p.hi : ratio) * adv;  // NaN stays NaN
-      const float w = weight * p.total[0];
-      float slope = free <= held ? -free : free > held ? 0.0f : free;
-      terms[0] = -w * (free < held || free != free ? free : held);
-      terms[2] = held < free ? w : 0.0f;
-      if (p.ref_logp != nullptr) {
-        const float back = p.ref_logp[t] - lp;
-        const float grow = expm1f(back);
-        terms[1] = w * (grow - back);
-        slope -= p.kl * grow;
-      }
-      if (p.d != nullptr) {
-        const float up = w * slope * p.grad_scale * p.inv_temp;
-        write_gradient<BF16, kRowThreads>(p, t, x, label, label < p.vocab ? up : __int_as_float(0x7fffffff), k, shift,
-                                          1.0f / z.s);
-      }
+  const Slice<BF16, THREADS> slice(x, int(p.vocab), rank, ranks);
+  uint4 raw[kVecs];
+  const bool keep = MODE == kPrefForward && (p.rows - t) * p.vocab * ES < p.keep_bytes;
+  slice.load(raw, slice.v0, keep);
+  const float edge = slice.edge >= 0 ? load_one<BF16>(x, slice.edge) : -INFINITY;
+  if (MODE == kPrefBackward) {
+    const float2 z = p.row_lse[t];  // the sign of 1 / sum tells the scale
+    write_gradient<BF16, THREADS>(slice, d, raw, edge, label, p.row_a[t] * p.inv_temp, z.y < 0.0f ? 1.0f : p.k, z.x,
+                                  fabsf(z.y));
+    return;
+  }
+  const float nan = __int_as_float(0x7fffffff);
+  // (barriers follow: this is read before any gradient is written)
+  const float x_label = label < p.vocab ? load_one<BF16>(x, label) : nan;
+  float weight = 0.0f, adv = 0.0f, old = 0.0f, ref = 0.0f;
+  if (MODE == kPolicy) {
+    weight = p.row_a[t];
+    adv = p.adv[t];
+    old = p.old_logp[t];
+    if (threadIdx.x < 32) {
+      const float m = mean_scale(p);
+      if (threadIdx.x == 0) mean_shared = m;
     }
   }
-  if (threadIdx.x == 0) p.logp[t] = lp;
+  if ((MODE == kPolicy || MODE == kPrefForward) && p.ref_logp != nullptr) ref = p.ref_logp[t];
+  // Where x k itself is not finite (a row whose largest logit is near the
+  // type's lowest or highest value), two logits differ by 0 or by more than any
+  // exponent holds, at any scale: k = 1 serves.
+  float k = p.k;
+  Lse z = row_lse<BF16, THREADS>(slice, raw, edge, k, sh, rank, ranks);
+  if (isinf(z.c)) {
+    k = 1.0f;
+    __syncthreads();
+    if (ranks > 1) cluster_barrier();
+    z = row_lse<BF16, THREADS>(slice, raw, edge, k, sh, rank, ranks);
+  }
+  const Two exact = log_prob(x_label, k, z);
+  const float lp = exact.hi + exact.lo, shift = finite_shift(z.c), inv_sum = 1.0f / z.s;
+  const bool teller = rank == 0 && threadIdx.x == 0;
+  if (teller) p.logp[t] = lp;
+  if (MODE == kPrefForward && teller) {
+    // the log ratio before lp is rounded: sequences sum hundreds of them
+    p.row_terms[t] = (exact.hi - ref) + exact.lo;
+    p.row_lse[t] = make_float2(shift, copysignf(inv_sum, k == p.k ? 1.0f : -1.0f));
+  }
   if (MODE != kPolicy) return;
-  __shared__ bool last;
-  __shared__ double sums[kRowThreads];
+  const PolicyTerm term = policy_term(p, lp, weight, mean_shared, adv, old, ref);
+  if (d != nullptr) {
+    if (weight == 0.0f)
+      write_zeros<BF16, THREADS>(d, int(p.vocab), rank, ranks);
+    else
+      write_gradient<BF16, THREADS>(slice, d, raw, edge, label, label < p.vocab ? term.up : nan, k, shift, inv_sum);
+  }
+  if (teller)
+    for (int c = 0; c < 3; ++c) p.row_terms[c * p.rows + t] = term.terms[c];
+}
+
+// ---------------------------------------------------------------- many rows
+
+// Rows streamed through shared memory, for calls with many long rows: one
+// persistent CTA an SM, clusters of `p.cluster` CTAs sharing each row. A
+// producer warp copies rows in chunks of 32 KB, up to three rows ahead; 16
+// warps take sums and write gradients; one warp finishes a row (joins the
+// warps' and the cluster's sums, takes the logarithm, decides the loss's slope).
+// The sums of row n + 1 are taken before the gradient of row n is written, from
+// the same shared memory, so nothing waits for the finisher and each row
+// crosses HBM once each way.
+constexpr int kStreamWarps = 16, kStreamThreads = kStreamWarps * 32 + 64;
+constexpr int kStreamChunk = 32768, kStreamChunks = 6, kStreamRows = 4;
+constexpr int kStreamSlice = 65536;  // bytes of a row per CTA, at most, where a row is held until its gradient is written
+constexpr uint32_t kWaitPolls = 1u << 22;
+
+struct StreamRow {
+  int64_t t, label;   // t < 0: no more rows
+  int head, v0, v1;   // elements before the vectors; this CTA's vectors
+};
+struct StreamResult {
+  float k, shift, g, up;
+};
+struct StreamShared {
+  uint64_t full[kStreamChunks], empty[kStreamChunks];
+  uint64_t row_full[kStreamRows], row_free[kStreamRows], sum_full[kStreamRows], result_full[kStreamRows];
+  uint64_t cta_full[kStreamRows];
+  StreamRow row[kStreamRows];
+  StreamResult result[kStreamRows];
+  Lse warp_sum[kStreamRows][kStreamWarps];
+  float2 cta_sum[kStreamRows][kMaxCluster];
+  int abort_flag;
+};
+
+// A copy that is not kept in the L2 (`once`) or is.
+__device__ __forceinline__ void stream_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, bool once,
+                                            uint64_t evict_first) {
+  if (once)
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(evict_first)
+        : "memory");
+  else
+    bulk_load(dst, src, bytes, bar);
+}
+
+// Adds a vector to a running sum, raising its shift where needed.
+template <bool BF16>
+__device__ __forceinline__ void lse_add(Lse& z, const uint4& raw, float k) {
+  constexpr int W = Lane<BF16, true>::W;
+  const float c = ceilf(largest<BF16>(raw) * k);
+  if (c > z.c) {
+    z.s *= pow2(z.c - c);
+    z.c = c;
+  }
+  const float shift = finite_shift(z.c);
+  float f[W];
+  Lane<BF16, true>::widen(raw, f);
+#pragma unroll
+  for (int w = 0; w < W; ++w) z.s += exp2_approx(fmaf(f[w], k, -shift));
+}
+
+// The terms of a vector at a fixed shift.
+template <bool BF16>
+__device__ __forceinline__ float terms_of(const uint4& raw, float k, float shift) {
+  constexpr int W = Lane<BF16, true>::W;
+  float f[W];
+  Lane<BF16, true>::widen(raw, f);
+#pragma unroll
+  for (int w = 0; w < W; ++w) f[w] = exp2_approx(fmaf(f[w], k, -shift));
+#pragma unroll
+  for (int n = W / 2; n > 0; n /= 2)
+#pragma unroll
+    for (int w = 0; w < n; ++w) f[w] += f[w + n];
+  return f[0];
+}
+
+// A thread of the streaming kernel takes its shift from the first vectors of a
+// row that it sees, and no maximum after that: fp32 holds terms up to 2^127
+// times the shift's. kLeastShift keeps vectors that a mask has filled with low
+// values from setting it. Sums that left the range all the same (an overflow,
+// or nothing but tiny terms) are taken again by the finisher, with the maximum.
+constexpr float kLeastShift = -64.0f, kLeastSum = 1e-18f;
+
+template <bool BF16, int MODE>
+__global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p) {
+  using L = Lane<BF16, true>;
+  constexpr int W = L::W, ES = BF16 ? 2 : 4;
+  constexpr bool SUM = MODE != kPrefBackward, WRITE = MODE == kPolicy || MODE == kPrefBackward;
+  constexpr int kVecsChunk = kStreamChunk / 16, kThreadVecs = kVecsChunk / (kStreamWarps * 32);
+  using Part = Slice<BF16, kStreamWarps * 32>;
+  extern __shared__ char raw_shared[];
+  char* chunks = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(raw_shared) + 127) & ~uintptr_t(127));
+  __shared__ StreamShared sh;
+  volatile int* abort = &sh.abort_flag;
+  const StatusRef status = {p.status_word, p.status_host};
+  const int ranks = p.cluster, rank = int(blockIdx.x) % ranks;
+  const int64_t worker = blockIdx.x / ranks, workers = gridDim.x / ranks;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
-    for (int c = 0; c < 3; ++c) p.row_terms[c * p.rows + t] = terms[c];
-    __threadfence();
-    last = atomicAdd(&p.tickets[1], 1u) == gridDim.x - 1;
+    for (int i = 0; i < kStreamChunks; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], kStreamWarps);
+    }
+    for (int i = 0; i < kStreamRows; ++i) {
+      mbar_init(&sh.row_full[i], 1);
+      mbar_init(&sh.row_free[i], kStreamWarps + 1);
+      mbar_init(&sh.sum_full[i], kStreamWarps);
+      mbar_init(&sh.result_full[i], 1);
+      mbar_init(&sh.cta_full[i], 1);
+    }
+    sh.abort_flag = 0;
+    mbar_init_fence();
   }
   __syncthreads();
-  if (!last) return;
-  __threadfence();
-  double out[4];
-  sum_columns<kRowThreads>(p.row_terms, p.rows, p.rows, 3, sums, out);
+  if (ranks > 1) cluster_barrier();
+  grid_dependency_wait();
+  grid_dependents_launch();
+  if (MODE == kPrefForward && blockIdx.x == 0 && threadIdx.x == 0) p.tickets[0] = 0;
+  auto row_of = [&](int64_t t) { return static_cast<const char*>(p.x) + t * p.ld * ES; };
+  auto wait = [&](uint64_t* bar, int n, int ring) {
+    return mbar_wait(&bar[n % ring], (n / ring) & 1, kWaitPolls, abort, status);
+  };
+
+  if (warp == kStreamWarps) {
+    // ---- producer
+    if (lane == 0) {
+      uint64_t evict_first;
+      asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(evict_first));
+      int chunk = 0;
+      auto row_at = [&](int64_t i) { return MODE == kPrefBackward ? p.rows - 1 - i : i; };
+      int64_t ahead = worker < p.rows ? p.labels[row_at(worker)] : -1;
+      // Tells the others of the n-th row. Row n + 1 is told of before row n is
+      // copied: the finisher looks it up before it finishes row n, and a row
+      // may be longer than the ring.
+      auto announce = [&](int n, StreamRow& r) {
+        const int64_t i = worker + n * workers;
+        r = {-1, ahead, 0, 0, 0};
+        if (i < p.rows) {
+          r.t = row_at(i);
+          // a masked row's gradient is written at its own alignment
+          const char* at = ahead < 0 && WRITE && p.d != nullptr ? static_cast<const char*>(p.d) + r.t * p.dld * ES : row_of(r.t);
+          const Part part(at, int(p.vocab), rank, ranks);
+          r.head = part.span.head, r.v0 = part.v0, r.v1 = part.v1;
+        }
+        if (i + workers < p.rows) ahead = p.labels[row_at(i + workers)];
+        if (n >= kStreamRows && !wait(sh.row_free, n - kStreamRows, kStreamRows)) return false;
+        sh.row[n % kStreamRows] = r;
+        mbar_arrive(&sh.row_full[n % kStreamRows]);
+        return true;
+      };
+      StreamRow r, after;
+      bool more = announce(0, r);
+      for (int n = 0; more && r.t >= 0 && !*abort; ++n, r = after) {
+        more = announce(n + 1, after);
+        if (r.label < 0) continue;
+        const char* from = row_of(r.t) + r.head * ES;
+        const bool once = !(MODE == kPrefForward && (p.rows - r.t) * p.vocab * ES < p.keep_bytes);
+        for (int v = r.v0; v < r.v1; v += kVecsChunk, ++chunk) {
+          if (chunk >= kStreamChunks && !wait(sh.empty, chunk - kStreamChunks, kStreamChunks)) break;
+          const uint32_t bytes = uint32_t(min(r.v1 - v, kVecsChunk)) * 16;
+          mbar_arrive_expect_tx(&sh.full[chunk % kStreamChunks], bytes);
+          stream_load(chunks + chunk % kStreamChunks * kStreamChunk, from + int64_t(v) * 16, bytes,
+                      &sh.full[chunk % kStreamChunks], once, evict_first);
+        }
+      }
+      // copies in flight land before the shared memory goes away
+      for (int j = max(0, chunk - kStreamChunks); j < chunk; ++j)
+        for (uint32_t k = 0; k < kWaitPolls && !mbar_try_wait(&sh.full[j % kStreamChunks], (j / kStreamChunks) & 1); ++k) {
+        }
+    }
+  } else if (warp < kStreamWarps) {
+    // ---- sums and gradients
+    const int tid = threadIdx.x;
+    constexpr int kStep = kStreamWarps * 32;
+    int summed = 0, written = 0;  // ring places of the next chunk
+    uint32_t sum_phase = 0, write_phase = 0;
+    auto advance = [](int& at, uint32_t& phase) {
+      if (++at == kStreamChunks) {
+        at = 0;
+        phase ^= 1;
+      }
+    };
+    auto sum_row = [&](int n, const StreamRow& r) {
+      Lse z = {-INFINITY, 0.0f};
+      if (r.label >= 0) {
+#pragma unroll 1
+        for (int v = r.v0; v < r.v1; v += kVecsChunk) {
+          if (!mbar_wait(&sh.full[summed], sum_phase, kWaitPolls, abort, status)) return false;
+          const uint4* in = reinterpret_cast<const uint4*>(chunks + summed * kStreamChunk) + tid;
+          const int left = r.v1 - v - tid;  // vectors from this thread's first one on
+          uint4 raw[kThreadVecs];
+#pragma unroll
+          for (int j = 0; j < kThreadVecs; ++j)
+            if (j * kStep < left) raw[j] = in[j * kStep];
+          if (v == r.v0 && left > 0) {
+            float top = largest<BF16>(raw[0]);
+            if (kStep < left) top = fmaxf(top, largest<BF16>(raw[1]));
+            z.c = fmaxf(kLeastShift, ceilf(top * p.k));
+          }
+#pragma unroll
+          for (int j = 0; j < kThreadVecs; ++j)
+            if (j * kStep < left) z.s += terms_of<BF16>(raw[j], p.k, z.c);
+          if (!WRITE) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.empty[summed]);
+          }
+          advance(summed, sum_phase);
+        }
+        z = lse_warp(z, 32);
+      }
+      if (lane == 0) {
+        sh.warp_sum[n % kStreamRows][warp] = z;
+        mbar_arrive(&sh.sum_full[n % kStreamRows]);
+      }
+      return true;
+    };
+    auto write_row = [&](int n, const StreamRow& r) {
+      if (!wait(sh.result_full, n, kStreamRows)) return false;
+      const StreamResult q = sh.result[n % kStreamRows];
+      char* d = static_cast<char*>(p.d) + r.t * p.dld * ES + r.head * ES;
+      if (r.label < 0) {
+        if (p.d != nullptr)
+          for (int v = r.v0 + tid; v < r.v1; v += kStep) __stcs(reinterpret_cast<uint4*>(d) + v, make_uint4(0, 0, 0, 0));
+        return true;
+      }
+      const bool aligned = reinterpret_cast<uintptr_t>(d) % 16 == 0;
+      const int own = int(r.label) - r.head;  // the label's place among the vectors' elements
+#pragma unroll 1
+      for (int v = r.v0; v < r.v1; v += kVecsChunk) {
+        if (!SUM && !mbar_wait(&sh.full[written], write_phase, kWaitPolls, abort, status)) return false;
+        const uint4* in = reinterpret_cast<const uint4*>(chunks + written * kStreamChunk) + tid;
+        const int left = p.d == nullptr ? 0 : r.v1 - v - tid, mine = own - (v + tid) * W;
+        uint4* to = reinterpret_cast<uint4*>(d) + v + tid;
+#pragma unroll
+        for (int j = 0; j < kThreadVecs; ++j) {
+          if (j * kStep >= left) continue;
+          float f[W];
+          L::widen(in[j * kStep], f);
+#pragma unroll
+          for (int w = 0; w < W; ++w) f[w] = exp2_approx(fmaf(f[w], q.k, -q.shift)) * q.g;
+          if (unsigned(mine - j * kStep * W) < unsigned(W)) {
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+              if (mine - j * kStep * W == w) f[w] += q.up;
+          }
+          if (aligned) {
+            __stcs(to + j * kStep, narrow(f));
+          } else {
+#pragma unroll
+            for (int w = 0; w < W; ++w) store_one<BF16>(reinterpret_cast<char*>(to + j * kStep), w, f[w]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[written]);
+        advance(written, write_phase);
+      }
+      return true;
+    };
+    StreamRow before = {-1, -1, 0, 0, 0};
+    for (int n = 0;; ++n) {
+      if (!wait(sh.row_full, n, kStreamRows)) break;
+      const StreamRow r = sh.row[n % kStreamRows];
+      if (r.t >= 0 && SUM && !sum_row(n, r)) break;
+      const bool late = SUM && WRITE;  // writes trail the sums by a row
+      if (late && n > 0 && !write_row(n - 1, before)) break;
+      if (!late && WRITE && r.t >= 0 && !write_row(n, r)) break;
+      __syncwarp();
+      if (lane == 0 && (late ? n > 0 : r.t >= 0)) mbar_arrive(&sh.row_free[(late ? n - 1 : n) % kStreamRows]);
+      if (r.t < 0) break;
+      before = r;
+    }
+  } else {
+    // ---- finisher
+    float mean = 0.0f;
+    if (MODE == kPolicy) mean = mean_scale(p);
+    int exchanges = 0;
+    auto join_cluster = [&](Lse z, bool& ok) {
+      if (ranks == 1) return z;
+      const int slot = exchanges % kStreamRows;
+      if (lane == 0) mbar_arrive_expect_tx(&sh.cta_full[slot], 8 * ranks);
+      if (lane < ranks) send_peer(&sh.cta_sum[slot][rank], &sh.cta_full[slot], lane, make_float2(z.c, z.s));
+      ok = !__any_sync(~0u, !mbar_wait(&sh.cta_full[slot], (exchanges / kStreamRows) & 1, kWaitPolls, abort, status));
+      ++exchanges;
+      Lse all = {sh.cta_sum[slot][0].x, sh.cta_sum[slot][0].y};
+      for (int r = 1; r < ranks; ++r) all = lse_join(all, {sh.cta_sum[slot][r].x, sh.cta_sum[slot][r].y});
+      return all;
+    };
+    const float nan = __int_as_float(0x7fffffff);
+    // What a row needs from memory is read while the row before it is finished.
+    struct Known {
+      StreamRow r;
+      int edge;
+      float edge_value, x_label, weight, adv, old, ref;
+      float2 lse;
+    };
+    auto look_up = [&](int n, Known& q) {
+      if (__any_sync(~0u, !wait(sh.row_full, n, kStreamRows))) return false;
+      q.r = sh.row[n % kStreamRows];
+      q.edge = -1;
+      q.edge_value = -INFINITY;
+      q.x_label = nan;
+      q.weight = q.adv = q.old = q.ref = 0.0f;
+      q.lse = make_float2(0.0f, 0.0f);
+      const int64_t t = q.r.t;
+      if (t < 0 || q.r.label < 0) return true;
+      const char* x = row_of(t);
+      if (rank == 0) q.edge = RowSpan<W, ES>(x, int(p.vocab)).edge(lane);
+      if (q.edge >= 0) q.edge_value = load_one<BF16>(x, q.edge);
+      if (MODE == kPrefBackward) {
+        q.lse = p.row_lse[t];
+        q.weight = p.row_a[t];
+        return true;
+      }
+      if (q.r.label < p.vocab) q.x_label = load_one<BF16>(x, q.r.label);
+      if (MODE == kPolicy) {
+        q.weight = p.row_a[t];
+        q.adv = p.adv[t];
+        q.old = p.old_logp[t];
+      }
+      if ((MODE == kPolicy || MODE == kPrefForward) && p.ref_logp != nullptr) q.ref = p.ref_logp[t];
+      return true;
+    };
+    Known now, next;
+    bool some = look_up(0, now);
+    for (int n = 0; some && now.r.t >= 0; ++n, now = next) {
+      some = look_up(n + 1, next);
+      const StreamRow r = now.r;
+      const int64_t t = r.t;
+      StreamResult q = {p.k, 0.0f, 0.0f, 0.0f};
+      float terms[3] = {0.0f, 0.0f, 0.0f}, lp = 0.0f;
+      const float edge_value = now.edge_value, weight = now.weight;
+      const char* x = row_of(t);
+      const int edge = now.edge;
+      const bool teller = rank == 0 && lane == 0;
+      bool ok = true;
+      if (r.label >= 0) {
+        if (MODE == kPrefBackward) {
+          const float2 z = now.lse;  // the sign of 1 / sum tells the scale
+          q.up = weight * p.inv_temp;
+          q.k = z.y < 0.0f ? 1.0f : p.k;
+          q.shift = z.x;
+          q.g = -q.up * fabsf(z.y);
+        } else {
+          ok = !__any_sync(~0u, !wait(sh.sum_full, n, kStreamRows));
+          if (!ok) break;
+          Lse z = {-INFINITY, 0.0f};
+          if (lane < kStreamWarps) z = sh.warp_sum[n % kStreamRows][lane];
+          auto with_edge = [&](Lse v, float k) {
+            if (edge < 0) return v;
+            const float c = fmaxf(-INFINITY, ceilf(edge_value * k));
+            return lse_join(v, {c, exp2_approx(fmaf(edge_value, k, -finite_shift(c)))});
+          };
+          z = join_cluster(lse_warp(with_edge(z, q.k), 32), ok);
+          if (!ok) break;
+          // Sums that left fp32's range, once more from memory; where x k itself
+          // is not finite (see rows_kernel), at k = 1.
+          for (int again = 0; again < 2; ++again) {
+            if (again == 0 ? z.s < 3e38f && z.s > kLeastSum : !isinf(z.c)) break;
+            if (again == 1) q.k = 1.0f;
+            z = {-INFINITY, 0.0f};
+            for (int v = r.v0 + lane; v < r.v1; v += 32)
+              lse_add<BF16>(z, reinterpret_cast<const uint4*>(x + r.head * ES)[v], q.k);
+            z = join_cluster(lse_warp(with_edge(z, q.k), 32), ok);
+            if (!ok) break;
+          }
+          if (!ok) break;
+          const Two exact = log_prob(now.x_label, q.k, z);
+          lp = exact.hi + exact.lo;
+          q.shift = finite_shift(z.c);
+          const float inv_sum = 1.0f / z.s;
+          if (MODE == kPrefForward && teller) {
+            // the log ratio before lp is rounded: sequences sum hundreds of them
+            p.row_terms[t] = (exact.hi - now.ref) + exact.lo;
+            p.row_lse[t] = make_float2(q.shift, copysignf(inv_sum, q.k == p.k ? 1.0f : -1.0f));
+          }
+          if (MODE == kPolicy) {
+            const PolicyTerm term = policy_term(p, lp, weight, mean, now.adv, now.old, now.ref);
+            for (int c = 0; c < 3; ++c) terms[c] = term.terms[c];
+            q.up = r.label < p.vocab ? term.up : weight == 0.0f ? 0.0f : nan;
+            q.g = -q.up * inv_sum;
+            if (weight == 0.0f) q.k = q.shift = q.g = q.up = 0.0f;  // outside every sequence: zeros
+          }
+        }
+      } else if (SUM) {
+        ok = !__any_sync(~0u, !wait(sh.sum_full, n, kStreamRows));
+        if (!ok) break;
+      }
+      if (SUM && teller) {
+        p.logp[t] = lp;
+        if (MODE == kPolicy)
+          for (int c = 0; c < 3; ++c) p.row_terms[c * p.rows + t] = terms[c];
+      }
+      if (WRITE) {
+        if (lane == 0) {
+          sh.result[n % kStreamRows] = q;
+          mbar_arrive(&sh.result_full[n % kStreamRows]);
+        }
+        if (p.d != nullptr) {
+          char* d = static_cast<char*>(p.d) + t * p.dld * ES;
+          if (r.label < 0) {
+            const int zero = rank == 0 ? RowSpan<W, ES>(d, int(p.vocab)).edge(lane) : -1;
+            if (zero >= 0) store_one<BF16>(d, zero, 0.0f);
+          } else if (edge >= 0) {
+            const float v = exp2_approx(fmaf(edge_value, q.k, -q.shift)) * q.g;
+            store_one<BF16>(d, edge, r.label == edge ? v + q.up : v);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.row_free[n % kStreamRows]);
+    }
+  }
+  __syncwarp();
+  if (ranks > 1) cluster_barrier();  // no CTA goes while another may still write to it
+}
+
+// The policy loss's statistics from the rows' terms.
+__global__ void __launch_bounds__(1024) stats_kernel(LossParams p) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  double out[3];
+  sum_columns<1024, 3>(p.row_terms, p.rows, p.rows, out);
   if (threadIdx.x == 0) {
     p.stats[0] = float(out[0] + double(p.kl) * out[1]);
     p.stats[1] = float(out[0]);
@@ -378,68 +940,60 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(LossParams p) {
 // ---------------------------------------------------------------- pairs
 
 // One CTA a pair: the log ratios of its two sequences, the loss of the pair
-// and the coefficient of each of its rows.
+// and the coefficient of each of its rows; the last one sums the statistics.
 __global__ void __launch_bounds__(256) pair_kernel(LossParams p) {
   grid_dependency_wait();
   grid_dependents_launch();
   const int64_t pairs = p.n_seq / 2, i = blockIdx.x;
-  __shared__ double sums[256];
-  __shared__ int counts[8];
+  __shared__ double sums[2][8];
+  __shared__ int counts[2][8];
   __shared__ bool last;
-  auto bound = [&](int64_t s) {
-    const int64_t v = p.seq_start[s];
-    return v < 0 ? int64_t(0) : v > p.rows ? p.rows : v;
-  };
-  double ratio[2];
-  float over[2];
+  int64_t bounds[3];
+  for (int h = 0; h < 3; ++h) bounds[h] = seq_bound(p, 2 * i + h);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   for (int h = 0; h < 2; ++h) {
-    const int64_t lo = bound(2 * i + h), hi = bound(2 * i + h + 1);
     double a = 0.0;
     int n = 0;
-    for (int64_t t = lo + threadIdx.x; t < hi; t += 256)
+#pragma unroll 4
+    for (int64_t t = bounds[h] + threadIdx.x; t < bounds[h + 1]; t += 256)
       if (p.labels[t] >= 0) {
         a += double(p.row_terms[t]);
         ++n;
       }
-    __syncthreads();
-    sums[threadIdx.x] = a;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(~0u, a, o);
     n = __reduce_add_sync(~0u, n);
-    if (threadIdx.x % 32 == 0) counts[threadIdx.x / 32] = n;
-    __syncthreads();
-    for (int o = 128; o > 0; o >>= 1) {
-      if (threadIdx.x < o) sums[threadIdx.x] += sums[threadIdx.x + o];
-      __syncthreads();
-    }
-    n = 0;
-    for (int w = 0; w < 8; ++w) n += counts[w];
-    over[h] = p.normalize ? float(max(n, 1)) : 1.0f;
-    ratio[h] = sums[0] / double(over[h]);
+    if (lane == 0) sums[h][warp] = a, counts[h][warp] = n;
   }
-  const double z = double(p.beta) * (ratio[0] - ratio[1]);
-  double loss, slope;
-  if (p.square) {
-    const double off = z - double(p.target);
-    loss = off * off;
-    slope = 2.0 * off;
-  } else {
-    // log1p(e^-|z|) serves both signs of z
-    const double tail = log1p(exp(-fabs(z))), up = z > 0.0 ? z : 0.0, down = z < 0.0 ? -z : 0.0;
-    const double eps = double(p.smooth);
-    loss = (1.0 - eps) * (tail + down) + eps * (tail + up);
-    slope = -(1.0 - eps) / (1.0 + exp(z)) + eps / (1.0 + exp(-z));
-    if (z != z) loss = slope = z;
-  }
-  const double count = p.denominator > 0.0f ? double(p.denominator) : double(pairs);
+  __syncthreads();
+  double ratio[2];
+  float over[2];
   for (int h = 0; h < 2; ++h) {
-    const int64_t lo = bound(2 * i + h), hi = bound(2 * i + h + 1);
-    const float c = float((h ? -1.0 : 1.0) * slope * double(p.beta) / count / double(over[h]) * double(p.grad_scale));
-    for (int64_t t = lo + threadIdx.x; t < hi; t += 256) p.row_a[t] = c;
-    if (h == 0 && i == 0)
-      for (int64_t t = threadIdx.x; t < lo; t += 256) p.row_a[t] = 0.0f;
-    if (h == 1 && i == pairs - 1)
-      for (int64_t t = hi + threadIdx.x; t < p.rows; t += 256) p.row_a[t] = 0.0f;
+    double a = 0.0;
+    int n = 0;
+    for (int w = 0; w < 8; ++w) a += sums[h][w], n += counts[h][w];
+    over[h] = p.normalize ? float(max(n, 1)) : 1.0f;
+    ratio[h] = a / double(over[h]);
   }
+  __shared__ float coef[2];
+  const double count = p.denominator > 0.0f ? double(p.denominator) : double(pairs);
   if (threadIdx.x == 0) {
+    const double z = double(p.beta) * (ratio[0] - ratio[1]);
+    double loss, slope;
+    if (p.square) {
+      const double off = z - double(p.target);
+      loss = off * off;
+      slope = 2.0 * off;
+    } else {
+      // log1p(e^-|z|) serves both signs of z
+      const double tail = log1p(exp(-fabs(z))), up = z > 0.0 ? z : 0.0, down = z < 0.0 ? -z : 0.0;
+      const double eps = double(p.smooth);
+      loss = (1.0 - eps) * (tail + down) + eps * (tail + up);
+      slope = -(1.0 - eps) / (1.0 + exp(z)) + eps / (1.0 + exp(-z));
+      if (z != z) loss = slope = z;
+    }
+    for (int h = 0; h < 2; ++h)
+      coef[h] = float((h ? -1.0 : 1.0) * slope * double(p.beta) / count / double(over[h]) * double(p.grad_scale));
     p.ratios[2 * i] = float(ratio[0]);
     p.ratios[2 * i + 1] = float(ratio[1]);
     float* terms = p.row_terms + p.rows;
@@ -451,36 +1005,111 @@ __global__ void __launch_bounds__(256) pair_kernel(LossParams p) {
     last = atomicAdd(&p.tickets[0], 1u) == gridDim.x - 1;
   }
   __syncthreads();
+  for (int h = 0; h < 2; ++h)
+    for (int64_t t = bounds[h] + threadIdx.x; t < bounds[h + 1]; t += 256) p.row_a[t] = coef[h];
+  if (i == 0)
+    for (int64_t t = threadIdx.x; t < bounds[0]; t += 256) p.row_a[t] = 0.0f;
+  if (i == pairs - 1)
+    for (int64_t t = bounds[2] + threadIdx.x; t < p.rows; t += 256) p.row_a[t] = 0.0f;
   if (!last) return;
   __threadfence();
   double out[4];
-  sum_columns<256>(p.row_terms + p.rows, pairs, pairs, 4, sums, out);
+  sum_columns<256, 4>(p.row_terms + p.rows, pairs, pairs, out);
   if (threadIdx.x == 0)
     for (int c = 0; c < 4; ++c) p.stats[c] = float(out[c]);
 }
 
+// ---------------------------------------------------------------- launches
+
 // Launched so that it may be scheduled while the kernel before it drains; every
 // kernel here waits for that one before it touches memory.
-cudaError_t launch_after(void (*kernel)(LossParams), const LossParams& p, int64_t grid, int threads,
-                         cudaStream_t stream) {
+cudaError_t launch_after(void (*kernel)(LossParams), const LossParams& p, int64_t grid, int threads, int cluster,
+                         cudaStream_t stream, size_t smem = 0) {
   if (grid <= 0) return cudaSuccess;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
   cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// How many clusters of the streaming kernel run at once on the current device.
+cudaError_t active_clusters(const void* kernel, int cluster, size_t smem, int* workers) {
+  static std::mutex mu;
+  static std::vector<std::array<int, 3>> known;  // device, cluster, workers (the same for every kernel of its shape)
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  std::lock_guard<std::mutex> lock(mu);
+  for (const auto& k : known)
+    if (k[0] == dev && k[1] == cluster) {
+      *workers = k[2];
+      return cudaSuccess;
+    }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(device_sms() / cluster * cluster));
+  cfg.blockDim = dim3(kStreamThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(cluster);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  err = cudaOccupancyMaxActiveClusters(workers, kernel, &cfg);
+  if (err != cudaSuccess) return err;
+  if (*workers < 1) return cudaErrorInvalidConfiguration;
+  known.push_back({dev, cluster, *workers});
+  return cudaSuccess;
+}
+
+// Calls with many long rows stream them; the others take a cluster a row.
+constexpr int64_t kStreamRowBytes = 16384, kStreamRowsAnSm = 4;
+
+template <bool BF16, int MODE>
+cudaError_t launch_rows_typed(LossParams p, cudaStream_t stream) {
+  const int64_t bytes = p.vocab * (BF16 ? 2 : 4), vecs = (bytes + 15) / 16, sms = device_sms();
+  p.keep_bytes = int64_t(80) << 20;
+  p.cluster = 1;
+  while (MODE == kPolicy && p.cluster < kMaxCluster && bytes > int64_t(kStreamSlice) * p.cluster) p.cluster *= 2;
+  if (bytes >= kStreamRowBytes && (MODE != kPolicy || bytes <= int64_t(kStreamSlice) * p.cluster) && p.rows * p.cluster >= kStreamRowsAnSm * sms) {
+    void (*kernel)(LossParams) = stream_kernel<BF16, MODE>;
+    constexpr size_t kSmem = size_t(kStreamChunks) * kStreamChunk + 128;
+    cudaError_t err = status_ref(&p.status_word, &p.status_host);
+    if (err == cudaSuccess)
+      err = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+    int workers = int(sms);
+    if (err == cudaSuccess && p.cluster > 1) err = active_clusters(reinterpret_cast<const void*>(kernel), p.cluster, kSmem, &workers);
+    if (err != cudaSuccess) return err;
+    return launch_after(kernel, p, std::min<int64_t>(workers, p.rows) * p.cluster, kStreamThreads, p.cluster, stream, kSmem);
+  }
+  // The smallest CTA, then the smallest cluster, that holds a row; a few rows
+  // are spread over more CTAs, so that every SM has some.
+  const int threads = vecs <= 128 * kVecs ? 128 : vecs <= 256 * kVecs ? 256 : 512;
+  p.cluster = 1;
+  while (p.cluster < kMaxCluster && vecs > int64_t(threads) * kVecs * p.cluster) p.cluster *= 2;
+  while (p.cluster < kMaxCluster && p.rows * p.cluster * 2 <= 2 * sms && vecs >= int64_t(threads) * 2 * p.cluster)
+    p.cluster *= 2;
+  while (p.cluster > 1 && p.rows * p.cluster > 0x7fffffff) p.cluster /= 2;
+  void (*kernel)(LossParams) = threads == 128   ? rows_kernel<BF16, MODE, 128>
+                               : threads == 256 ? rows_kernel<BF16, MODE, 256>
+                                                : rows_kernel<BF16, MODE, 512>;
+  return launch_after(kernel, p, p.rows * p.cluster, threads, p.cluster, stream);
 }
 
 template <int MODE>
 cudaError_t launch_rows(const LossParams& p, ar_dtype dtype, cudaStream_t stream) {
-  return launch_after(dtype == AR_BF16 ? rows_kernel<true, MODE> : rows_kernel<false, MODE>, p, p.rows, kRowThreads,
-                      stream);
+  return dtype == AR_BF16 ? launch_rows_typed<true, MODE>(p, stream) : launch_rows_typed<false, MODE>(p, stream);
 }
 
 }  // namespace
@@ -490,17 +1119,16 @@ cudaError_t launch_token_logp(const LossParams& p, ar_dtype dtype, cudaStream_t 
 }
 
 cudaError_t launch_policy_loss(const LossParams& p, ar_dtype dtype, cudaStream_t stream) {
-  cudaError_t err = cudaMemsetAsync(p.tickets, 0, 8, stream);
-  if (err == cudaSuccess && p.rows == 0) return cudaMemsetAsync(p.stats, 0, 16, stream);
-  if (err == cudaSuccess) err = launch_after(count_kernel, p, p.n_seq, 256, stream);
+  if (p.rows == 0) return cudaMemsetAsync(p.stats, 0, 16, stream);
+  cudaError_t err = launch_after(count_kernel, p, p.n_seq, 256, 1, stream);
   if (err == cudaSuccess) err = launch_rows<kPolicy>(p, dtype, stream);
+  if (err == cudaSuccess) err = launch_after(stats_kernel, p, 1, 1024, 1, stream);
   return err;
 }
 
 cudaError_t launch_preference_loss(const LossParams& p, ar_dtype dtype, cudaStream_t stream) {
-  cudaError_t err = cudaMemsetAsync(p.tickets, 0, 8, stream);
-  if (err == cudaSuccess) err = launch_rows<kPrefForward>(p, dtype, stream);
-  if (err == cudaSuccess) err = launch_after(pair_kernel, p, p.n_seq / 2, 256, stream);
+  cudaError_t err = p.rows == 0 ? cudaMemsetAsync(p.tickets, 0, 4, stream) : launch_rows<kPrefForward>(p, dtype, stream);
+  if (err == cudaSuccess) err = launch_after(pair_kernel, p, p.n_seq / 2, 256, 1, stream);
   if (err == cudaSuccess && p.d != nullptr) err = launch_rows<kPrefBackward>(p, dtype, stream);
   return err;
 }

@@ -17,7 +17,6 @@ struct LossParams {
   int64_t rows, vocab, ld;
   const int64_t* labels;  // < 0: the row is not part of the loss
   float k;                // log2(e) / temperature
-  double to_ln;           // natural log-probability of a base-2 one (ln 2)
   float inv_temp;
   float* logp;            // [rows]
   void* d;                // gradient of the logits, row t at d + t * dld; null: none
@@ -39,10 +38,13 @@ struct LossParams {
   float* ratios;          // [n_seq]
   float* stats;           // [4]
   // workspace
-  unsigned int* tickets;  // [0]: counting pass, [1]: main pass; zeroed before the call's kernels
-  float* total;           // [0]: 1 / denominator
+  unsigned int* tickets;  // [0]: pairs done
   int32_t* seq_count;     // [n_seq] labelled tokens
   float* row_a;           // [rows] policy: weight before the total; preference: coefficient
+  int cluster;            // CTAs a row
+  unsigned int* status_word;         // where waits that ran out are recorded
+  unsigned int* const* status_host;
+  int64_t keep_bytes;     // logits that are worth keeping in the L2 between two passes
   float2* row_lse;        // [rows] preference: (base-2 shift, 1 / sum)
   float* row_terms;       // policy: [3 * rows] weighted loss terms;
                           // preference: [rows] log ratios, then [4 * pairs] terms
@@ -55,7 +57,7 @@ struct LossLayout {
 inline LossLayout loss_layout(int64_t rows, int64_t n_seq) {
   auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
   LossLayout l;
-  l.seq_count = 256;  // tickets and total come first
+  l.seq_count = 256;  // tickets come first
   l.row_a = l.seq_count + up(4 * n_seq);
   l.row_lse = l.row_a + up(4 * rows);
   l.row_terms = l.row_lse + up(8 * rows);

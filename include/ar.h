@@ -569,7 +569,7 @@ typedef struct {
 /* Log-probabilities of the labelled tokens: logp[t] = lp_t. The old and
  * reference log-probabilities of the two losses below are made by this call.
  * AR_EINVAL: a NULL or misaligned pointer, a bad size, type or temperature;
- * AR_EUNSUPPORTED: rows >= 2^31. */
+ * AR_EUNSUPPORTED: rows >= 2^31 or vocab > 2^30. */
 ar_status ar_token_logp(const ar_logits* logits, float* logp, void* stream);
 
 /* Device bytes (16-byte aligned) that ar_policy_loss and ar_preference_loss
@@ -733,8 +733,8 @@ ar_status ar_muon_step(const ar_ortho_plan_t* plan, const ar_muon_desc* desc, co
  * work has returned, since initiation is non-blocking (Scaling ML Systems,
  * "Collective communication"). From then on the executing calls
  * (ar_execute, ar_execute_host, ar_execute_noalloc, ar_bind,
- * ar_execute_bound, ar_bucket_allreduce, ar_orthogonalize, ar_muon_step) on
- * that device return AR_ETIMEOUT
+ * ar_execute_bound, ar_bucket_allreduce, ar_token_logp, ar_policy_loss,
+ * ar_preference_loss, ar_orthogonalize, ar_muon_step) on that device return AR_ETIMEOUT
  * and enqueue nothing, until ar_device_status(1) clears the word. */
 
 /* Read (and clear, if clear != 0) the calling device's sticky status word.

@@ -261,6 +261,107 @@ def test_preference_in_place_and_forward_only(g):
     assert torch.equal(d, apart[3])
 
 
+# Calls with many long rows, which are streamed: (rows, vocab, dtype); the policy loss in clusters of 1, 1, 4 and
+# 2 CTAs a row.
+STREAMED = [(650, 8200, torch.bfloat16), (700, 5001, torch.float32), (160, 50021, torch.float32),
+            (330, 40003, torch.bfloat16)]
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", STREAMED)
+@pytest.mark.parametrize("shift", [0, 3])
+def test_streamed_rows(g, rows, vocab, dtype, shift):
+    inputs = make(rows, vocab, dtype, seed=rows, shift=shift, pad=2, n_seq=6, ruled=0.02)
+    x, host, dev, cpu = inputs
+    check_logp(g.ar_token_logp(x, dev["labels"], temperature=0.9), losses.token_logp(host, cpu["labels"], 0.9))
+    stats, logp, d = policy(g, *inputs, mean="sequence", temperature=0.9)
+    preference(g, *inputs, temperature=1.1, length_normalized=True)
+    # gradients over the logits, and at another alignment
+    room = torch.full((rows, vocab + 5), 7.0, dtype=dtype, device="cuda")
+    assert torch.equal(d, policy(g, *inputs, mean="sequence", temperature=0.9, dlogits=room[:, 4:vocab + 4])[2])
+    assert (room[:, :4] == 7).all() and (room[:, vocab + 4:] == 7).all()
+    # (at the logits' own alignment: sums run in an order that depends on it)
+    own = torch.empty(rows, shift + vocab + 2, dtype=dtype, device="cuda")[:, shift:shift + vocab]
+    own.copy_(x)
+    pref = preference(g, *inputs, beta=0.3)[3]
+    got = g.ar_preference_loss(own, dev["labels"], dev["ref"], dev["start"], beta=0.3, dlogits=own)[3]
+    assert torch.equal(got, pref)
+    own.copy_(x)
+    again = g.ar_policy_loss(own, dev["labels"], dev["old"], dev["adv"], dev["start"], ref_logp=dev["ref"],
+                             clip_low=CLIP[0], clip_high=CLIP[1], kl_coef=0.1, reduction="sequence", temperature=0.9,
+                             dlogits=own)
+    assert torch.equal(again[2], d) and torch.equal(again[0], stats) and torch.equal(again[1], logp)
+    assert g.ar_device_status() == g.AR_OK
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", STREAMED)
+def test_streamed_rows_of_extreme_values(g, rows, vocab, dtype):
+    low = torch.finfo(dtype).min
+    x, host, dev, cpu = make(rows, vocab, dtype, seed=1, n_seq=2, masked=0.0)
+    dev["labels"][:6] = 5
+    x[0] = low               # uniform
+    x[1, 9:] = low           # uniform over nine
+    x[1, :9] = 0.0
+    x[2] = -float("inf")
+    x[3, vocab - 1] = float("nan")
+    x[4, 0] = float("inf")
+    dev["labels"][5] = vocab + 3
+    lp = g.ar_token_logp(x, dev["labels"]).cpu().numpy()
+    assert abs(lp[0] + np.log(vocab)) < 1e-5 and abs(lp[1] + np.log(9)) < 1e-6 and np.isnan(lp[2:6]).all()
+    check_logp(torch.tensor(lp[6:]), losses.token_logp(host[6:], cpu["labels"][6:]))
+    d = g.ar_policy_loss(x, dev["labels"], dev["old"], dev["adv"], dev["start"])[2].float()
+    assert torch.isnan(d[2:6]).all() and torch.isfinite(d[6:]).all()
+    # rows that a mask takes out are not read
+    dev["labels"][:6] = -1
+    stats, _, d = g.ar_policy_loss(x, dev["labels"], dev["old"], dev["adv"], dev["start"])
+    assert not d[:6].any() and torch.isfinite(stats).all()
+
+
+def test_streamed_rows_longer_than_the_ring(g):
+    """Rows of 200 and 400 KB; the definition in 64 bits on the device. Bounds as at the top."""
+    for vocab, dtype in ((100003, torch.bfloat16), (100003, torch.float32)):
+        rows = 620
+        gen = torch.Generator(device="cuda").manual_seed(vocab)
+        x = (torch.randn(rows, vocab, generator=gen, device="cuda") * 3).to(dtype)
+        labels = torch.randint(0, vocab, (rows,), generator=gen, device="cuda")
+        labels[::7] = -1
+        start = torch.tensor([0, 100, 333, 400, rows], device="cuda")
+        ref = torch.full((rows,), -9.0, device="cuda")
+        logp = torch.log_softmax(x.double(), 1).gather(1, labels.clamp(min=0)[:, None])[:, 0]
+        logp = torch.where(labels >= 0, logp, 0.0)
+        check_logp(g.ar_token_logp(x, labels), logp.cpu().numpy())
+        stats, ratios, got, d = g.ar_preference_loss(x, labels, ref, start, beta=0.01)
+        check_logp(got, logp.cpu().numpy())
+        gap = torch.where(labels >= 0, logp + 9.0, 0.0)
+        want = torch.stack([gap[a:b].sum() for a, b in zip([0, 100, 333, 400], [100, 333, 400, rows])])
+        z = 0.01 * (want[0::2] - want[1::2])
+        slope = torch.stack([-torch.sigmoid(-z), torch.sigmoid(-z)], 1).reshape(-1) * 0.01 / 2
+        up = torch.repeat_interleave(slope, torch.tensor([100, 233, 67, rows - 400], device="cuda"))
+        up = torch.where(labels >= 0, up, 0.0)
+        exact = torch.softmax(x.double(), 1) * -up[:, None]
+        exact[torch.arange(rows), labels.clamp(min=0)] += up
+        # the slope moves by at most beta * 620 * 1e-4 of itself
+        bound = 1e-3 * exact.abs() + (2.0 ** -8 if dtype == torch.bfloat16 else 0) * exact.abs() + 1e-3 * up.abs()[:, None] * GRAD
+        assert ((d.double() - exact).abs() <= bound + 1e-12).all()
+        old, adv = logp.float() - 0.05, torch.ones(rows, device="cuda")
+        _, got, d = g.ar_policy_loss(x, labels, old, adv)
+        check_logp(got, logp.cpu().numpy())
+        up = torch.where(labels >= 0, -torch.exp(logp - old.double()) / (labels >= 0).sum(), 0.0)
+        exact = torch.softmax(x.double(), 1) * -up[:, None]
+        exact[torch.arange(rows), labels.clamp(min=0)] += up
+        bound = 1e-3 * exact.abs() + (2.0 ** -8 if dtype == torch.bfloat16 else 0) * exact.abs() + up.abs()[:, None] * GRAD
+        assert ((d.double() - exact).abs() <= bound + 1e-12).all()
+        assert g.ar_device_status() == g.AR_OK
+
+
+def test_streamed_rows_outside_the_sequences(g):
+    rows, vocab = 700, 8200
+    x, host, dev, cpu = make(rows, vocab, torch.bfloat16, seed=3, masked=0.1)
+    start = np.array([5, 300, 300, 690], np.int64)
+    cpu["start"], dev["start"] = start, torch.tensor(start, device="cuda")
+    _, logp, d = policy(g, x, host, dev, cpu, mean="sequence")
+    assert not d[:5].any() and not d[690:].any()
+
+
 def test_gradients_against_differences(g):
     """The device's own loss along a direction: central differences at step h of fp32 losses.
 

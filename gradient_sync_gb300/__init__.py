@@ -10,6 +10,7 @@ fallback, and importing a function whose library is missing raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import _lib
 
@@ -329,24 +330,35 @@ def ar_compressed_allreduce(grads, block: int, dtype="f32", residuals=None, scal
 # ---------------------------------------------------------------- losses
 
 
+_KINDS: dict = {}  # torch type -> the library's, once torch is needed
+
+
+def _torch_kinds() -> dict:
+    if not _KINDS:
+        import torch
+
+        _KINDS.update({torch.float32: AR_F32, torch.bfloat16: AR_BF16})
+    return _KINDS
+
+
 def _dtype_of(t) -> int:
     """The library's type of a torch tensor; TypeError for any other type."""
-    name = str(t.dtype).replace("torch.", "")
-    if name not in ("float32", "bfloat16"):
+    kind = _torch_kinds().get(t.dtype)
+    if kind is None:
         raise TypeError(f"float32 or bfloat16 wanted, got {t.dtype}")
-    return AR_F32 if name == "float32" else AR_BF16
+    return kind
 
 
-def _dense(t, dtype: str, shape, what: str):
-    """Check a contiguous device tensor of one type and shape."""
-    if str(t.dtype) != "torch." + dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{what}: a contiguous {dtype} CUDA tensor of shape {tuple(shape)} wanted, got {t.dtype} "
+def _vector(t, dtype, n: int, what: str) -> int:
+    """The address of a contiguous device vector of one type and length."""
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous {dtype} CUDA tensor of {n} elements wanted, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
-    return t
+    return t.data_ptr()
 
 
-def _row_major(t, what: str):
-    """Check a 2-D device tensor whose rows are contiguous (any row stride)."""
+def _row_major(t, what: str) -> int:
+    """The row stride of a 2-D device tensor whose rows are contiguous."""
     if t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{what}: a 2-D CUDA tensor with contiguous rows wanted, got shape {tuple(t.shape)}, "
                          f"strides {t.stride()} on {t.device}")
@@ -354,33 +366,38 @@ def _row_major(t, what: str):
 
 
 def _logits(logits, labels, temperature):
+    import torch
+
     ld = _row_major(logits, "logits")
-    _dense(labels, "int64", logits.shape[:1], "labels")
-    return _lib.ArLogits(_ptr(logits), logits.shape[0], logits.shape[1], ld, _dtype_of(logits), _ptr(labels),
-                         float(temperature))
+    rows, vocab = logits.shape
+    return _lib.ArLogits(logits.data_ptr(), rows, vocab, ld, _dtype_of(logits),
+                         _vector(labels, torch.int64, rows, "labels"), temperature)
 
 
 def _gradient(logits, dlogits, grad: bool):
-    """(tensor or None, row stride) of the gradient of the logits."""
-    import torch
-
+    """(tensor or None, address, row stride) of the gradient of the logits."""
     if dlogits is None:
         if not grad:
-            return None, 0
+            return None, 0, 0
+        import torch
+
         dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
+    elif dlogits.dtype is not logits.dtype or dlogits.shape != logits.shape:
         raise ValueError("dlogits: the logits' type and shape wanted")
-    return dlogits, _row_major(dlogits, "dlogits")
+    return dlogits, dlogits.data_ptr(), _row_major(dlogits, "dlogits")
 
 
-def _output(t, shape, like, what: str):
+def _output(t, n: int, like, what: str):
+    """An fp32 vector to write to, and its address."""
     import torch
 
     if t is None:
-        return torch.empty(shape, dtype=torch.float32, device=like.device)
-    return _dense(t, "float32", shape, what)
+        t = torch.empty(n, dtype=torch.float32, device=like.device)
+        return t, t.data_ptr()
+    return t, _vector(t, torch.float32, n, what)
 
 
+@functools.lru_cache(maxsize=1024)
 def ar_loss_workspace(rows: int, n_seq: int) -> int:
     """Device bytes that the two losses need for `rows` tokens in `n_seq` sequences."""
     b = _lib.c_size_t()
@@ -388,23 +405,23 @@ def ar_loss_workspace(rows: int, n_seq: int) -> int:
     return b.value
 
 
-def _loss_workspace(workspace, rows, n_seq, like):
-    need = ar_loss_workspace(rows, n_seq)
+def _room(workspace, need: int, like):
+    """A workspace of at least `need` bytes, and its address."""
     if workspace is None:
         import torch
 
-        return torch.empty(need, dtype=torch.uint8, device=like.device)
-    if workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    elif workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace: {need} bytes wanted")
-    return workspace
+    return workspace, workspace.data_ptr()
 
 
 def ar_token_logp(logits, labels, temperature: float = 1.0, logp=None, stream=None):
     """Log-probabilities of the labelled tokens, [rows] fp32 (0 where the label
     is negative). `logits` [rows, vocab] fp32 or bf16, any row stride; `labels` int64."""
     d = _logits(logits, labels, temperature)
-    logp = _output(logp, logits.shape[:1], logits, "logp")
-    _check(_lib.load().ar_token_logp(d, _ptr(logp), _stream(stream)), "ar_token_logp")
+    logp, out = _output(logp, d.rows, logits, "logp")
+    _check(_lib.load().ar_token_logp(d, out, _stream(stream)), "ar_token_logp")
     return logp
 
 
@@ -418,23 +435,22 @@ def ar_policy_loss(logits, labels, old_logp, advantages, seq_start=None, ref_log
     `seq_start` int64 [n_seq + 1] row offsets (None: one sequence). `dlogits`
     may be the logits themselves. Returns (stats [loss, surrogate, kl, clipped
     share], logp, dlogits or None)."""
+    import torch
+
     d = _logits(logits, labels, temperature)
-    rows = logits.shape[0]
-    for t, what in ((old_logp, "old_logp"), (advantages, "advantages"), (ref_logp, "ref_logp")):
-        if t is not None or what != "ref_logp":
-            _dense(t, "float32", (rows,), what)
-    n_seq = 1
+    rows, f32 = d.rows, torch.float32
+    old, adv = _vector(old_logp, f32, rows, "old_logp"), _vector(advantages, f32, rows, "advantages")
+    ref = 0 if ref_logp is None else _vector(ref_logp, f32, rows, "ref_logp")
+    n_seq, start = 1, 0
     if seq_start is not None:
-        n_seq = seq_start.numel() - 1
-        _dense(seq_start, "int64", (n_seq + 1,), "seq_start")
-    dlogits, dld = _gradient(logits, dlogits, grad)
-    stats = _output(stats, (4,), logits, "stats")
-    logp = _output(logp, (rows,), logits, "logp")
-    workspace = _loss_workspace(workspace, rows, max(n_seq, 0), logits)
-    desc = _lib.ArPolicyDesc(float(clip_low), float(clip_high), float(kl_coef), LOSS_MEANS.get(reduction, reduction),
-                             float(denominator), float(grad_scale))
-    _check(_lib.load().ar_policy_loss(d, _ptr(old_logp), _ptr(ref_logp), _ptr(advantages), _ptr(seq_start), n_seq,
-                                      desc, _ptr(stats), _ptr(logp), _ptr(dlogits), dld, _ptr(workspace),
+        n_seq = seq_start.shape[0] - 1 if seq_start.dim() else 0
+        start = _vector(seq_start, torch.int64, n_seq + 1, "seq_start")
+    dlogits, d_at, dld = _gradient(logits, dlogits, grad)
+    stats, stats_at = _output(stats, 4, logits, "stats")
+    logp, logp_at = _output(logp, rows, logits, "logp")
+    workspace, room = _room(workspace, ar_loss_workspace(rows, max(n_seq, 0)), logits)
+    desc = _lib.ArPolicyDesc(clip_low, clip_high, kl_coef, LOSS_MEANS.get(reduction, reduction), denominator, grad_scale)
+    _check(_lib.load().ar_policy_loss(d, old, ref, adv, start, n_seq, desc, stats_at, logp_at, d_at, dld, room,
                                       _stream(stream)), "ar_policy_loss")
     return stats, logp, dlogits
 
@@ -450,20 +466,21 @@ def ar_preference_loss(logits, labels, ref_logp, seq_start, beta: float = 0.1, l
     and the rejected answer of pair i; `ref_logp` fp32 [rows]. Returns (stats
     [loss, chosen reward, rejected reward, accuracy], ratios, logp, dlogits or
     None)."""
+    import torch
+
     d = _logits(logits, labels, temperature)
-    rows, n_seq = logits.shape[0], seq_start.numel() - 1
-    _dense(ref_logp, "float32", (rows,), "ref_logp")
-    _dense(seq_start, "int64", (n_seq + 1,), "seq_start")
-    dlogits, dld = _gradient(logits, dlogits, grad)
-    stats = _output(stats, (4,), logits, "stats")
-    ratios = _output(ratios, (max(n_seq, 0),), logits, "ratios")
-    logp = _output(logp, (rows,), logits, "logp")
-    workspace = _loss_workspace(workspace, rows, max(n_seq, 0), logits)
-    desc = _lib.ArPreferenceDesc(float(beta), PREFERENCE_FORMS.get(loss, loss), float(label_smoothing), float(target),
-                                 int(bool(length_normalized)), float(denominator), float(grad_scale))
-    _check(_lib.load().ar_preference_loss(d, _ptr(ref_logp), _ptr(seq_start), n_seq, desc, _ptr(stats), _ptr(ratios),
-                                          _ptr(logp), _ptr(dlogits), dld, _ptr(workspace), _stream(stream)),
-           "ar_preference_loss")
+    rows, n_seq = d.rows, seq_start.shape[0] - 1 if seq_start.dim() else 0
+    ref = _vector(ref_logp, torch.float32, rows, "ref_logp")
+    start = _vector(seq_start, torch.int64, n_seq + 1, "seq_start")
+    dlogits, d_at, dld = _gradient(logits, dlogits, grad)
+    stats, stats_at = _output(stats, 4, logits, "stats")
+    ratios, ratios_at = _output(ratios, max(n_seq, 0), logits, "ratios")
+    logp, logp_at = _output(logp, rows, logits, "logp")
+    workspace, room = _room(workspace, ar_loss_workspace(rows, max(n_seq, 0)), logits)
+    desc = _lib.ArPreferenceDesc(beta, PREFERENCE_FORMS.get(loss, loss), label_smoothing, target,
+                                 1 if length_normalized else 0, denominator, grad_scale)
+    _check(_lib.load().ar_preference_loss(d, ref, start, n_seq, desc, stats_at, ratios_at, logp_at, d_at, dld, room,
+                                          _stream(stream)), "ar_preference_loss")
     return stats, ratios, logp, dlogits
 
 
@@ -475,6 +492,7 @@ class OrthoPlan:
 
     def __init__(self, handle: int, shapes, in_dtype: int, out_dtype: int):
         self.handle, self.shapes, self.in_dtype, self.out_dtype = handle, shapes, in_dtype, out_dtype
+        self.workspace_bytes = None
 
     def __del__(self):
         h, self.handle = getattr(self, "handle", None), None
@@ -511,9 +529,11 @@ def ar_ortho_plan(shapes, in_dtype="f32", out_dtype="f32", steps: int = 5, coeff
 
 def ar_ortho_workspace(plan: OrthoPlan) -> int:
     """Device bytes that a call with the plan needs."""
-    b = _lib.c_size_t()
-    _check(_lib.load().ar_ortho_workspace(plan.handle, b), "ar_ortho_workspace")
-    return b.value
+    if plan.workspace_bytes is None:
+        b = _lib.c_size_t()
+        _check(_lib.load().ar_ortho_workspace(plan.handle, b), "ar_ortho_workspace")
+        plan.workspace_bytes = b.value
+    return plan.workspace_bytes
 
 
 def _matrices(plan: OrthoPlan, tensors, dtype: int, what: str):
@@ -530,17 +550,6 @@ def _matrices(plan: OrthoPlan, tensors, dtype: int, what: str):
     return arr
 
 
-def _ortho_room(plan: OrthoPlan, workspace, like):
-    need = ar_ortho_workspace(plan)
-    if workspace is None:
-        import torch
-
-        return torch.empty(need, dtype=torch.uint8, device=like.device)
-    if workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace: {need} bytes wanted")
-    return workspace
-
-
 def ar_orthogonalize(plan: OrthoPlan, matrices, outs=None, workspace=None, stream=None):
     """Newton-Schulz orthogonalisation of every matrix of the plan; returns `outs`
     (new tensors by default; may be `matrices` themselves where the types agree)."""
@@ -550,8 +559,8 @@ def ar_orthogonalize(plan: OrthoPlan, matrices, outs=None, workspace=None, strea
         kind = torch.bfloat16 if plan.out_dtype == AR_BF16 else torch.float32
         outs = [torch.empty(m.shape, dtype=kind, device=m.device) for m in matrices]
     a, b = _matrices(plan, matrices, plan.in_dtype, "matrices"), _matrices(plan, outs, plan.out_dtype, "outs")
-    workspace = _ortho_room(plan, workspace, matrices[0])
-    _check(_lib.load().ar_orthogonalize(plan.handle, a, b, _ptr(workspace), _stream(stream)), "ar_orthogonalize")
+    workspace, room = _room(workspace, ar_ortho_workspace(plan), matrices[0])
+    _check(_lib.load().ar_orthogonalize(plan.handle, a, b, room, _stream(stream)), "ar_orthogonalize")
     return outs
 
 
@@ -564,10 +573,10 @@ def ar_muon_step(plan: OrthoPlan, params, grads, momenta, lr: float, momentum: f
     p, g = _matrices(plan, params, plan.out_dtype, "params"), _matrices(plan, grads, plan.in_dtype, "grads")
     m = _matrices(plan, momenta, AR_F32, "momenta")
     po, mo = _matrices(plan, params_out, plan.out_dtype, "params_out"), _matrices(plan, momenta_out, AR_F32, "momenta_out")
-    workspace = _ortho_room(plan, workspace, params[0])
+    workspace, room = _room(workspace, ar_ortho_workspace(plan), params[0])
     d = _lib.ArMuonDesc(float(lr), float(momentum), float(weight_decay), int(bool(nesterov)),
                         ADJUSTS.get(adjust, adjust), float(grad_scale))
-    _check(_lib.load().ar_muon_step(plan.handle, d, p, g, m, po, mo, _ptr(workspace), _stream(stream)), "ar_muon_step")
+    _check(_lib.load().ar_muon_step(plan.handle, d, p, g, m, po, mo, room, _stream(stream)), "ar_muon_step")
 
 
 # ---------------------------------------------------------------- status

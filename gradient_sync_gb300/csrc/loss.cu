@@ -45,6 +45,48 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// Two fp32 operations an instruction.
+struct Pair {
+  uint64_t v;
+};
+__device__ __forceinline__ Pair pair_of(float lo, float hi) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 floats_of(Pair a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+// The pairs of a vector: 4 of bf16, 2 of fp32.
+template <bool BF16>
+__device__ __forceinline__ Pair pair_at(const uint4& r, int i) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  if (BF16) return pair_of(bf16lo(w[i]), bf16hi(w[i]));
+  return pair_of(__uint_as_float(w[2 * i % 4]), __uint_as_float(w[(2 * i + 1) % 4]));
+}
+// 2^(x k - shift) of both.
+__device__ __forceinline__ Pair exp2_pair(Pair x, Pair k, Pair minus_shift) {
+  const float2 y = floats_of(fma2(x, k, minus_shift));
+  return pair_of(exp2_approx(y.x), exp2_approx(y.y));
+}
+
 // A shift of -inf (a part of the row that is all -inf) is replaced by 0:
 // its terms are then 2^-inf = 0 rather than 2^(-inf + inf).
 __device__ __forceinline__ float finite_shift(float c) { return c == -INFINITY ? 0.0f : c; }
@@ -399,25 +441,23 @@ __device__ __forceinline__ float mean_scale(const LossParams& p) {
 // Sums `n` entries of each of COLUMNS columns (`pitch` apart) in a fixed order,
 // by the CTA; results in thread 0.
 template <int THREADS, int COLUMNS>
-__device__ __forceinline__ void sum_columns(const float* col, int64_t pitch, int64_t n, double (&out)[COLUMNS]) {
-  __shared__ double warp_sum[COLUMNS][THREADS / 32];
-  float a[COLUMNS];
+__device__ __forceinline__ void sum_columns(const float* col, int64_t pitch, int64_t n, float (&out)[COLUMNS]) {
+  __shared__ float warp_sum[COLUMNS][THREADS / 32];
+  float a[COLUMNS] = {};
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < n; i += THREADS)
+#pragma unroll
+    for (int c = 0; c < COLUMNS; ++c) a[c] += __ldcg(col + c * pitch + i);
 #pragma unroll
   for (int c = 0; c < COLUMNS; ++c) {
-    a[c] = 0.0f;
-    for (int64_t i = threadIdx.x; i < n; i += THREADS) a[c] += __ldcg(col + c * pitch + i);
-  }
 #pragma unroll
-  for (int c = 0; c < COLUMNS; ++c) {
-    double s = double(a[c]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-    if (threadIdx.x % 32 == 0) warp_sum[c][threadIdx.x / 32] = s;
+    for (int o = 16; o > 0; o >>= 1) a[c] += __shfl_xor_sync(~0u, a[c], o);
+    if (threadIdx.x % 32 == 0) warp_sum[c][threadIdx.x / 32] = a[c];
   }
   __syncthreads();
 #pragma unroll
   for (int c = 0; c < COLUMNS; ++c) {
-    out[c] = 0.0;
+    out[c] = 0.0f;
     if (threadIdx.x == 0)
       for (int w = 0; w < THREADS / 32; ++w) out[c] += warp_sum[c][w];
   }
@@ -570,17 +610,28 @@ __device__ __forceinline__ void lse_add(Lse& z, const uint4& raw, float k) {
 
 // The terms of a vector at a fixed shift.
 template <bool BF16>
-__device__ __forceinline__ float terms_of(const uint4& raw, float k, float shift) {
-  constexpr int W = Lane<BF16, true>::W;
-  float f[W];
-  Lane<BF16, true>::widen(raw, f);
+__device__ __forceinline__ Pair terms_of(const uint4& raw, Pair k, Pair minus_shift) {
+  constexpr int P = Lane<BF16, true>::W / 2;
+  Pair f[P];
 #pragma unroll
-  for (int w = 0; w < W; ++w) f[w] = exp2_approx(fmaf(f[w], k, -shift));
+  for (int w = 0; w < P; ++w) f[w] = exp2_pair(pair_at<BF16>(raw, w), k, minus_shift);
 #pragma unroll
-  for (int n = W / 2; n > 0; n /= 2)
+  for (int n = P / 2; n > 0; n /= 2)
 #pragma unroll
-    for (int w = 0; w < n; ++w) f[w] += f[w + n];
+    for (int w = 0; w < n; ++w) f[w] = add2(f[w], f[w + n]);
   return f[0];
+}
+
+// A vector of the gradient but for the label's element: 2^(x k - shift) g.
+template <bool BF16>
+__device__ __forceinline__ void gradient_of(const uint4& raw, Pair k, Pair minus_shift, Pair g,
+                                            float (&f)[Lane<BF16, true>::W]) {
+#pragma unroll
+  for (int w = 0; w < Lane<BF16, true>::W / 2; ++w) {
+    const float2 y = floats_of(mul2(exp2_pair(pair_at<BF16>(raw, w), k, minus_shift), g));
+    f[2 * w] = y.x;
+    f[2 * w + 1] = y.y;
+  }
 }
 
 // A thread of the streaming kernel takes its shift from the first vectors of a
@@ -692,6 +743,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
     auto sum_row = [&](int n, const StreamRow& r) {
       Lse z = {-INFINITY, 0.0f};
       if (r.label >= 0) {
+        const Pair kk = pair_of(p.k, p.k);
+        Pair ss = pair_of(0.0f, 0.0f), sum = ss;
 #pragma unroll 1
         for (int v = r.v0; v < r.v1; v += kVecsChunk) {
           if (!mbar_wait(&sh.full[summed], sum_phase, kWaitPolls, abort, status)) return false;
@@ -705,16 +758,19 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
             float top = largest<BF16>(raw[0]);
             if (kStep < left) top = fmaxf(top, largest<BF16>(raw[1]));
             z.c = fmaxf(kLeastShift, ceilf(top * p.k));
+            ss = pair_of(-z.c, -z.c);
           }
 #pragma unroll
           for (int j = 0; j < kThreadVecs; ++j)
-            if (j * kStep < left) z.s += terms_of<BF16>(raw[j], p.k, z.c);
+            if (j * kStep < left) sum = add2(sum, terms_of<BF16>(raw[j], kk, ss));
           if (!WRITE) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.empty[summed]);
           }
           advance(summed, sum_phase);
         }
+        const float2 both = floats_of(sum);
+        z.s = both.x + both.y;
         z = lse_warp(z, 32);
       }
       if (lane == 0) {
@@ -734,6 +790,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
       }
       const bool aligned = reinterpret_cast<uintptr_t>(d) % 16 == 0;
       const int own = int(r.label) - r.head;  // the label's place among the vectors' elements
+      const Pair kk = pair_of(q.k, q.k), ss = pair_of(-q.shift, -q.shift), gg = pair_of(q.g, q.g);
 #pragma unroll 1
       for (int v = r.v0; v < r.v1; v += kVecsChunk) {
         if (!SUM && !mbar_wait(&sh.full[written], write_phase, kWaitPolls, abort, status)) return false;
@@ -744,9 +801,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
         for (int j = 0; j < kThreadVecs; ++j) {
           if (j * kStep >= left) continue;
           float f[W];
-          L::widen(in[j * kStep], f);
-#pragma unroll
-          for (int w = 0; w < W; ++w) f[w] = exp2_approx(fmaf(f[w], q.k, -q.shift)) * q.g;
+          gradient_of<BF16>(in[j * kStep], kk, ss, gg, f);
           if (unsigned(mine - j * kStep * W) < unsigned(W)) {
 #pragma unroll
             for (int w = 0; w < W; ++w)
@@ -927,13 +982,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
 __global__ void __launch_bounds__(1024) stats_kernel(LossParams p) {
   grid_dependency_wait();
   grid_dependents_launch();
-  double out[3];
+  float out[3];
   sum_columns<1024, 3>(p.row_terms, p.rows, p.rows, out);
   if (threadIdx.x == 0) {
-    p.stats[0] = float(out[0] + double(p.kl) * out[1]);
-    p.stats[1] = float(out[0]);
-    p.stats[2] = float(out[1]);
-    p.stats[3] = float(out[2]);
+    p.stats[0] = out[0] + p.kl * out[1];
+    p.stats[1] = out[0];
+    p.stats[2] = out[1];
+    p.stats[3] = out[2];
   }
 }
 
@@ -945,62 +1000,72 @@ __global__ void __launch_bounds__(256) pair_kernel(LossParams p) {
   grid_dependency_wait();
   grid_dependents_launch();
   const int64_t pairs = p.n_seq / 2, i = blockIdx.x;
-  __shared__ double sums[2][8];
+  __shared__ Two sums[2][8];
   __shared__ int counts[2][8];
   __shared__ bool last;
   int64_t bounds[3];
   for (int h = 0; h < 3; ++h) bounds[h] = seq_bound(p, 2 * i + h);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // Sums of log ratios in pairs of fp32 (fp64 adds are slow here).
+  auto add = [](Two a, float hi, float lo) {
+    const Two s = two_sum(a.hi, hi);
+    return Two{s.hi, a.lo + s.lo + lo};
+  };
   for (int h = 0; h < 2; ++h) {
-    double a = 0.0;
+    Two a = {0.0f, 0.0f};
     int n = 0;
 #pragma unroll 4
     for (int64_t t = bounds[h] + threadIdx.x; t < bounds[h + 1]; t += 256)
       if (p.labels[t] >= 0) {
-        a += double(p.row_terms[t]);
+        a = add(a, p.row_terms[t], 0.0f);
         ++n;
       }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(~0u, a, o);
+    for (int o = 16; o > 0; o >>= 1) a = add(a, __shfl_xor_sync(~0u, a.hi, o), __shfl_xor_sync(~0u, a.lo, o));
     n = __reduce_add_sync(~0u, n);
     if (lane == 0) sums[h][warp] = a, counts[h][warp] = n;
   }
   __syncthreads();
-  double ratio[2];
-  float over[2];
-  for (int h = 0; h < 2; ++h) {
-    double a = 0.0;
-    int n = 0;
-    for (int w = 0; w < 8; ++w) a += sums[h][w], n += counts[h][w];
-    over[h] = p.normalize ? float(max(n, 1)) : 1.0f;
-    ratio[h] = a / double(over[h]);
-  }
   __shared__ float coef[2];
-  const double count = p.denominator > 0.0f ? double(p.denominator) : double(pairs);
   if (threadIdx.x == 0) {
-    const double z = double(p.beta) * (ratio[0] - ratio[1]);
-    double loss, slope;
+    const float count = p.denominator > 0.0f ? p.denominator : float(pairs);
+    float ratio[2], over[2];
+    Two rest[2];
+    for (int h = 0; h < 2; ++h) {
+      Two a = sums[h][0];
+      int n = counts[h][0];
+      for (int w = 1; w < 8; ++w) a = add(a, sums[h][w].hi, sums[h][w].lo), n += counts[h][w];
+      over[h] = p.normalize ? float(max(n, 1)) : 1.0f;
+      ratio[h] = (a.hi + a.lo) / over[h];
+      rest[h] = a;
+      if (!isfinite(ratio[h])) ratio[h] = a.hi;  // (an infinity has no low part)
+    }
+    // without the length, the difference of the ratios comes before their rounding
+    const float apart = p.normalize || !isfinite(ratio[0] - ratio[1])
+                            ? ratio[0] - ratio[1]
+                            : (rest[0].hi - rest[1].hi) + (rest[0].lo - rest[1].lo);
+    const float z = p.beta * apart;
+    float loss, slope;
     if (p.square) {
-      const double off = z - double(p.target);
+      const float off = z - p.target;
       loss = off * off;
-      slope = 2.0 * off;
+      slope = 2.0f * off;
     } else {
       // log1p(e^-|z|) serves both signs of z
-      const double tail = log1p(exp(-fabs(z))), up = z > 0.0 ? z : 0.0, down = z < 0.0 ? -z : 0.0;
-      const double eps = double(p.smooth);
-      loss = (1.0 - eps) * (tail + down) + eps * (tail + up);
-      slope = -(1.0 - eps) / (1.0 + exp(z)) + eps / (1.0 + exp(-z));
+      const float tail = log1pf(expf(-fabsf(z))), up = z > 0.0f ? z : 0.0f, down = z < 0.0f ? -z : 0.0f;
+      loss = (1.0f - p.smooth) * (tail + down) + p.smooth * (tail + up);
+      slope = -(1.0f - p.smooth) / (1.0f + expf(z)) + p.smooth / (1.0f + expf(-z));
       if (z != z) loss = slope = z;
     }
     for (int h = 0; h < 2; ++h)
-      coef[h] = float((h ? -1.0 : 1.0) * slope * double(p.beta) / count / double(over[h]) * double(p.grad_scale));
-    p.ratios[2 * i] = float(ratio[0]);
-    p.ratios[2 * i + 1] = float(ratio[1]);
+      coef[h] = (h ? -1.0f : 1.0f) * slope * p.beta / count / over[h] * p.grad_scale;
+    p.ratios[2 * i] = ratio[0];
+    p.ratios[2 * i + 1] = ratio[1];
     float* terms = p.row_terms + p.rows;
-    terms[i] = float(loss / count);
-    terms[pairs + i] = float(double(p.beta) * ratio[0] / count);
-    terms[2 * pairs + i] = float(double(p.beta) * ratio[1] / count);
-    terms[3 * pairs + i] = ratio[0] > ratio[1] ? float(1.0 / count) : 0.0f;
+    terms[i] = loss / count;
+    terms[pairs + i] = p.beta * ratio[0] / count;
+    terms[2 * pairs + i] = p.beta * ratio[1] / count;
+    terms[3 * pairs + i] = ratio[0] > ratio[1] ? 1.0f / count : 0.0f;
     __threadfence();
     last = atomicAdd(&p.tickets[0], 1u) == gridDim.x - 1;
   }
@@ -1013,10 +1078,10 @@ __global__ void __launch_bounds__(256) pair_kernel(LossParams p) {
     for (int64_t t = bounds[2] + threadIdx.x; t < p.rows; t += 256) p.row_a[t] = 0.0f;
   if (!last) return;
   __threadfence();
-  double out[4];
+  float out[4];
   sum_columns<256, 4>(p.row_terms + p.rows, pairs, pairs, out);
   if (threadIdx.x == 0)
-    for (int c = 0; c < 4; ++c) p.stats[c] = float(out[c]);
+    for (int c = 0; c < 4; ++c) p.stats[c] = out[c];
 }
 
 // ---------------------------------------------------------------- launches

@@ -68,6 +68,8 @@ def _stream(stream) -> int:
     if stream is None:
         import torch
 
+        if torch.cuda.is_initialized():  # without the Stream object, which takes longer to make than a call to enqueue
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return int(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return stream

@@ -239,6 +239,15 @@ __host__ __device__ inline int tiles_of(int op, int nu, int mb, int nb) {
   return n;
 }
 
+// Whether the input of a step is held as hi + lo. The last two steps amplify
+// little: dropping lo there changes the error of a half-precision result by
+// less than its own spread (1.1e-3 either way, Gaussian 512 x 2048), and saves
+// 8 of the 18 bytes of lo that an element's five steps move.
+template <bool SPLIT>
+__device__ __forceinline__ bool has_lo(const OrthoTable& p, int step) {
+  return SPLIT || step + 2 < p.steps;
+}
+
 // One tile of one product.
 struct Tile {
   int op, step;  // product (kNone: no more tiles), Newton-Schulz step
@@ -392,12 +401,14 @@ __device__ __forceinline__ void write_rows(const OrthoIo& io, const OrthoMat& ma
 // the new ones: as hi and lo, or (last) as fp32.
 struct Combine {
   float scale, add, diag;
+  bool lo_in, lo_out;  // hi + lo, or hi alone
 };
-template <int OP>
-__device__ __forceinline__ Combine combine_of(const OrthoMat& mat, const OrthoPoly& poly) {
-  if (OP == kGram) return {kScaleA / (mat.sx * mat.sx), 0.0f, 0.0f};
-  if (OP == kSquare) return {poly.c / kScaleA, poly.b, poly.t * kScaleA};
-  return {1.0f / kScaleA, poly.a - poly.t, 0.0f};
+template <int OP, bool SPLIT>
+__device__ __forceinline__ Combine combine_of(const OrthoTable& p, const OrthoMat& mat, int step) {
+  const OrthoPoly& poly = p.poly[step];
+  if (OP == kGram) return {kScaleA / (mat.sx * mat.sx), 0.0f, 0.0f, false, SPLIT};
+  if (OP == kSquare) return {poly.c / kScaleA, poly.b, poly.t * kScaleA, SPLIT, SPLIT};
+  return {1.0f / kScaleA, poly.a - poly.t, 0.0f, has_lo<SPLIT>(p, step), has_lo<SPLIT>(p, step + 1)};
 }
 template <int OP, bool SPLIT>
 __device__ __forceinline__ void combine16(const Combine& f, int q, int diag, float (&v)[16], char* buf) {
@@ -409,7 +420,7 @@ __device__ __forceinline__ void combine16(const Combine& f, int q, int diag, flo
     if (OP != kGram) {
       const uint4 hi = *reinterpret_cast<const uint4*>(buf + off);
       uint4 lo = make_uint4(0, 0, 0, 0);
-      if (OP >= kApply || SPLIT) lo = *reinterpret_cast<const uint4*>(buf + 4096 + off);
+      if (f.lo_in) lo = *reinterpret_cast<const uint4*>(buf + 4096 + off);
       const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -436,7 +447,7 @@ __device__ __forceinline__ void combine16(const Combine& f, int q, int diag, flo
       split_pair(u[4], u[5], hi.z, lo.z);
       split_pair(u[6], u[7], hi.w, lo.w);
       *reinterpret_cast<uint4*>(buf + off) = hi;
-      if (OP == kApply || SPLIT) *reinterpret_cast<uint4*>(buf + 4096 + off) = lo;
+      if (f.lo_out) *reinterpret_cast<uint4*>(buf + 4096 + off) = lo;
     }
   }
 }
@@ -448,7 +459,7 @@ __device__ __forceinline__ void finish_block(const OrthoTable& p, const Tile& t,
   constexpr int HALVES = SPLIT ? 2 : 1;
   const int lane = threadIdx.x % 32;
   const OrthoMat& mat = p.mat[t.i];
-  const Combine f = combine_of<OP>(mat, p.poly[t.step]);
+  const Combine f = combine_of<OP, SPLIT>(p, mat, t.step);
   const int diag = row0 + lane - cb * 64;
   auto group = [&](int q, float(&v)[16]) {
     combine16<OP, SPLIT>(f, q, diag, v, buf);
@@ -495,7 +506,7 @@ __device__ __forceinline__ void finish_block(const OrthoTable& p, const Tile& t,
         lo_at = mat.a_bytes;
       }
       bulk_store(to, buf, 4096);
-      if (OP == kApply || SPLIT) bulk_store(to + lo_at, buf + 4096, 4096);
+      if (f.lo_out) bulk_store(to + lo_at, buf + 4096, 4096);
       bulk_commit();
     }
   }
@@ -524,8 +535,9 @@ __device__ __forceinline__ bool tiles_complete(const unsigned int* done, unsigne
 // in order. A tile waits for its matrix's earlier products only, and those are
 // taken before it, so some worker can always go on, however many run at once;
 // and one matrix's tiles fill the others' waits. Of a CTA, one warp takes tiles
-// and waits for what they need, two tiles ahead; one copies operands; one
-// issues products into one half of TMEM; the others empty the other half.
+// up to two ahead, tells the others of each and, once what it needs is there,
+// that it can start; one copies operands; one issues products into one half of
+// TMEM; the others empty the other half.
 template <bool SPLIT, int CLUSTER>
 __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
     steps_kernel(const __grid_constant__ OrthoTable p) {
@@ -535,7 +547,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
   constexpr int SEGMENT = SPLIT ? kSegment : 1 << 30;
   extern __shared__ char smem_raw[];
   __shared__ uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], done, old_full[EPI];
-  __shared__ uint64_t item_full[RING], item_free[RING], mail_full[RING], mail_free[RING];
+  __shared__ uint64_t item_full[RING], item_free[RING], item_ready[RING], mail_full[RING], mail_free[RING], mail_ready[RING];
   __shared__ int items[RING][kTileWords], mail[RING][kTileWords];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
@@ -559,6 +571,8 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
     for (int s = 0; s < RING; ++s) {
       mbar_init(&item_full[s], 1);
       mbar_init(&item_free[s], rank == 0 ? EPI + 2 : EPI + 1);  // epilogue, producer, tensor core
+      mbar_init(&item_ready[s], 1);
+      mbar_init(&mail_ready[s], 1);
       mbar_init(&mail_full[s], 1);
       mbar_init(&mail_free[s], 1);
     }
@@ -577,14 +591,19 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
   grid_dependents_launch();
   asm volatile("fence.proxy.async;" ::: "memory");
 
-  // The n-th tile of this worker.
+  // The n-th tile of this worker, and whether what it needs is there.
   auto receive = [&](int n, Tile& t) {
     const bool ok = mbar_wait(&item_full[n % RING], (n / RING) & 1, kWaitPolls, abort, p.status);
     const volatile int* w = items[n % RING];
     t.op = w[0], t.step = w[1], t.i = w[2], t.tm = w[3], t.tn = w[4], t.nu = w[5], t.ks = w[6];
+    return !__any_sync(~0u, !ok) && t.op != kNone;
+  };
+  auto ready = [&](int n) {
+    return !__any_sync(~0u, !mbar_wait(&item_ready[n % RING], (n / RING) & 1, kWaitPolls, abort, p.status));
+  };
+  auto taken = [&](int n) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&item_free[n % RING]);
-    return !__any_sync(~0u, !ok) && t.op != kNone;
   };
 
   if (warp == EPI + 2) {
@@ -596,13 +615,10 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
         const int s = n % RING;
         const uint32_t reuse = (n / RING + 1) & 1;
         int words[7];
+        Tile t = {kNone, 0, 0, 0, 0, 0, 0, 0};
         if (rank == 0) {
           const int item = int(atomicAdd(queue, 1u));
-          Tile t = {kNone, 0, 0, 0, 0, 0, 0, 0};
-          if (item < n_items) {
-            t = find_tile<S>(p, item);
-            if (t.need > 0 && !tiles_complete(complete + t.i, unsigned(t.need) * S::PER_TILE, abort, p.status)) break;
-          }
+          if (item < n_items) t = find_tile<S>(p, item);
           words[0] = t.op, words[1] = t.step, words[2] = t.i, words[3] = t.tm, words[4] = t.tn, words[5] = t.nu;
           words[6] = t.ks;
           if (PAIR) {
@@ -615,13 +631,20 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
           if (!mbar_wait<true>(&mail_full[s], (n / RING) & 1, kWaitPolls, abort, p.status)) break;
 #pragma unroll
           for (int w = 0; w < 7; ++w) words[w] = *static_cast<volatile int*>(&mail[s][w]);
-          mbar_arrive_remote<true>(&mail_free[s], 0);
         }
         if (n >= RING && !mbar_wait(&item_free[s], reuse, kWaitPolls, abort, p.status)) break;
 #pragma unroll
         for (int w = 0; w < 7; ++w) items[s][w] = words[w];
         mbar_arrive(&item_full[s]);
         if (words[0] == kNone) break;
+        if (rank == 0) {
+          if (t.need > 0 && !tiles_complete(complete + t.i, unsigned(t.need) * S::PER_TILE, abort, p.status)) break;
+          if (PAIR) mbar_arrive_remote<true>(&mail_ready[s], 1);
+        } else {
+          if (!mbar_wait<true>(&mail_ready[s], (n / RING) & 1, kWaitPolls, abort, p.status)) break;
+          mbar_arrive_remote<true>(&mail_free[s], 0);
+        }
+        mbar_arrive(&item_ready[s]);
       }
     }
   } else if (warp == EPI) {
@@ -631,18 +654,21 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
     const uint32_t bar0 = PAIR ? cluster_addr(&full[0], 0) : smem_u32(&full[0]);
     int s = 0, steps_issued = 0;
     uint32_t phase = 1;  // the empty barriers' parity: the first round waits for nothing
-    Tile t;
-    for (int n = 0; receive(n, t); ++n) {
-      asm volatile("fence.proxy.async;" ::: "memory");
+    // One lane's copies of a tile: half of an operand unit's 128 rows x 64 of k,
+    // or (mn) half a block of one of the two column blocks that hold those rows
+    // as columns. Places in the workspace count in rows of 128 bytes.
+    struct Copies {
+      int ks, at_k, at_mn, mn_from, nb;
+      uint32_t dst, bytes;
+      bool active, whole;  // whole: a k-major unit in one copy of this lane
+    };
+    auto set_up = [&](const Tile& t, Copies& q) {
       const OrthoMat& mat = p.mat[t.i];
-      // This lane's copy: half of an operand unit's 128 rows x 64 of k, or (mn)
-      // half a block of one of the two column blocks that hold those rows as
-      // columns. Places in the workspace count in rows of 128 bytes.
       const bool is_a = lane < 2 * HALVES;
       const int per_half = PAIR ? t.nu : 2 * t.nu;  // copies of the right operand
       const int c = is_a ? lane : lane - 2 * HALVES;
       const int h = is_a ? c / 2 : c / per_half;
-      const bool active = is_a || h < HALVES;
+      q.active = is_a || h < HALVES;
       int row, sub;  // block of rows, half of it
       if (is_a) {
         row = t.tm * S::CTAS + rank;
@@ -657,30 +683,49 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
         row = t.tn + rank;
         sub = c % per_half;
       }
-      const uint32_t dst =
-          smem_u32(stage0) + (is_a ? h * kUnit + sub * (kUnit / 2)
-                                   : HALVES * kUnit + h * S::B_BYTES + c % per_half * (kUnit / 2));
+      q.whole = sub == 0;
+      q.dst = smem_u32(stage0) + (is_a ? h * kUnit + sub * (kUnit / 2)
+                                       : HALVES * kUnit + h * S::B_BYTES + c % per_half * (kUnit / 2));
       const bool is_x = is_a ? t.op == kGram : t.op != kSquare;
-      const int nb = is_x ? mat.nb : 2 * mat.mb;
+      q.nb = is_x ? mat.nb : 2 * mat.mb;
       const int64_t base = is_x ? mat.x + (t.step & 1) * 2 * mat.x_bytes + h * mat.x_bytes
                                 : mat.a + (t.op == kApply ? HALVES * mat.a_bytes : 0) + h * mat.a_bytes;
-      const int at_k = int(base / 128) + row * nb * 128 + sub * 64, at_mn = int(base / 128) + row * 256 + sub * 128;
-      const int mn_from = is_a ? left_mn_from<S>(t) : right_mn_from<S>(t);
-      const uint32_t bytes = HALVES * (S::CTAS * kUnit + t.nu * kUnit);
-      for (int k = 0; k < t.ks; ++k) {
+      q.at_k = int(base / 128) + row * q.nb * 128 + sub * 64;
+      q.at_mn = int(base / 128) + row * 256 + sub * 128;
+      q.mn_from = is_a ? left_mn_from<S>(t) : right_mn_from<S>(t);
+      q.bytes = HALVES * (S::CTAS * kUnit + t.nu * kUnit);
+      q.ks = t.ks;
+    };
+    Tile t;
+    Copies q, after;
+    bool more = receive(0, t);
+    if (more) set_up(t, q);
+    for (int n = 0; more; ++n, q = after) {
+      if (!ready(n)) break;
+      taken(n);
+      asm volatile("fence.proxy.async;" ::: "memory");
+      // the next tile is prepared while this one's copies wait for room
+      const int prepare = min(STAGES, q.ks) - 1;
+      for (int k = 0; k < q.ks; ++k) {
         if (!mbar_wait(&empty[s], phase, kWaitPolls, abort, p.status)) break;
         // the second CTA's copies count on the first one's barrier
-        if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-        const int from = k >= mn_from ? at_mn + (k >> 1) * nb * 128 + (k & 1) * 64 : at_k + k * 128;
-        const uint32_t to = dst + s * S::STAGE, bar = bar0 + s * 8;
-        if (active) {
+        if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&full[s], q.bytes);
+        const int from = k >= q.mn_from ? q.at_mn + (k >> 1) * q.nb * 128 + (k & 1) * 64 : q.at_k + k * 128;
+        const uint32_t to = q.dst + s * S::STAGE, bar = bar0 + s * 8;
+        if (q.active) {
           if (PAIR) pair_load(to, &p.map, from, bar);
-          else bulk_load_at(to, p.ws + int64_t(from) * 128, kUnit / 2, bar);
+          else if (k >= q.mn_from) bulk_load_at(to, p.ws + int64_t(from) * 128, kUnit / 2, bar);
+          else if (q.whole) bulk_load_at(to, p.ws + int64_t(from) * 128, kUnit, bar);
         }
         ++steps_issued;
         if (++s == STAGES) {
           s = 0;
           phase ^= 1;
+        }
+        if (k == prepare) {
+          __syncwarp();
+          more = receive(n + 1, t);
+          if (more) set_up(t, after);
         }
       }
       __syncwarp();
@@ -701,6 +746,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
     const uint32_t stage_addr = smem_u32(stage0);
     Tile t;
     for (int n = 0; receive(n, t); ++n) {
+      taken(n);
       const int a_from = left_mn_from<S>(t), b_from = right_mn_from<S>(t);
       const uint32_t idesc = instr_desc(S::CTAS * 128, t.nu * 128);
       for (int k0 = 0; k0 < t.ks; k0 += SEGMENT, ++part) {
@@ -773,7 +819,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
       const OrthoMat& mat = p.mat[t.i];
       bulk_wait_read<0>();
       if (t.op == kGram) return;
-      const bool two = t.op == kApply || SPLIT;
+      const bool two = SPLIT || (t.op == kApply && has_lo<SPLIT>(p, t.step));
       mbar_arrive_expect_tx(&old_full[warp], two ? 8192 : 4096);
       const char* from = p.ws + block + (t.op == kSquare ? mat.a : mat.x + (t.step & 1) * 2 * mat.x_bytes);
       bulk_load(buf, from, 4096, &old_full[warp]);
@@ -786,12 +832,16 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
       if (!receive(n, t)) break;
       const OrthoMat& mat = p.mat[t.i];
       const int rb = t.tm * S::CTAS + rank, row0 = rb * 128 + quad * 32;
-      const bool mine = SPLIT || part_of < t.nu;  // else no such column block in this tile
-      const int cb0 = 2 * t.tn + part_of * S::BLOCKS;  // its first block of 64 columns
+      // Blocks of 64 columns of this warp: two, or one of a tile of 128 columns.
+      const int blocks = min(S::BLOCKS, t.nu);
+      const int cb0 = 2 * t.tn + part_of * blocks;
       const int64_t block0 = (int64_t(rb) * (t.op == kApply ? mat.nb : 2 * mat.mb) + cb0) * kBlockBytes + quad * 4096;
       bool landed = true;
+      if (!mbar_test(&item_ready[n % RING], (n / RING) & 1)) report(false);
+      if (!ready(n)) break;
+      taken(n);
       if (lane == 0) asm volatile("fence.proxy.async;" ::: "memory");
-      if (mine) load_old(t, block0);
+      load_old(t, block0);
       float sum[SPLIT ? 64 : 1];
       uint32_t at = 0;  // this warp's accumulator
       for (int k0 = 0; k0 < t.ks; k0 += SEGMENT, ++part) {
@@ -804,7 +854,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
           break;
         }
         fence_after();
-        at = tmem + (uint32_t(quad * 32) << 16) + acc * 256 + part_of * S::BLOCKS * 64;
+        at = tmem + (uint32_t(quad * 32) << 16) + acc * 256 + part_of * blocks * 64;
         if (SPLIT) {
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
@@ -820,8 +870,8 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
         }
       }
 #pragma unroll 1
-      for (int h = 0; h < S::BLOCKS; ++h) {
-        if (!mine || !landed) break;
+      for (int h = 0; h < blocks; ++h) {
+        if (!landed) break;
         const int64_t block = block0 + h * kBlockBytes;
         if (h > 0) load_old(t, block);
         if (t.op != kGram) {
@@ -837,7 +887,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
         if (h == 0) report(t.op != kApply || t.step + 1 < p.steps);  // (the last product leaves no bulk stores)
       }
       if (!landed) {  // winding down: a copy in flight still lands before the CTA goes
-        if (mine && t.op != kGram)
+        if (t.op != kGram)
           for (uint32_t k = 0; k < kWaitPolls && !mbar_try_wait(&old_full[warp], old_phase); ++k) {
           }
         break;

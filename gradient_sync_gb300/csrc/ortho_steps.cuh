@@ -133,8 +133,7 @@ __device__ __forceinline__ void store_remote(int* p, uint32_t rank, int v) {
 // complete: count them, for whoever reads them next.
 __device__ __forceinline__ void signal_complete(unsigned int* count, bool newer) {
   if (newer) asm volatile("cp.async.bulk.wait_group 1;" ::: "memory");
-  else bulk_wait_all();
-  asm volatile("fence.proxy.async;" ::: "memory");
+  else bulk_wait_all();  // (complete: visible to this thread, hence to whom the count tells)
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
 }
 
@@ -477,7 +476,7 @@ __device__ __forceinline__ void finish_block(const OrthoTable& p, const Tile& t,
       group(q, v);
     }
   } else {
-#pragma unroll 1
+#pragma unroll 2
     for (int q = 0; q < 4; ++q) {
       float v[16];
       tmem_load16(at + 16 * q, v);
@@ -512,8 +511,8 @@ __device__ __forceinline__ void finish_block(const OrthoTable& p, const Tile& t,
   }
 }
 
-// Waits until `need` of the matrix's tiles are complete and their writes can
-// be copied from.
+// Waits until `need` of the matrix's tiles are complete. (Copies of what they
+// wrote need a proxy fence of the thread that issues them.)
 __device__ __forceinline__ bool tiles_complete(const unsigned int* done, unsigned int need, volatile int* abort,
                                                const StatusRef& status) {
   bool ok = false;
@@ -527,7 +526,6 @@ __device__ __forceinline__ bool tiles_complete(const unsigned int* done, unsigne
     __nanosleep(32);
   }
   if (!ok && !*abort) report_timeout(abort, status);
-  asm volatile("fence.proxy.async;" ::: "memory");
   return ok;
 }
 

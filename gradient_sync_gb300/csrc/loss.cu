@@ -463,6 +463,148 @@ __device__ __forceinline__ void sum_columns(const float* col, int64_t pitch, int
   }
 }
 
+// Calls of a few rows do without the kernels that count sequences and join
+// pairs: every CTA of the rows' kernels does that for its own row, while its
+// part of the row is on the way.
+constexpr int kFewRows = 512, kFewSequences = 32;
+
+struct FewShared {
+  int64_t bound[kFewSequences + 1];
+  int count[kFewSequences];
+};
+
+// Bounds of the sequences (shared memory), and the one that row t is in (-1:
+// none). Ends with the bounds visible to the CTA.
+template <int THREADS>
+__device__ __forceinline__ void few_bounds(const LossParams& p, FewShared& sh) {
+  if (threadIdx.x <= p.n_seq) sh.bound[threadIdx.x] = seq_bound(p, threadIdx.x);
+  if (threadIdx.x < p.n_seq) sh.count[threadIdx.x] = 0;
+  __syncthreads();
+}
+__device__ __forceinline__ int few_sequence(const LossParams& p, const FewShared& sh, int64_t t) {
+  for (int s = 0; s < p.n_seq; ++s)
+    if (t >= sh.bound[s] && t < sh.bound[s + 1]) return s;
+  return -1;
+}
+
+// A row's weight, the mean's denominator included.
+template <int THREADS>
+__device__ __forceinline__ float few_weight(const LossParams& p, FewShared& sh, int64_t t) {
+  few_bounds<THREADS>(p, sh);
+  for (int64_t r = threadIdx.x; r < p.rows; r += THREADS)
+    if (p.labels[r] >= 0) {
+      const int s = few_sequence(p, sh, r);
+      if (s >= 0) atomicAdd(&sh.count[s], 1);
+    }
+  __syncthreads();
+  int total = 0;
+  for (int s = 0; s < p.n_seq; ++s) total += p.by_sequence ? sh.count[s] > 0 : sh.count[s];
+  const int own = few_sequence(p, sh, t);
+  if (own < 0) return 0.0f;
+  const float weight = p.by_sequence ? 1.0f / float(max(sh.count[own], 1)) : 1.0f;
+  return weight * (p.denominator > 0.0f ? 1.0f / p.denominator : 1.0f / float(max(total, 1)));
+}
+
+// The log ratio of a sequence before any division, and its labelled tokens, by one warp.
+__device__ __forceinline__ Two add_two(Two a, float hi, float lo) {
+  const Two s = two_sum(a.hi, hi);
+  return {s.hi, a.lo + s.lo + lo};
+}
+__device__ __forceinline__ Two warp_ratio(const LossParams& p, int64_t lo, int64_t hi, int& count) {
+  Two a = {0.0f, 0.0f};
+  int n = 0;
+#pragma unroll 4
+  for (int64_t t = lo + threadIdx.x % 32; t < hi; t += 32)
+    if (p.labels[t] >= 0) {
+      a = add_two(a, __ldcg(&p.row_terms[t]), 0.0f);
+      ++n;
+    }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a = add_two(a, __shfl_xor_sync(~0u, a.hi, o), __shfl_xor_sync(~0u, a.lo, o));
+  count = __reduce_add_sync(~0u, n);
+  return a;
+}
+
+// One pair: statistics' terms and the coefficients of its rows.
+struct PairTerms {
+  float ratio[2], terms[4], coef[2];
+};
+__device__ __forceinline__ PairTerms pair_terms(const LossParams& p, const Two (&sum)[2], const int (&n)[2]) {
+  PairTerms r;
+  const float count = p.denominator > 0.0f ? p.denominator : float(p.n_seq / 2);
+  float over[2];
+  for (int h = 0; h < 2; ++h) {
+    over[h] = p.normalize ? float(max(n[h], 1)) : 1.0f;
+    r.ratio[h] = (sum[h].hi + sum[h].lo) / over[h];
+    if (!isfinite(r.ratio[h])) r.ratio[h] = sum[h].hi;  // (an infinity has no low part)
+  }
+  // without the length, the difference of the ratios comes before their rounding
+  const float apart = p.normalize || !isfinite(r.ratio[0] - r.ratio[1])
+                          ? r.ratio[0] - r.ratio[1]
+                          : (sum[0].hi - sum[1].hi) + (sum[0].lo - sum[1].lo);
+  const float z = p.beta * apart;
+  float loss, slope;
+  if (p.square) {
+    const float off = z - p.target;
+    loss = off * off;
+    slope = 2.0f * off;
+  } else {
+    // log1p(e^-|z|) serves both signs of z
+    const float tail = log1pf(expf(-fabsf(z))), up = z > 0.0f ? z : 0.0f, down = z < 0.0f ? -z : 0.0f;
+    loss = (1.0f - p.smooth) * (tail + down) + p.smooth * (tail + up);
+    slope = -(1.0f - p.smooth) / (1.0f + expf(z)) + p.smooth / (1.0f + expf(-z));
+    if (z != z) loss = slope = z;
+  }
+  for (int h = 0; h < 2; ++h)
+    r.coef[h] = (h ? -1.0f : 1.0f) * slope * p.beta / count / over[h] * p.grad_scale;
+  r.terms[0] = loss / count;
+  r.terms[1] = p.beta * r.ratio[0] / count;
+  r.terms[2] = p.beta * r.ratio[1] / count;
+  r.terms[3] = r.ratio[0] > r.ratio[1] ? 1.0f / count : 0.0f;
+  return r;
+}
+
+// The coefficient of row t; the first CTA also writes ratios and statistics.
+template <int THREADS>
+__device__ __forceinline__ float few_coefficient(const LossParams& p, FewShared& sh, int64_t t, bool first) {
+  __shared__ Two sum[kFewSequences];
+  __shared__ float terms[4][kFewSequences / 2];
+  few_bounds<THREADS>(p, sh);
+  const int warp = threadIdx.x / 32, own = few_sequence(p, sh, t);
+  // the row's pair, or all of them
+  const int from = first ? 0 : own < 0 ? 0 : own / 2 * 2, to = first ? int(p.n_seq) : own < 0 ? 0 : from + 2;
+  for (int s = from + warp; s < to; s += THREADS / 32) {
+    int n;
+    const Two a = warp_ratio(p, sh.bound[s], sh.bound[s + 1], n);
+    if (threadIdx.x % 32 == 0) {
+      sum[s] = a;
+      sh.count[s] = n;
+    }
+  }
+  __syncthreads();
+  auto pair = [&](int i) {
+    const Two two[2] = {sum[2 * i], sum[2 * i + 1]};
+    const int n[2] = {sh.count[2 * i], sh.count[2 * i + 1]};
+    return pair_terms(p, two, n);
+  };
+  if (first) {
+    const int i = threadIdx.x;
+    if (i < p.n_seq / 2) {
+      const PairTerms r = pair(i);
+      p.ratios[2 * i] = r.ratio[0];
+      p.ratios[2 * i + 1] = r.ratio[1];
+      for (int c = 0; c < 4; ++c) terms[c][i] = r.terms[c];
+    }
+    __syncthreads();
+    if (threadIdx.x < 4) {
+      float a = 0.0f;
+      for (int k = 0; k < p.n_seq / 2; ++k) a += terms[threadIdx.x][k];
+      p.stats[threadIdx.x] = a;
+    }
+  }
+  return own < 0 ? 0.0f : pair(own / 2).coef[own & 1];
+}
+
 // ---------------------------------------------------------------- rows
 
 // One cluster a row.
@@ -480,7 +622,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) rows_kernel(LossParam
   char* d = p.d == nullptr ? nullptr : static_cast<char*>(p.d) + t * p.dld * ES;
   if (MODE == kPrefForward && blockIdx.x == 0 && threadIdx.x == 0) p.tickets[0] = 0;
   const int64_t label = p.labels[t];
+  __shared__ FewShared few;
+  const bool first = blockIdx.x == 0;
   if (label < 0) {
+    if (MODE == kPrefBackward && p.few && first) few_coefficient<THREADS>(p, few, t, true);
     if ((MODE == kPolicy || MODE == kPrefBackward) && d != nullptr) write_zeros<BF16, THREADS>(d, int(p.vocab), rank, ranks);
     if (MODE != kPrefBackward && rank == 0 && threadIdx.x == 0) {
       p.logp[t] = 0.0f;
@@ -496,7 +641,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) rows_kernel(LossParam
   const float edge = slice.edge >= 0 ? load_one<BF16>(x, slice.edge) : -INFINITY;
   if (MODE == kPrefBackward) {
     const float2 z = p.row_lse[t];  // the sign of 1 / sum tells the scale
-    write_gradient<BF16, THREADS>(slice, d, raw, edge, label, p.row_a[t] * p.inv_temp, z.y < 0.0f ? 1.0f : p.k, z.x,
+    const float coef = p.few ? few_coefficient<THREADS>(p, few, t, first) : p.row_a[t];
+    write_gradient<BF16, THREADS>(slice, d, raw, edge, label, coef * p.inv_temp, z.y < 0.0f ? 1.0f : p.k, z.x,
                                   fabsf(z.y));
     return;
   }
@@ -505,12 +651,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) rows_kernel(LossParam
   const float x_label = label < p.vocab ? load_one<BF16>(x, label) : nan;
   float weight = 0.0f, adv = 0.0f, old = 0.0f, ref = 0.0f;
   if (MODE == kPolicy) {
-    weight = p.row_a[t];
     adv = p.adv[t];
     old = p.old_logp[t];
-    if (threadIdx.x < 32) {
-      const float m = mean_scale(p);
-      if (threadIdx.x == 0) mean_shared = m;
+    if (p.few) {
+      weight = few_weight<THREADS>(p, few, t);
+    } else {
+      weight = p.row_a[t];
+      if (threadIdx.x < 32) {
+        const float m = mean_scale(p);
+        if (threadIdx.x == 0) mean_shared = m;
+      }
     }
   }
   if ((MODE == kPolicy || MODE == kPrefForward) && p.ref_logp != nullptr) ref = p.ref_logp[t];
@@ -535,7 +685,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) rows_kernel(LossParam
     p.row_lse[t] = make_float2(shift, copysignf(inv_sum, k == p.k ? 1.0f : -1.0f));
   }
   if (MODE != kPolicy) return;
-  const PolicyTerm term = policy_term(p, lp, weight, mean_shared, adv, old, ref);
+  const PolicyTerm term = policy_term(p, lp, weight, p.few ? 1.0f : mean_shared, adv, old, ref);
   if (d != nullptr) {
     if (weight == 0.0f)
       write_zeros<BF16, THREADS>(d, int(p.vocab), rank, ranks);
@@ -1007,65 +1157,37 @@ __global__ void __launch_bounds__(256) pair_kernel(LossParams p) {
   for (int h = 0; h < 3; ++h) bounds[h] = seq_bound(p, 2 * i + h);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   // Sums of log ratios in pairs of fp32 (fp64 adds are slow here).
-  auto add = [](Two a, float hi, float lo) {
-    const Two s = two_sum(a.hi, hi);
-    return Two{s.hi, a.lo + s.lo + lo};
-  };
   for (int h = 0; h < 2; ++h) {
     Two a = {0.0f, 0.0f};
     int n = 0;
 #pragma unroll 4
     for (int64_t t = bounds[h] + threadIdx.x; t < bounds[h + 1]; t += 256)
       if (p.labels[t] >= 0) {
-        a = add(a, p.row_terms[t], 0.0f);
+        a = add_two(a, p.row_terms[t], 0.0f);
         ++n;
       }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = add(a, __shfl_xor_sync(~0u, a.hi, o), __shfl_xor_sync(~0u, a.lo, o));
+    for (int o = 16; o > 0; o >>= 1) a = add_two(a, __shfl_xor_sync(~0u, a.hi, o), __shfl_xor_sync(~0u, a.lo, o));
     n = __reduce_add_sync(~0u, n);
     if (lane == 0) sums[h][warp] = a, counts[h][warp] = n;
   }
   __syncthreads();
   __shared__ float coef[2];
   if (threadIdx.x == 0) {
-    const float count = p.denominator > 0.0f ? p.denominator : float(pairs);
-    float ratio[2], over[2];
-    Two rest[2];
+    Two sum[2];
+    int n[2];
     for (int h = 0; h < 2; ++h) {
-      Two a = sums[h][0];
-      int n = counts[h][0];
-      for (int w = 1; w < 8; ++w) a = add(a, sums[h][w].hi, sums[h][w].lo), n += counts[h][w];
-      over[h] = p.normalize ? float(max(n, 1)) : 1.0f;
-      ratio[h] = (a.hi + a.lo) / over[h];
-      rest[h] = a;
-      if (!isfinite(ratio[h])) ratio[h] = a.hi;  // (an infinity has no low part)
+      sum[h] = sums[h][0];
+      n[h] = counts[h][0];
+      for (int w = 1; w < 8; ++w) sum[h] = add_two(sum[h], sums[h][w].hi, sums[h][w].lo), n[h] += counts[h][w];
     }
-    // without the length, the difference of the ratios comes before their rounding
-    const float apart = p.normalize || !isfinite(ratio[0] - ratio[1])
-                            ? ratio[0] - ratio[1]
-                            : (rest[0].hi - rest[1].hi) + (rest[0].lo - rest[1].lo);
-    const float z = p.beta * apart;
-    float loss, slope;
-    if (p.square) {
-      const float off = z - p.target;
-      loss = off * off;
-      slope = 2.0f * off;
-    } else {
-      // log1p(e^-|z|) serves both signs of z
-      const float tail = log1pf(expf(-fabsf(z))), up = z > 0.0f ? z : 0.0f, down = z < 0.0f ? -z : 0.0f;
-      loss = (1.0f - p.smooth) * (tail + down) + p.smooth * (tail + up);
-      slope = -(1.0f - p.smooth) / (1.0f + expf(z)) + p.smooth / (1.0f + expf(-z));
-      if (z != z) loss = slope = z;
-    }
-    for (int h = 0; h < 2; ++h)
-      coef[h] = (h ? -1.0f : 1.0f) * slope * p.beta / count / over[h] * p.grad_scale;
-    p.ratios[2 * i] = ratio[0];
-    p.ratios[2 * i + 1] = ratio[1];
+    const PairTerms r = pair_terms(p, sum, n);
     float* terms = p.row_terms + p.rows;
-    terms[i] = loss / count;
-    terms[pairs + i] = p.beta * ratio[0] / count;
-    terms[2 * pairs + i] = p.beta * ratio[1] / count;
-    terms[3 * pairs + i] = ratio[0] > ratio[1] ? 1.0f / count : 0.0f;
+    for (int h = 0; h < 2; ++h) {
+      p.ratios[2 * i + h] = r.ratio[h];
+      coef[h] = r.coef[h];
+    }
+    for (int c = 0; c < 4; ++c) terms[c * pairs + i] = r.terms[c];
     __threadfence();
     last = atomicAdd(&p.tickets[0], 1u) == gridDim.x - 1;
   }
@@ -1147,7 +1269,7 @@ cudaError_t launch_rows_typed(LossParams p, cudaStream_t stream) {
   p.keep_bytes = int64_t(80) << 20;
   p.cluster = 1;
   while (MODE == kPolicy && p.cluster < kMaxCluster && bytes > int64_t(kStreamSlice) * p.cluster) p.cluster *= 2;
-  if (bytes >= kStreamRowBytes && (MODE != kPolicy || bytes <= int64_t(kStreamSlice) * p.cluster) && p.rows * p.cluster >= kStreamRowsAnSm * sms) {
+  if (bytes >= kStreamRowBytes && (MODE != kPolicy || bytes <= int64_t(kStreamSlice) * p.cluster) && p.rows * p.cluster >= kStreamRowsAnSm * sms && !p.few) {
     void (*kernel)(LossParams) = stream_kernel<BF16, MODE>;
     constexpr size_t kSmem = size_t(kStreamChunks) * kStreamChunk + 128;
     cudaError_t err = status_ref(&p.status_word, &p.status_host);
@@ -1183,17 +1305,21 @@ cudaError_t launch_token_logp(const LossParams& p, ar_dtype dtype, cudaStream_t 
   return launch_rows<kLogp>(p, dtype, stream);
 }
 
-cudaError_t launch_policy_loss(const LossParams& p, ar_dtype dtype, cudaStream_t stream) {
+cudaError_t launch_policy_loss(const LossParams& q, ar_dtype dtype, cudaStream_t stream) {
+  LossParams p = q;
+  p.few = p.rows <= kFewRows && p.n_seq <= kFewSequences;
   if (p.rows == 0) return cudaMemsetAsync(p.stats, 0, 16, stream);
-  cudaError_t err = launch_after(count_kernel, p, p.n_seq, 256, 1, stream);
+  cudaError_t err = p.few ? cudaSuccess : launch_after(count_kernel, p, p.n_seq, 256, 1, stream);
   if (err == cudaSuccess) err = launch_rows<kPolicy>(p, dtype, stream);
   if (err == cudaSuccess) err = launch_after(stats_kernel, p, 1, 1024, 1, stream);
   return err;
 }
 
-cudaError_t launch_preference_loss(const LossParams& p, ar_dtype dtype, cudaStream_t stream) {
+cudaError_t launch_preference_loss(const LossParams& q, ar_dtype dtype, cudaStream_t stream) {
+  LossParams p = q;
+  p.few = p.rows > 0 && p.rows <= kFewRows && p.n_seq <= kFewSequences && p.d != nullptr;
   cudaError_t err = p.rows == 0 ? cudaMemsetAsync(p.tickets, 0, 4, stream) : launch_rows<kPrefForward>(p, dtype, stream);
-  if (err == cudaSuccess) err = launch_after(pair_kernel, p, p.n_seq / 2, 256, 1, stream);
+  if (err == cudaSuccess && !p.few) err = launch_after(pair_kernel, p, p.n_seq / 2, 256, 1, stream);
   if (err == cudaSuccess && p.d != nullptr) err = launch_rows<kPrefBackward>(p, dtype, stream);
   return err;
 }

@@ -42,6 +42,7 @@ struct LossParams {
   int32_t* seq_count;     // [n_seq] labelled tokens
   float* row_a;           // [rows] policy: weight before the total; preference: coefficient
   int cluster;            // CTAs a row
+  int few;                // a few rows: weights and pairs are worked out by the rows' kernels
   unsigned int* status_word;         // where waits that ran out are recorded
   unsigned int* const* status_host;
   int64_t keep_bytes;     // logits that are worth keeping in the L2 between two passes

@@ -203,16 +203,15 @@ struct Slice {
     edge = rank == 0 ? span.edge(threadIdx.x) : -1;
   }
   __device__ __forceinline__ bool held() const { return v1 - v0 <= kChunk; }
-  // Vectors first + threadIdx.x + j THREADS, -inf beyond the slice. `keep`: the
-  // row will be read again soon.
-  __device__ __forceinline__ void load(uint4 (&raw)[kVecs], int first, bool keep) const {
+  // Vectors first + threadIdx.x + j THREADS, -inf beyond the slice.
+  __device__ __forceinline__ void load(uint4 (&raw)[kVecs], int first) const {
     const uint32_t none = BF16 ? 0xFF80FF80u : 0xFF800000u;
     const int v = first + int(threadIdx.x);
     const uint4* from = reinterpret_cast<const uint4*>(x + span.head * ES) + v;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       raw[j] = make_uint4(none, none, none, none);
-      if (v + j * THREADS < v1) raw[j] = keep ? from[j * THREADS] : __ldcs(from + j * THREADS);
+      if (v + j * THREADS < v1) raw[j] = __ldcs(from + j * THREADS);
     }
   }
 };
@@ -332,7 +331,7 @@ __device__ __forceinline__ Lse row_lse(const Slice<BF16, THREADS>& slice, uint4 
   } else {
 #pragma unroll 1
     for (int first = slice.v0; first < slice.v1; first += slice.kChunk) {
-      slice.load(raw, first, true);
+      slice.load(raw, first);
       z = lse_join(z, thread_lse<BF16>(raw, k));
     }
   }
@@ -355,7 +354,7 @@ __device__ __forceinline__ void write_gradient(const Slice<BF16, THREADS>& slice
   const int own = int(label) - slice.span.head;  // the label's place among the vectors' elements
 #pragma unroll 1
   for (int first = slice.v0; first < slice.v1; first += slice.kChunk) {
-    if (!slice.held()) slice.load(raw, first, false);
+    if (!slice.held()) slice.load(raw, first);
     const int v = first + int(threadIdx.x);
     char* to = d + (slice.span.head + int64_t(v) * W) * slice.ES;
 #pragma unroll
@@ -616,8 +615,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) rows_kernel(LossParam
   grid_dependency_wait();
   grid_dependents_launch();
   const int ranks = p.cluster, rank = int(blockIdx.x) % ranks;
-  // the gradient of a pair's rows starts with the rows that were read last
-  const int64_t at = blockIdx.x / ranks, t = MODE == kPrefBackward ? p.rows - 1 - at : at;
+  const int64_t t = blockIdx.x / ranks;
   const char* x = static_cast<const char*>(p.x) + t * p.ld * ES;
   char* d = p.d == nullptr ? nullptr : static_cast<char*>(p.d) + t * p.dld * ES;
   if (MODE == kPrefForward && blockIdx.x == 0 && threadIdx.x == 0) p.tickets[0] = 0;
@@ -636,8 +634,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) rows_kernel(LossParam
   }
   const Slice<BF16, THREADS> slice(x, int(p.vocab), rank, ranks);
   uint4 raw[kVecs];
-  const bool keep = MODE == kPrefForward && (p.rows - t) * p.vocab * ES < p.keep_bytes;
-  slice.load(raw, slice.v0, keep);
+  slice.load(raw, slice.v0);
   const float edge = slice.edge >= 0 ? load_one<BF16>(x, slice.edge) : -INFINITY;
   if (MODE == kPrefBackward) {
     const float2 z = p.row_lse[t];  // the sign of 1 / sum tells the scale
@@ -729,17 +726,15 @@ struct StreamShared {
   int abort_flag;
 };
 
-// A copy that is not kept in the L2 (`once`) or is.
-__device__ __forceinline__ void stream_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, bool once,
+// A copy of what is not read again soon. (Keeping the last 40 to 110 MB of the
+// logits in the L2 between a pair's two passes changed nothing: 227 to 229 us.)
+__device__ __forceinline__ void stream_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar,
                                             uint64_t evict_first) {
-  if (once)
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
-            smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(evict_first)
-        : "memory");
-  else
-    bulk_load(dst, src, bytes, bar);
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(evict_first)
+      : "memory");
 }
 
 // Adds a vector to a running sum, raising its shift where needed.
@@ -837,8 +832,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
       uint64_t evict_first;
       asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(evict_first));
       int chunk = 0;
-      auto row_at = [&](int64_t i) { return MODE == kPrefBackward ? p.rows - 1 - i : i; };
-      int64_t ahead = worker < p.rows ? p.labels[row_at(worker)] : -1;
+      int64_t ahead = worker < p.rows ? p.labels[worker] : -1;
       // Tells the others of the n-th row. Row n + 1 is told of before row n is
       // copied: the finisher looks it up before it finishes row n, and a row
       // may be longer than the ring.
@@ -846,13 +840,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
         const int64_t i = worker + n * workers;
         r = {-1, ahead, 0, 0, 0};
         if (i < p.rows) {
-          r.t = row_at(i);
+          r.t = i;
           // a masked row's gradient is written at its own alignment
           const char* at = ahead < 0 && WRITE && p.d != nullptr ? static_cast<const char*>(p.d) + r.t * p.dld * ES : row_of(r.t);
           const Part part(at, int(p.vocab), rank, ranks);
           r.head = part.span.head, r.v0 = part.v0, r.v1 = part.v1;
         }
-        if (i + workers < p.rows) ahead = p.labels[row_at(i + workers)];
+        if (i + workers < p.rows) ahead = p.labels[i + workers];
         if (n >= kStreamRows && !wait(sh.row_free, n - kStreamRows, kStreamRows)) return false;
         sh.row[n % kStreamRows] = r;
         mbar_arrive(&sh.row_full[n % kStreamRows]);
@@ -864,13 +858,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
         more = announce(n + 1, after);
         if (r.label < 0) continue;
         const char* from = row_of(r.t) + r.head * ES;
-        const bool once = !(MODE == kPrefForward && (p.rows - r.t) * p.vocab * ES < p.keep_bytes);
         for (int v = r.v0; v < r.v1; v += kVecsChunk, ++chunk) {
           if (chunk >= kStreamChunks && !wait(sh.empty, chunk - kStreamChunks, kStreamChunks)) break;
           const uint32_t bytes = uint32_t(min(r.v1 - v, kVecsChunk)) * 16;
           mbar_arrive_expect_tx(&sh.full[chunk % kStreamChunks], bytes);
           stream_load(chunks + chunk % kStreamChunks * kStreamChunk, from + int64_t(v) * 16, bytes,
-                      &sh.full[chunk % kStreamChunks], once, evict_first);
+                      &sh.full[chunk % kStreamChunks], evict_first);
         }
       }
       // copies in flight land before the shared memory goes away
@@ -1266,7 +1259,6 @@ constexpr int64_t kStreamRowBytes = 16384, kStreamRowsAnSm = 4;
 template <bool BF16, int MODE>
 cudaError_t launch_rows_typed(LossParams p, cudaStream_t stream) {
   const int64_t bytes = p.vocab * (BF16 ? 2 : 4), vecs = (bytes + 15) / 16, sms = device_sms();
-  p.keep_bytes = int64_t(80) << 20;
   p.cluster = 1;
   while (MODE == kPolicy && p.cluster < kMaxCluster && bytes > int64_t(kStreamSlice) * p.cluster) p.cluster *= 2;
   if (bytes >= kStreamRowBytes && (MODE != kPolicy || bytes <= int64_t(kStreamSlice) * p.cluster) && p.rows * p.cluster >= kStreamRowsAnSm * sms && !p.few) {

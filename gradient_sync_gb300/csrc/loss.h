@@ -45,7 +45,6 @@ struct LossParams {
   int few;                // a few rows: weights and pairs are worked out by the rows' kernels
   unsigned int* status_word;         // where waits that ran out are recorded
   unsigned int* const* status_host;
-  int64_t keep_bytes;     // logits that are worth keeping in the L2 between two passes
   float2* row_lse;        // [rows] preference: (base-2 shift, 1 / sum)
   float* row_terms;       // policy: [3 * rows] weighted loss terms;
                           // preference: [rows] log ratios, then [4 * pairs] terms

@@ -37,7 +37,6 @@ namespace {
 // threads and clusters of up to 8 CTAs a row that is up to 8 x 32768 bf16 or
 // 8 x 16384 fp32 long; longer ones are read twice.
 constexpr int kVecs = 8;
-constexpr double kExpLow = 4.9e-8;
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -131,13 +130,9 @@ __device__ __forceinline__ Two log_prob(float x, float k, Lse z) {
   const float xk = x * k;
   const Two a = two_sum(xk, -c), b = two_sum(a.hi, -float(e)), d = two_sum(b.hi, -log2f(f));
   const float lo = fmaf(x, k, -xk) + a.lo + b.lo + d.lo;
-  // The hardware's exponential is low by kExpLow of its value in the mean over
-  // its fraction (measured over [-20, 0]), hence the sum too, but for the
-  // label's own term where that dominates.
-  const float own = exp2_approx(fmaf(x, k, -c)) / z.s;
   constexpr float kLn2 = 0.69314718f, kLn2Low = float(0.69314718055994530942 - double(kLn2));
   const float r = d.hi * kLn2;
-  float low = fmaf(d.hi, kLn2, -r) + fmaf(d.hi, kLn2Low, lo * kLn2) - float(kExpLow) * (1.0f - own);
+  const float low = fmaf(d.hi, kLn2, -r) + fmaf(d.hi, kLn2Low, lo * kLn2);
   if (!isfinite(r) || low != low) return {r, 0.0f};  // -inf or NaN as it is
   return {r, low};
 }

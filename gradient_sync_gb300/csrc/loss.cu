@@ -1249,14 +1249,19 @@ cudaError_t active_clusters(const void* kernel, int cluster, size_t smem, int* w
 }
 
 // Calls with many long rows stream them; the others take a cluster a row.
-constexpr int64_t kStreamRowBytes = 16384, kStreamRowsAnSm = 4;
+// Measured, a cluster a row against streaming (log-probabilities / policy loss):
+// 6000 rows of 24 KB 42 / 75 and 51 / 85 us, of 32 KB 43 / 82 and 53 / 91, of
+// 40 KB (where a row needs 512 threads) 91 / 140 and 59 / 113, of 56 KB 95 / 152
+// and 65 / 127; rows of 64 KB, 300 of them 7.0 / 20.8 and 7.4 / 22.2, 600 of them
+// 11.1 / 24.4 and 9.9 / 26.0, 1200 of them 22.0 / 41.2 and 17.5 / 35.1.
+constexpr int64_t kStreamRowBytes = 32768, kStreamRowsAnSm = 4;
 
 template <bool BF16, int MODE>
 cudaError_t launch_rows_typed(LossParams p, cudaStream_t stream) {
   const int64_t bytes = p.vocab * (BF16 ? 2 : 4), vecs = (bytes + 15) / 16, sms = device_sms();
   p.cluster = 1;
   while (MODE == kPolicy && p.cluster < kMaxCluster && bytes > int64_t(kStreamSlice) * p.cluster) p.cluster *= 2;
-  if (bytes >= kStreamRowBytes && (MODE != kPolicy || bytes <= int64_t(kStreamSlice) * p.cluster) && p.rows * p.cluster >= kStreamRowsAnSm * sms && !p.few) {
+  if (bytes > kStreamRowBytes && (MODE != kPolicy || bytes <= int64_t(kStreamSlice) * p.cluster) && p.rows * p.cluster >= kStreamRowsAnSm * sms && !p.few) {
     void (*kernel)(LossParams) = stream_kernel<BF16, MODE>;
     constexpr size_t kSmem = size_t(kStreamChunks) * kStreamChunk + 128;
     cudaError_t err = status_ref(&p.status_word, &p.status_host);

@@ -13,8 +13,13 @@ namespace {
 using namespace ar;
 
 constexpr int64_t kMaxDim = 1 << 20;
-// Plans with at least this many 256 x 256 tiles of X run tiles of two CTAs.
-constexpr int64_t kPairTiles = 64;
+// Plans with at least this many 256 x 256 tiles of X run tiles of two CTAs,
+// which read less per product but pad row blocks to 256 and have fewer tiles.
+// Measured, one CTA against two: half precision 512 x 512 (4 tiles) 124 and
+// 153 us, 1536 x 1536 (36) 216 and 223, 1024 x 4096 (64) 266 and 254,
+// 2048 x 4096 (128) 422 and 380; split 256 x 256 (1) 143 and 137, 512 x 512
+// 187 and 173, 1024 x 1024 (16) 283 and 233, 2048 x 4096 1027 and 753.
+constexpr int64_t kPairTiles = 64, kPairTilesSplit = 2;
 constexpr float kDefault[3] = {3.4445f, -4.7750f, 2.0315f};
 
 size_t esize(ar_dtype d) { return d == AR_BF16 ? 2 : 4; }
@@ -136,13 +141,12 @@ ar_status ar_ortho_plan(const ar_ortho_desc* desc, ar_ortho_plan_t** out) try {
   p.out_dtype = desc->out_dtype;
   p.eps = desc->eps;
   p.split = desc->precision == AR_PRECISION_SPLIT || (desc->precision == AR_PRECISION_AUTO && desc->out_dtype == AR_F32);
-  // Tiles of two CTAs read less per product, but pad row blocks to 256.
   int64_t work = 0;
   for (int i = 0; i < n; ++i) {
     const int64_t r = desc->rows[i], c = desc->cols[i], mb = (std::min(r, c) + 127) / 128, nb = (std::max(r, c) + 127) / 128;
     work += (mb + 1) / 2 * ((nb + 1) / 2);
   }
-  p.cluster = work >= kPairTiles ? 2 : 1;
+  p.cluster = work >= (p.split ? kPairTilesSplit : kPairTiles) ? 2 : 1;
   int64_t at = 0, parts = 0, blocks = 0;
   for (int i = 0; i < n; ++i) {
     const int64_t r = desc->rows[i], c = desc->cols[i];

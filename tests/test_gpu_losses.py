@@ -264,7 +264,7 @@ def test_preference_in_place_and_forward_only(g):
 # Calls with many long rows, which are streamed: (rows, vocab, dtype); the policy loss in clusters of 1, 1, 4 and
 # 2 CTAs a row.
 STREAMED = [(650, 8200, torch.bfloat16), (700, 5001, torch.float32), (160, 50021, torch.float32),
-            (330, 40003, torch.bfloat16)]
+            (330, 40003, torch.bfloat16), (640, 16500, torch.bfloat16), (650, 8300, torch.float32)]
 
 
 @pytest.mark.parametrize("rows,vocab,dtype", STREAMED)

@@ -14,15 +14,16 @@ namespace {
 constexpr uint32_t kWaitPolls = 1u << 22;
 constexpr float kScaleA = 4096.0f;  // A and B are held times this
 constexpr int kUnit = 16384;        // one operand unit: 128 rows x 64 of k
-// Split products are summed over this many steps of 64 along k in the tensor
-// core and added up in registers, hi hi apart from the cross terms: the tensor
-// core's fp32 sums round towards zero, and every addition to the large sum
-// counts. Relative error of X against 64 bits and time, 1024 x 4096 and
-// 4096 x 4096: one sum 4.5e-5; 4 steps 6.6e-6, 2.9e-6, 398 us, 2.65 ms; 2 steps
-// 3.7e-6, 1.6e-6, 424 us, 2.81 ms; 1 step 2.2e-6, 1.1e-6, 497 us, 3.36 ms.
-// Elementary fp32 operations: 3.9e-6, 4.4e-6.
-constexpr int kSegment = 2;
-
+// Split products are summed over a few steps of 64 along k in the tensor core
+// and added up in registers, hi hi apart from the cross terms: the tensor core's
+// fp32 sums round towards zero, and every addition to the large sum counts.
+// Relative error of X against 64 bits and time, 1024 x 4096 and 4096 x 4096:
+// one sum 4.5e-5; every 4 steps 6.6e-6, 2.9e-6, 398 us, 2.65 ms; every 2 steps
+// 3.7e-6, 1.6e-6, 424 us, 2.81 ms; every step 2.2e-6, 1.1e-6, 497 us, 3.36 ms.
+// Elementary fp32 operations: 3.9e-6, 4.4e-6, growing with the length, so long
+// products are added up every 4 steps.
+constexpr int kLongSums = 64;
+__host__ __device__ constexpr int segment_steps(bool split, int ks) { return !split ? ks : ks < kLongSums ? 2 : 4; }
 
 // ---------------------------------------------------------------- tensor core
 
@@ -538,14 +539,27 @@ __device__ __forceinline__ bool tiles_complete(const unsigned int* done, unsigne
 // and one matrix's tiles fill the others' waits. Of a CTA, one warp takes tiles
 // up to two ahead, tells the others of each and, once what it needs is there,
 // that it can start; one copies operands; one issues products into one half of
-// TMEM; the others empty the other half.
+// TMEM; eight empty the other half.
+//
+// What bounds it, and what it measured (products counted with the symmetric
+// ones at one triangle; a 256 x 256 x 64 step of a pair takes 480 clocks, the
+// tensor core's rate, when its operands are there):
+//  one transformer layer, half precision (4 x 2048 x 2048, 3 x 2048 x 8192):
+//  1.8 ms, 1.3 PFLOP/s, 0.69 of the bf16 matrix rate. A tile of the last
+//  product of a step takes 20 thousand clocks instead of 16: with its old and
+//  new values a CTA moves 78 bytes a clock, and an SM gets about 70 from the
+//  L2; 2.5 thousand pass between tiles.
+//  two 4096 x 4096: 1.57 PFLOP/s (0.82). 12288 x 4096, split: 7.2 ms, three
+//  times the products at 1.43 PFLOP/s (0.75); operands (62 bytes a clock and
+//  SM) and the last, partly filled round of each product's tiles.
+//  256 x 256: 95 us: 15 products that wait for one another, 12 thousand clocks
+//  each: a copy's latency, the epilogue, and the way of a count through the L2.
 template <bool SPLIT, int CLUSTER>
 __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
     steps_kernel(const __grid_constant__ OrthoTable p) {
   using S = Shape<SPLIT, CLUSTER>;
   constexpr bool PAIR = S::PAIR;
   constexpr int HALVES = S::HALVES, EPI = S::EPI, STAGES = S::STAGES, RING = 3;
-  constexpr int SEGMENT = SPLIT ? kSegment : 1 << 30;
   extern __shared__ char smem_raw[];
   __shared__ uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], done, old_full[EPI];
   __shared__ uint64_t item_full[RING], item_free[RING], item_ready[RING], mail_full[RING], mail_free[RING], mail_ready[RING];
@@ -750,13 +764,14 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
       taken(n);
       const int a_from = left_mn_from<S>(t), b_from = right_mn_from<S>(t);
       const uint32_t idesc = instr_desc(S::CTAS * 128, t.nu * 128);
-      for (int k0 = 0; k0 < t.ks; k0 += SEGMENT, ++part) {
+      const int segment = segment_steps(SPLIT, t.ks);
+      for (int k0 = 0; k0 < t.ks; k0 += segment, ++part) {
         const int acc = part & 1;
         if (part >= 2 && __any_sync(~0u, !mbar_wait(&acc_empty[acc], (part / 2 + 1) & 1, kWaitPolls, abort, p.status)))
           break;
         fence_after();
         const uint32_t d = tmem + acc * 256;
-        const int k1 = min(t.ks, k0 + SEGMENT);
+        const int k1 = min(t.ks, k0 + segment);
         for (int k = k0; k < k1; ++k) {
           if (__any_sync(~0u, !mbar_wait(&full[s], phase, kWaitPolls, abort, p.status))) break;
           fence_after();
@@ -845,7 +860,8 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
       load_old(t, block0);
       float sum[SPLIT ? 64 : 1];
       uint32_t at = 0;  // this warp's accumulator
-      for (int k0 = 0; k0 < t.ks; k0 += SEGMENT, ++part) {
+      const int segment = segment_steps(SPLIT, t.ks);
+      for (int k0 = 0; k0 < t.ks; k0 += segment, ++part) {
         const int acc = part & 1;
         if (owed >= 0 && !mbar_test(&acc_full[acc], (part / 2) & 1)) report(false);
         __syncwarp();

@@ -841,7 +841,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
       uint64_t evict_first;
       asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(evict_first));
       int chunk = 0;
-      int64_t ahead = worker < p.rows ? p.labels[worker] : -1;
+      // A preference loss's second pass goes backwards, from the rows that the
+      // first one read last: 8192 x 32000 bf16 230.6 us a call and 233.4
+      // forwards, 3500 x 131072 365 and 368.
+      auto row_at = [&](int64_t i) { return MODE == kPrefBackward ? p.rows - 1 - i : i; };
+      int64_t ahead = worker < p.rows ? p.labels[row_at(worker)] : -1;
       // Tells the others of the n-th row. Row n + 1 is told of before row n is
       // copied: the finisher looks it up before it finishes row n, and a row
       // may be longer than the ring.
@@ -849,13 +853,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
         const int64_t i = worker + n * workers;
         r = {-1, ahead, 0, 0, 0};
         if (i < p.rows) {
-          r.t = i;
+          r.t = row_at(i);
           // a masked row's gradient is written at its own alignment
           const char* at = ahead < 0 && WRITE && p.d != nullptr ? static_cast<const char*>(p.d) + r.t * p.dld * ES : row_of(r.t);
           const Part part(at, int(p.vocab), rank, ranks);
           r.head = part.span.head, r.v0 = part.v0, r.v1 = part.v1;
         }
-        if (i + workers < p.rows) ahead = p.labels[i + workers];
+        if (i + workers < p.rows) ahead = p.labels[row_at(i + workers)];
         if (n >= kStreamRows && !wait(sh.row_free, n - kStreamRows, kStreamRows)) return false;
         sh.row[n % kStreamRows] = r;
         mbar_arrive(&sh.row_full[n % kStreamRows]);

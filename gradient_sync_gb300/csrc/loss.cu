@@ -25,14 +25,14 @@
 // first; each gradient row is written once), by launches and latency where
 // there are few. One GB300, copy bandwidth 6771 GB/s:
 //  stream_kernel  many long rows. 16384 x 32000 bf16, a quarter masked, policy
-//                 loss: 296 us in the kernel for 1.78 GB, 0.89 of the copy
-//                 bandwidth (two exponentials an element keep the special
-//                 function unit half busy); 3001 x 32003 fp32: 113 us a call;
+//                 loss: 304 us in the kernel for 1.78 GB, 0.86 of the copy
+//                 bandwidth (two exponentials an element: special function
+//                 unit 31 % busy, issue slots 55 %); 3001 x 32003 fp32: 113 us a call;
 //                 log-probabilities of 6007 x 50021 bf16: 77 us, 0.87.
 //  rows_kernel    a cluster of CTAs a row, the row in registers: 16 x 32000
-//                 fp32 log-probabilities 4.3 us on the device
+//                 fp32 log-probabilities 3.9 us in a graph of calls
 //  count_kernel, stats_kernel, pair_kernel  sequences; not needed where a call
-//                 has a few rows (64-token policy loss 12 us on the device)
+//                 has a few rows (64-token policy loss 11 us in a graph of calls)
 #include "loss.h"
 
 #include <algorithm>

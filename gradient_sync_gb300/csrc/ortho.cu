@@ -22,7 +22,8 @@
 //
 // Layout. Every operand is stored as blocks of 128 rows x 64 columns (16 KB),
 // in the 128-byte-swizzled order that the tensor core reads from shared
-// memory, so a tile is one contiguous bulk copy and no tensor map is needed.
+// memory, so a tile is one contiguous bulk copy. (Pairs of CTAs copy through a
+// tensor map over the same bytes, so that both CTAs' copies count on one barrier.)
 // The same bytes serve both ways round: 128 rows of 64 along k (k-major), or
 // 64 of the 128 rows as k of 128 columns (two blocks side by side, mn-major).
 // X is therefore stored once for X X^T and for B X, and of the symmetric A and
@@ -32,8 +33,8 @@
 //
 // Kernels (three launches for all matrices of a call):
 //  squares_kernel  momentum update, partial sums of squares of the update. HBM:
-//                  116 us for one transformer layer's 67 M elements (fp32
-//                  gradients and momentum: 806 MB, 1.03 of the copy bandwidth)
+//                  114 us for one transformer layer's 67 M elements (fp32
+//                  gradients and momentum: 806 MB, 1.04 of the copy bandwidth)
 //  pack_kernel     X in blocks, scaled, transposed where tall. HBM: 124 us for
 //                  the same (805 MB, 0.96)
 //  steps_kernel    every product of every step (ortho_steps.cuh)

@@ -645,11 +645,11 @@ ar_status ar_preference_loss(const ar_logits* logits, const float* ref_logp, con
  * optimiser). A tall matrix is handled as its transpose (X^T X on the other
  * side), so the products have min(rows, cols) rows.
  *
- * All matrices of a plan run together, in 2 + 3 * steps kernels.
+ * All matrices of a plan run together, in three kernels for each 64 of them.
  *
  * Precision. The products are tensor-core products of fp16 operands with
  * fp32 sums: AR_PRECISION_HALF rounds each operand to fp16 (X itself is kept
- * to 22 bits); AR_PRECISION_SPLIT keeps operands as two fp16 numbers and
+ * to 22 bits, but for the inputs of the last two steps); AR_PRECISION_SPLIT keeps operands as two fp16 numbers and
  * multiplies three of the four combinations, about 22 bits throughout, at
  * about 3 times the work. AR_PRECISION_AUTO is SPLIT for AR_F32 results and
  * HALF for AR_BF16 results (whose own rounding is larger than HALF's error).

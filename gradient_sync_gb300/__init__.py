@@ -364,7 +364,9 @@ def _row_major(t, what: str) -> int:
     if t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{what}: a 2-D CUDA tensor with contiguous rows wanted, got shape {tuple(t.shape)}, "
                          f"strides {t.stride()} on {t.device}")
-    return max(t.stride(0), t.shape[1])
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:  # an expanded tensor, or rows inside one another
+        raise ValueError(f"{what}: rows that share no memory wanted, got shape {tuple(t.shape)}, strides {t.stride()}")
+    return max(t.stride(0), t.shape[1])  # (the stride of a single row means nothing)
 
 
 def _logits(logits, labels, temperature):

@@ -1,0 +1,69 @@
+"""What the binding of the losses and of the optimiser takes from tensors, without a GPU: host
+tensors stand in for device ones, and the library's calls are recorded in place of being made."""
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def g():
+    from gradient_sync_gb300 import build
+
+    build.build()
+    import gradient_sync_gb300 as g
+
+    return g
+
+
+class Device:
+    """A host tensor that calls itself a device tensor."""
+
+    def __init__(self, t):
+        self.t = t
+
+    is_cuda = True
+    device = torch.device("cpu")  # where tensors made beside it go
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def overlapping(which):
+    """2 x 8 tensors whose rows share memory: one row twice, rows one apart, rows that share one element."""
+    flat = torch.zeros(16)
+    return flat[:8].expand(2, 8) if which == 0 else flat.as_strided((2, 8), (1 if which == 1 else 7, 1))
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_rows_that_share_memory_are_refused(g, which):
+    """A row stride below the width is no row stride that a kernel could use, on inputs and outputs alike."""
+    x = Device(overlapping(which))
+    good = Device(torch.zeros(2, 8))
+    labels = Device(torch.zeros(2, dtype=torch.int64))
+    row, start = Device(torch.zeros(2)), Device(torch.tensor([0, 1, 2]))
+    with pytest.raises(ValueError, match="logits"):
+        g.ar_token_logp(x, labels)
+    with pytest.raises(ValueError, match="dlogits"):
+        g.ar_policy_loss(good, labels, row, row, dlogits=x)
+    with pytest.raises(ValueError, match="dlogits"):
+        g.ar_preference_loss(good, labels, row, start, dlogits=x)
+    plan = g.ar_ortho_plan([(2, 8)])
+    with pytest.raises(ValueError, match="matrices"):
+        g.ar_orthogonalize(plan, [x], outs=[good])
+    with pytest.raises(ValueError, match="outs"):
+        g.ar_orthogonalize(plan, [good], outs=[x])
+    for bad in ("params", "grads", "momenta", "params_out", "momenta_out"):
+        with pytest.raises(ValueError, match=bad):
+            g.ar_muon_step(plan, **{**{k: [good] for k in ("params", "grads", "momenta")}, bad: [x]}, lr=0.1)
+
+
+def test_strides_that_no_row_uses(g):
+    """Of a single row, or none, the stride may be anything; rows of one element may be adjacent or
+    apart."""
+    flat = torch.zeros(64)
+    for t, ld in ((flat.as_strided((1, 8), (0, 1)), 8), (flat.as_strided((1, 8), (3, 1)), 8),
+                  (flat.as_strided((0, 8), (0, 1)), 8), (flat.as_strided((4, 1), (1, 7)), 1),
+                  (flat.as_strided((4, 1), (9, 0)), 9), (flat.as_strided((4, 8), (11, 1)), 11)):
+        assert g._row_major(Device(t), "x") == ld
+    with pytest.raises(ValueError):
+        g._row_major(Device(flat[:1].expand(4, 1)), "x")

@@ -415,8 +415,11 @@ def _room(workspace, need: int, like):
         import torch
 
         workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-    elif workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace: {need} bytes wanted")
+    elif (not workspace.is_cuda or not workspace.is_contiguous()
+          or workspace.numel() * workspace.element_size() < need):
+        raise ValueError(f"workspace: a contiguous CUDA tensor of at least {need} bytes wanted, got "
+                         f"{workspace.numel() * workspace.element_size()} bytes on {workspace.device}, strides "
+                         f"{workspace.stride()}")
     return workspace, workspace.data_ptr()
 
 

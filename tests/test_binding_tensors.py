@@ -67,3 +67,19 @@ def test_strides_that_no_row_uses(g):
         assert g._row_major(Device(t), "x") == ld
     with pytest.raises(ValueError):
         g._row_major(Device(flat[:1].expand(4, 1)), "x")
+
+
+def test_workspaces_that_the_kernels_could_not_use(g):
+    """A workspace in host memory, one with gaps (whose size is not its extent), and one that is too small."""
+    x, labels, row = (Device(t) for t in (torch.zeros(2, 8), torch.zeros(2, dtype=torch.int64), torch.zeros(2)))
+    start = Device(torch.tensor([0, 1, 2]))
+    plan = g.ar_ortho_plan([(2, 8)])
+    calls = [(g.ar_loss_workspace(2, 1), lambda w: g.ar_policy_loss(x, labels, row, row, workspace=w)),
+             (g.ar_loss_workspace(2, 2), lambda w: g.ar_preference_loss(x, labels, row, start, workspace=w)),
+             (g.ar_ortho_workspace(plan), lambda w: g.ar_orthogonalize(plan, [x], outs=[x], workspace=w)),
+             (g.ar_ortho_workspace(plan), lambda w: g.ar_muon_step(plan, [x], [x], [x], lr=0.1, workspace=w))]
+    for need, call in calls:
+        for bad in (torch.zeros(need, dtype=torch.uint8), Device(torch.zeros(need, dtype=torch.uint8).expand(4, need)),
+                    Device(torch.zeros(2 * need, dtype=torch.uint8)[::2]), Device(torch.zeros(need - 1, dtype=torch.uint8))):
+            with pytest.raises(ValueError, match="workspace"):
+                call(bad)

@@ -74,12 +74,13 @@ def test_workspaces_that_the_kernels_could_not_use(g):
     x, labels, row = (Device(t) for t in (torch.zeros(2, 8), torch.zeros(2, dtype=torch.int64), torch.zeros(2)))
     start = Device(torch.tensor([0, 1, 2]))
     plan = g.ar_ortho_plan([(2, 8)])
-    calls = [(g.ar_loss_workspace(2, 1), lambda w: g.ar_policy_loss(x, labels, row, row, workspace=w)),
-             (g.ar_loss_workspace(2, 2), lambda w: g.ar_preference_loss(x, labels, row, start, workspace=w)),
+    forward = dict(grad=False)
+    calls = [(g.ar_loss_workspace(2, 1), lambda w: g.ar_policy_loss(x, labels, row, row, workspace=w, **forward)),
+             (g.ar_loss_workspace(2, 2), lambda w: g.ar_preference_loss(x, labels, row, start, workspace=w, **forward)),
              (g.ar_ortho_workspace(plan), lambda w: g.ar_orthogonalize(plan, [x], outs=[x], workspace=w)),
              (g.ar_ortho_workspace(plan), lambda w: g.ar_muon_step(plan, [x], [x], [x], lr=0.1, workspace=w))]
     for need, call in calls:
-        for bad in (torch.zeros(need, dtype=torch.uint8), Device(torch.zeros(need, dtype=torch.uint8).expand(4, need)),
-                    Device(torch.zeros(2 * need, dtype=torch.uint8)[::2]), Device(torch.zeros(need - 1, dtype=torch.uint8))):
+        room = torch.zeros(2 * need, dtype=torch.uint8)
+        for bad in (room, Device(room[:need].expand(4, need)), Device(room[::2]), Device(room[:need - 1])):
             with pytest.raises(ValueError, match="workspace"):
                 call(bad)

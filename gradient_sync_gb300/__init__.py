@@ -330,6 +330,9 @@ def ar_compressed_allreduce(grads, block: int, dtype="f32", residuals=None, scal
 
 
 # ---------------------------------------------------------------- losses
+# Calls run on `stream` (default: the current one). Outputs and workspaces that
+# are not given are made for that stream; on another one the caller orders the
+# streams before it reads the outputs, as for any call.
 
 
 _KINDS: dict = {}  # torch type -> the library's, once torch is needed
@@ -378,25 +381,43 @@ def _logits(logits, labels, temperature):
                          _vector(labels, torch.int64, rows, "labels"), temperature)
 
 
-def _gradient(logits, dlogits, grad: bool):
+def _empty(shape, dtype, like, stream, read: bool = True):
+    """A new tensor beside `like` for a call on `stream`: memory of that stream, so that the allocator
+    neither hands it out again nor has it in use elsewhere while the call runs. What the caller reads on
+    the current stream is known to that one too."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    handle = _stream(stream)
+    if handle == 1:  # another name of the default stream
+        handle = 0
+    if handle == _stream(None):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=like.device)):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    if read:
+        t.record_stream(torch.cuda.current_stream(like.device))
+    return t
+
+
+def _gradient(logits, dlogits, grad: bool, stream):
     """(tensor or None, address, row stride) of the gradient of the logits."""
     if dlogits is None:
         if not grad:
             return None, 0, 0
-        import torch
-
-        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        dlogits = _empty(logits.shape, logits.dtype, logits, stream)
     elif dlogits.dtype is not logits.dtype or dlogits.shape != logits.shape:
         raise ValueError("dlogits: the logits' type and shape wanted")
     return dlogits, dlogits.data_ptr(), _row_major(dlogits, "dlogits")
 
 
-def _output(t, n: int, like, what: str):
+def _output(t, n: int, like, what: str, stream):
     """An fp32 vector to write to, and its address."""
     import torch
 
     if t is None:
-        t = torch.empty(n, dtype=torch.float32, device=like.device)
+        t = _empty(n, torch.float32, like, stream)
         return t, t.data_ptr()
     return t, _vector(t, torch.float32, n, what)
 
@@ -409,12 +430,12 @@ def ar_loss_workspace(rows: int, n_seq: int) -> int:
     return b.value
 
 
-def _room(workspace, need: int, like):
+def _room(workspace, need: int, like, stream):
     """A workspace of at least `need` bytes, and its address."""
     if workspace is None:
         import torch
 
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        workspace = _empty(need, torch.uint8, like, stream, read=False)
     elif (not workspace.is_cuda or not workspace.is_contiguous()
           or workspace.numel() * workspace.element_size() < need):
         raise ValueError(f"workspace: a contiguous CUDA tensor of at least {need} bytes wanted, got "
@@ -427,7 +448,7 @@ def ar_token_logp(logits, labels, temperature: float = 1.0, logp=None, stream=No
     """Log-probabilities of the labelled tokens, [rows] fp32 (0 where the label
     is negative). `logits` [rows, vocab] fp32 or bf16, any row stride; `labels` int64."""
     d = _logits(logits, labels, temperature)
-    logp, out = _output(logp, d.rows, logits, "logp")
+    logp, out = _output(logp, d.rows, logits, "logp", stream)
     _check(_lib.load().ar_token_logp(d, out, _stream(stream)), "ar_token_logp")
     return logp
 
@@ -452,10 +473,10 @@ def ar_policy_loss(logits, labels, old_logp, advantages, seq_start=None, ref_log
     if seq_start is not None:
         n_seq = seq_start.shape[0] - 1 if seq_start.dim() else 0
         start = _vector(seq_start, torch.int64, n_seq + 1, "seq_start")
-    dlogits, d_at, dld = _gradient(logits, dlogits, grad)
-    stats, stats_at = _output(stats, 4, logits, "stats")
-    logp, logp_at = _output(logp, rows, logits, "logp")
-    workspace, room = _room(workspace, ar_loss_workspace(rows, max(n_seq, 0)), logits)
+    dlogits, d_at, dld = _gradient(logits, dlogits, grad, stream)
+    stats, stats_at = _output(stats, 4, logits, "stats", stream)
+    logp, logp_at = _output(logp, rows, logits, "logp", stream)
+    workspace, room = _room(workspace, ar_loss_workspace(rows, max(n_seq, 0)), logits, stream)
     desc = _lib.ArPolicyDesc(clip_low, clip_high, kl_coef, LOSS_MEANS.get(reduction, reduction), denominator, grad_scale)
     _check(_lib.load().ar_policy_loss(d, old, ref, adv, start, n_seq, desc, stats_at, logp_at, d_at, dld, room,
                                       _stream(stream)), "ar_policy_loss")
@@ -479,11 +500,11 @@ def ar_preference_loss(logits, labels, ref_logp, seq_start, beta: float = 0.1, l
     rows, n_seq = d.rows, seq_start.shape[0] - 1 if seq_start.dim() else 0
     ref = _vector(ref_logp, torch.float32, rows, "ref_logp")
     start = _vector(seq_start, torch.int64, n_seq + 1, "seq_start")
-    dlogits, d_at, dld = _gradient(logits, dlogits, grad)
-    stats, stats_at = _output(stats, 4, logits, "stats")
-    ratios, ratios_at = _output(ratios, max(n_seq, 0), logits, "ratios")
-    logp, logp_at = _output(logp, rows, logits, "logp")
-    workspace, room = _room(workspace, ar_loss_workspace(rows, max(n_seq, 0)), logits)
+    dlogits, d_at, dld = _gradient(logits, dlogits, grad, stream)
+    stats, stats_at = _output(stats, 4, logits, "stats", stream)
+    ratios, ratios_at = _output(ratios, max(n_seq, 0), logits, "ratios", stream)
+    logp, logp_at = _output(logp, rows, logits, "logp", stream)
+    workspace, room = _room(workspace, ar_loss_workspace(rows, max(n_seq, 0)), logits, stream)
     desc = _lib.ArPreferenceDesc(beta, PREFERENCE_FORMS.get(loss, loss), label_smoothing, target,
                                  1 if length_normalized else 0, denominator, grad_scale)
     _check(_lib.load().ar_preference_loss(d, ref, start, n_seq, desc, stats_at, ratios_at, logp_at, d_at, dld, room,
@@ -564,9 +585,9 @@ def ar_orthogonalize(plan: OrthoPlan, matrices, outs=None, workspace=None, strea
         import torch
 
         kind = torch.bfloat16 if plan.out_dtype == AR_BF16 else torch.float32
-        outs = [torch.empty(m.shape, dtype=kind, device=m.device) for m in matrices]
+        outs = [_empty(m.shape, kind, m, stream) for m in matrices]
     a, b = _matrices(plan, matrices, plan.in_dtype, "matrices"), _matrices(plan, outs, plan.out_dtype, "outs")
-    workspace, room = _room(workspace, ar_ortho_workspace(plan), matrices[0])
+    workspace, room = _room(workspace, ar_ortho_workspace(plan), matrices[0], stream)
     _check(_lib.load().ar_orthogonalize(plan.handle, a, b, room, _stream(stream)), "ar_orthogonalize")
     return outs
 
@@ -580,7 +601,7 @@ def ar_muon_step(plan: OrthoPlan, params, grads, momenta, lr: float, momentum: f
     p, g = _matrices(plan, params, plan.out_dtype, "params"), _matrices(plan, grads, plan.in_dtype, "grads")
     m = _matrices(plan, momenta, AR_F32, "momenta")
     po, mo = _matrices(plan, params_out, plan.out_dtype, "params_out"), _matrices(plan, momenta_out, AR_F32, "momenta_out")
-    workspace, room = _room(workspace, ar_ortho_workspace(plan), params[0])
+    workspace, room = _room(workspace, ar_ortho_workspace(plan), params[0], stream)
     d = _lib.ArMuonDesc(float(lr), float(momentum), float(weight_decay), int(bool(nesterov)),
                         ADJUSTS.get(adjust, adjust), float(grad_scale))
     _check(_lib.load().ar_muon_step(plan.handle, d, p, g, m, po, mo, room, _stream(stream)), "ar_muon_step")

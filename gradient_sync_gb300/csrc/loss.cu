@@ -257,8 +257,11 @@ __device__ __forceinline__ Lse thread_lse(const uint4 (&raw)[kVecs], float k) {
   return {c, s[0] + s[1]};
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 __device__ __forceinline__ void store_peer(void* p, int rank, float2 v) {
   const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -314,7 +317,9 @@ struct RowShared {
 };
 
 // The row's sum, from every thread's; the same bits in every thread of the
-// cluster. May be called again after a barrier.
+// cluster. Every thread has arrived at the cluster's barrier before: only when
+// all have (the peers run, and are done with an earlier sum) is a peer's shared
+// memory written to.
 template <int THREADS>
 __device__ __forceinline__ Lse row_sum(Lse v, RowShared& sh, int rank, int ranks) {
   constexpr int W = THREADS / 32;
@@ -323,6 +328,7 @@ __device__ __forceinline__ Lse row_sum(Lse v, RowShared& sh, int rank, int ranks
   __syncthreads();
   v = lse_warp(sh.warp[threadIdx.x % W], W);
   if (ranks > 1) {
+    cluster_wait();
     if (threadIdx.x < ranks) store_peer(&sh.cta[rank], threadIdx.x, make_float2(v.c, v.s));
     cluster_barrier();
     v = {sh.cta[0].x, sh.cta[0].y};
@@ -641,6 +647,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) rows_kernel(LossParam
     }
     return;
   }
+  // (all CTAs of a cluster have the same row: they return above together, or come here)
+  if (MODE != kPrefBackward && ranks > 1) cluster_arrive();  // waited for in row_sum, behind the loads
   const Slice<BF16, THREADS> slice(x, int(p.vocab), rank, ranks);
   uint4 raw[kVecs];
   slice.load(raw, slice.v0);
@@ -678,7 +686,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) rows_kernel(LossParam
   if (isinf(z.c)) {
     k = 1.0f;
     __syncthreads();
-    if (ranks > 1) cluster_barrier();
+    if (ranks > 1) cluster_arrive();
     z = row_lse<BF16, THREADS>(slice, raw, edge, k, sh, rank, ranks);
   }
   const Two exact = log_prob(x_label, k, z);

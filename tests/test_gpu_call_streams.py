@@ -28,6 +28,7 @@ def test_memory_of_a_call_is_not_handed_out_while_it_runs(g, raw):
     x = torch.randn(rows, vocab, generator=gen, device="cuda")
     labels = torch.randint(0, vocab, (rows,), generator=gen, device="cuda")
     lp = g.ar_token_logp(x, labels)
+    ref = lp + 0.1
     start = torch.tensor([0, 9, 20, 33, rows], device="cuda")
     m = torch.randn(shape, generator=gen, device="cuda")
     plan = g.ar_ortho_plan([shape])
@@ -37,7 +38,7 @@ def test_memory_of_a_call_is_not_handed_out_while_it_runs(g, raw):
         at = dict(params_out=[torch.empty_like(m)], momenta_out=[torch.empty_like(m)])
         outs = [g.ar_token_logp(x, labels, stream=stream),
                 g.ar_policy_loss(x, labels, lp, lp, start, stream=stream),
-                g.ar_preference_loss(x, labels, lp + 0.1, start, stream=stream),
+                g.ar_preference_loss(x, labels, ref, start, stream=stream),
                 g.ar_orthogonalize(plan, [m], stream=stream)]
         g.ar_muon_step(plan, [params], [m], [momenta], lr=0.1, stream=stream, **at)
         return flat(outs) + at["params_out"] + at["momenta_out"]
@@ -49,8 +50,8 @@ def test_memory_of_a_call_is_not_handed_out_while_it_runs(g, raw):
         with torch.cuda.stream(side):
             torch.cuda._sleep(10_000_000)  # some milliseconds
         got = calls(side.cuda_stream if raw else side)
-        sizes = {t.numel() * t.element_size() for t in want} | {g.ar_loss_workspace(rows, 1), g.ar_loss_workspace(rows, 4),
-                                                                g.ar_ortho_workspace(plan)}
+        sizes = {t.numel() * t.element_size() for t in want}
+        sizes |= {g.ar_loss_workspace(rows, 1), g.ar_loss_workspace(rows, 4), g.ar_ortho_workspace(plan)}
         junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(6)]
         torch.cuda.current_stream().wait_stream(side)
         assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -163,6 +163,11 @@ struct RowSpan {
     vecs = (n - head) / W;
     tail = n - head - vecs * W;
   }
+  // Which of `ranks` CTAs that share the row's vectors (see Slice) has element e; the first has what lies outside them.
+  __device__ __forceinline__ int owner(int64_t e, int ranks) const {
+    const int64_t at = e - head;
+    return at < 0 || at >= int64_t(vecs) * W ? 0 : int(at) / W / ((vecs + ranks - 1) / ranks);
+  }
   // The element outside the vectors that thread `i` takes (-1: none).
   __device__ __forceinline__ int edge(int i) const {
     if (i < head) return i;
@@ -275,16 +280,16 @@ __device__ __forceinline__ void store_peer(void* p, int rank, float2 v) {
       : "memory");
 }
 
-// The same counted (8 bytes) on a barrier of that CTA, which needs no fence between the CTAs.
-__device__ __forceinline__ void send_peer(void* p, uint64_t* bar, int rank, float2 v) {
+// The same counted (16 bytes) on a barrier of that CTA, which needs no fence between the CTAs.
+__device__ __forceinline__ void send_peer(void* p, uint64_t* bar, int rank, float4 v) {
   asm volatile(
       "{\n"
       ".reg .b32 to, count;\n"
       "mapa.shared::cluster.u32 to, %0, %2;\n"
       "mapa.shared::cluster.u32 count, %1, %2;\n"
-      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [to], {%3, %4}, [count];\n"
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [to], {%3, %4, %5, %6}, [count];\n"
       "}\n" ::"r"(smem_u32(p)),
-      "r"(smem_u32(bar)), "r"(rank), "f"(v.x), "f"(v.y)
+      "r"(smem_u32(bar)), "r"(rank), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
       : "memory");
 }
 
@@ -739,7 +744,7 @@ struct StreamShared {
   StreamRow row[kStreamRows];
   StreamResult result[kStreamRows];
   Lse warp_sum[kStreamRows][kStreamWarps];
-  float2 cta_sum[kStreamRows][kMaxCluster];
+  float4 cta_sum[kStreamRows][kMaxCluster];  // shift, sum, the label's logit where the CTA has it
   int abort_flag;
 };
 
@@ -1002,13 +1007,18 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
     float mean = 0.0f;
     if (MODE == kPolicy) mean = mean_scale(p);
     int exchanges = 0;
-    auto join_cluster = [&](Lse z, bool& ok) {
+    // The cluster's sum. The label's logit (x_label) goes with the owner's part of
+    // it: where the gradient is written over the logits, the CTA that overwrites
+    // that logit is the only one that reads it.
+    auto join_cluster = [&](Lse z, int owner, float& x_label, bool& ok) {
       if (ranks == 1) return z;
       const int slot = exchanges % kStreamRows;
-      if (lane == 0) mbar_arrive_expect_tx(&sh.cta_full[slot], 8 * ranks);
-      if (lane < ranks) send_peer(&sh.cta_sum[slot][rank], &sh.cta_full[slot], lane, make_float2(z.c, z.s));
+      if (lane == 0) mbar_arrive_expect_tx(&sh.cta_full[slot], 16 * ranks);
+      if (lane < ranks)
+        send_peer(&sh.cta_sum[slot][rank], &sh.cta_full[slot], lane, make_float4(z.c, z.s, x_label, 0.0f));
       ok = !__any_sync(~0u, !mbar_wait(&sh.cta_full[slot], (exchanges / kStreamRows) & 1, kWaitPolls, abort, status));
       ++exchanges;
+      x_label = sh.cta_sum[slot][owner].z;
       Lse all = {sh.cta_sum[slot][0].x, sh.cta_sum[slot][0].y};
       for (int r = 1; r < ranks; ++r) all = lse_join(all, {sh.cta_sum[slot][r].x, sh.cta_sum[slot][r].y});
       return all;
@@ -1017,7 +1027,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
     // What a row needs from memory is read while the row before it is finished.
     struct Known {
       StreamRow r;
-      int edge;
+      int edge, owner;
       float edge_value, x_label, weight, adv, old, ref;
       float2 lse;
     };
@@ -1025,6 +1035,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
       if (__any_sync(~0u, !wait(sh.row_full, n, kStreamRows))) return false;
       q.r = sh.row[n % kStreamRows];
       q.edge = -1;
+      q.owner = 0;
       q.edge_value = -INFINITY;
       q.x_label = nan;
       q.weight = q.adv = q.old = q.ref = 0.0f;
@@ -1032,14 +1043,16 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
       const int64_t t = q.r.t;
       if (t < 0 || q.r.label < 0) return true;
       const char* x = row_of(t);
-      if (rank == 0) q.edge = RowSpan<W, ES>(x, int(p.vocab)).edge(lane);
+      const RowSpan<W, ES> span(x, int(p.vocab));
+      if (rank == 0) q.edge = span.edge(lane);
       if (q.edge >= 0) q.edge_value = load_one<BF16>(x, q.edge);
       if (MODE == kPrefBackward) {
         q.lse = p.row_lse[t];
         q.weight = p.row_a[t];
         return true;
       }
-      if (q.r.label < p.vocab) q.x_label = load_one<BF16>(x, q.r.label);
+      q.owner = span.owner(q.r.label, ranks);
+      if (q.r.label < p.vocab && q.owner == rank) q.x_label = load_one<BF16>(x, q.r.label);
       if (MODE == kPolicy) {
         q.weight = p.row_a[t];
         q.adv = p.adv[t];
@@ -1078,7 +1091,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
             const float c = fmaxf(-INFINITY, ceilf(edge_value * k));
             return lse_join(v, {c, exp2_approx(fmaf(edge_value, k, -finite_shift(c)))});
           };
-          z = join_cluster(lse_warp(with_edge(z, q.k), 32), ok);
+          float x_label = now.x_label;
+          z = join_cluster(lse_warp(with_edge(z, q.k), 32), now.owner, x_label, ok);
           if (!ok) break;
           // Sums that left fp32's range, once more from memory; where x k itself
           // is not finite (see rows_kernel), at k = 1.
@@ -1088,11 +1102,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
             z = {-INFINITY, 0.0f};
             for (int v = r.v0 + lane; v < r.v1; v += 32)
               lse_add<BF16>(z, reinterpret_cast<const uint4*>(x + r.head * ES)[v], q.k);
-            z = join_cluster(lse_warp(with_edge(z, q.k), 32), ok);
+            z = join_cluster(lse_warp(with_edge(z, q.k), 32), now.owner, x_label, ok);
             if (!ok) break;
           }
           if (!ok) break;
-          const Two exact = log_prob(now.x_label, q.k, z);
+          const Two exact = log_prob(x_label, q.k, z);
           lp = exact.hi + exact.lo;
           q.shift = finite_shift(z.c);
           const float inv_sum = 1.0f / z.s;

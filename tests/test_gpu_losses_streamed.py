@@ -1,0 +1,91 @@
+"""The losses where they stream rows (more than 32 KB a row, more than 512 rows and at least four rows times CTAs for
+each SM), on a GB300, against their definition in 64 bits on the device."""
+
+import math
+
+import pytest
+import torch
+
+from _loss_checks import check_all, check_gradient, check_logp, log_probs
+
+pytestmark = pytest.mark.gpu
+
+# (rows, vocab, type): the policy loss in clusters of 1, 1, 2, 4 and 8 CTAs a row
+STREAMED = [(640, 16500, torch.bfloat16), (640, 8300, torch.float32), (640, 40003, torch.bfloat16),
+            (620, 100003, torch.bfloat16), (620, 100003, torch.float32)]
+
+
+@pytest.fixture(scope="module")
+def g():
+    from gradient_sync_gb300 import build
+
+    build.build()
+    import gradient_sync_gb300 as g
+
+    return g
+
+
+def normal(rows, vocab, dtype, shift=0, pad=0, seed=0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    x = (torch.randn(rows, shift + vocab + pad, generator=gen, device="cuda") * 3).to(dtype)[:, shift:shift + vocab]
+    labels = torch.randint(0, vocab, (rows,), generator=gen, device="cuda")
+    edges = torch.arange(0, rows, 9, device="cuda")  # first and last elements, outside the vectors or not
+    labels[edges] = torch.where(edges % 2 == 0, edges // 9 % 8, vocab - 1 - edges // 9 % 8)
+    labels[::4] = -100
+    return x, labels
+
+
+@pytest.mark.parametrize("shift,pad", [(0, 0), (3, 2)])
+@pytest.mark.parametrize("rows,vocab,dtype", STREAMED)
+def test_streamed_rows(g, rows, vocab, dtype, shift, pad):
+    x, labels = normal(rows, vocab, dtype, shift, pad, seed=vocab + shift)
+    check_all(g, x, labels, 0.9)
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", STREAMED)
+def test_gradient_over_the_logits(g, rows, vocab, dtype):
+    """In place and apart, the same bits, call after call."""
+    x, labels = normal(rows, vocab, dtype, seed=2)
+    start = torch.tensor([0, 99, 300, 301, rows], device="cuda")
+    lp = g.ar_token_logp(x, labels)
+    for loss, args in ((g.ar_policy_loss, (lp - 0.1, lp, start)), (g.ar_preference_loss, (lp + 0.1, start))):
+        want = loss(x, labels, *args)
+        for _ in range(4):
+            own = x.clone()
+            got = loss(own, labels, *args, dlogits=own)
+            assert got[-1].data_ptr() == own.data_ptr() and all(torch.equal(a, b) for a, b in zip(got, want))
+    assert g.ar_device_status() == g.AR_OK
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", STREAMED)
+def test_extreme_values(g, rows, vocab, dtype):
+    """Rows whose sums are taken again, in every CTA of a cluster, among others whose are not."""
+    low, top = torch.finfo(dtype).min, torch.finfo(dtype).max
+    x, labels = normal(rows, vocab, dtype, seed=3)
+    labels[:9] = 5
+    x[0] = low                           # uniform
+    x[1, 9:] = low                       # uniform over nine
+    x[1, :9] = 0.0
+    x[2] = -float("inf")                 # no distribution
+    x[3, vocab - 1] = float("nan")
+    x[4, 0] = float("inf")
+    labels[5] = vocab + 3
+    x[6] = top                           # uniform
+    x[7] = low
+    x[7, 5] = x[7, vocab - 7] = top      # uniform over two, far apart
+    x[8] = -300.0                        # below what a thread's shift takes in at first
+    x[8, 5] = -298.0
+    want = [-math.log(vocab), -math.log(9), *[math.nan] * 4, -math.log(vocab), -math.log(2),
+            2 - math.log(vocab - 1 + math.exp(2.0))]
+    lp = g.ar_token_logp(x, labels)
+    for i, v in enumerate(want):
+        assert math.isnan(lp[i]) if math.isnan(v) else abs(float(lp[i]) - v) < 4e-5, (i, lp[i], v)
+    check_logp(lp[9:], log_probs(x[9:], labels[9:], 1.0)[0])
+    start = torch.tensor([0, rows], device="cuda")
+    _, got, d = g.ar_policy_loss(x, labels, torch.nan_to_num(lp, 0.0), torch.ones(rows, device="cuda"), start)
+    check_logp(torch.nan_to_num(got), torch.nan_to_num(lp).double())
+    assert torch.isnan(d[2:6]).all() and torch.isfinite(d[6:]).all() and torch.isfinite(d[:2]).all()
+    even = torch.full((1, vocab), 1 / vocab, dtype=torch.float64, device="cuda")
+    up = torch.full((1,), -1.0 / int((labels >= 0).sum()), dtype=torch.float64, device="cuda")
+    for i in (0, 6):
+        check_gradient(d[i:i + 1], up, even, labels[i:i + 1], 1.0)

@@ -114,9 +114,20 @@ __device__ __forceinline__ float pow2(float d) {
 // integers, so that joining two pairs rounds only their sum; with shifts of any
 // value every level of the joins would bring in the exponential's error, whose
 // mean is not zero, and log-probabilities summed over a sequence would drift.
+// A join drops a part whose shift is 127 or more below the other's: sums have to
+// be of the order of their number of terms, or normalized.
 struct Lse {
   float c, s;
 };
+// The same value with its sum in [1/2, 1), or a shift of -inf for a sum of 0.
+// What has no such form (an infinite shift, a sum of infinity or NaN) is as it was.
+__device__ __forceinline__ Lse normalized(Lse v) {
+  if (!isfinite(v.s) || v.c == INFINITY) return v;
+  if (v.s == 0.0f) return {-INFINITY, 0.0f};
+  int e = 0;
+  const float f = frexpf(v.s, &e);
+  return {v.c + float(e), f};
+}
 __device__ __forceinline__ Lse lse_join(Lse a, Lse b) {
   const float c = fmaxf(a.c, b.c), z = finite_shift(c);
   return {c, a.s * pow2(a.c - z) + b.s * pow2(b.c - z)};
@@ -804,9 +815,12 @@ __device__ __forceinline__ void gradient_of(const uint4& raw, Pair k, Pair minus
 // A thread of the streaming kernel takes its shift from the first vectors of a
 // row that it sees, and no maximum after that: fp32 holds terms up to 2^127
 // times the shift's. kLeastShift keeps vectors that a mask has filled with low
-// values from setting it. Sums that left the range all the same (an overflow,
-// or nothing but tiny terms) are taken again by the finisher, with the maximum.
-constexpr float kLeastShift = -64.0f, kLeastSum = 1e-18f;
+// values from setting it. A thread's sum may so lie anywhere in fp32's range
+// and is normalized before it meets the others'. Sums that left the range all
+// the same are taken again by the finisher, with the maximum: an overflow, or
+// a row below 2^kLeastTotal, of which kLeastShift may have cost terms below
+// 2^(kLeastShift - 126).
+constexpr float kLeastShift = -64.0f, kLeastTotal = -124.0f;
 
 template <bool BF16, int MODE>
 __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p) {
@@ -940,7 +954,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
         }
         const float2 both = floats_of(sum);
         z.s = both.x + both.y;
-        z = lse_warp(z, 32);
+        z = lse_warp(normalized(z), 32);
       }
       if (lane == 0) {
         sh.warp_sum[n % kStreamRows][warp] = z;
@@ -1097,7 +1111,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
           // Sums that left fp32's range, once more from memory; where x k itself
           // is not finite (see rows_kernel), at k = 1.
           for (int again = 0; again < 2; ++again) {
-            if (again == 0 ? z.s < 3e38f && z.s > kLeastSum : !isinf(z.c)) break;
+            if (again == 0 ? z.s > 0.0f && isfinite(z.s) && z.c > kLeastTotal : !isinf(z.c)) break;
             if (again == 1) q.k = 1.0f;
             z = {-INFINITY, 0.0f};
             for (int v = r.v0 + lane; v < r.v1; v += 32)

@@ -89,3 +89,53 @@ def test_extreme_values(g, rows, vocab, dtype):
     up = torch.full((1,), -1.0 / int((labels >= 0).sum()), dtype=torch.float64, device="cuda")
     for i in (0, 6):
         check_gradient(d[i:i + 1], up, even, labels[i:i + 1], 1.0)
+
+
+# logit / temperature of the two entries that are left in a row; the first is among the first
+# vectors of its thread, the second is not, and its thread's first vectors hold the mask
+PAIRS = [(43.75, 43.75), (43.5, 44.0), (44.0, 46.0), (44.0, 50.0), (50.0, 44.0), (60.0, 61.0), (120.0, 119.0),
+         (-150.0, -151.0), (3.0, 2.0), (-30.0, 43.0)]
+
+
+@pytest.mark.parametrize("low", ["inf", "lowest", "far"])
+@pytest.mark.parametrize("tau", [1.0, 0.25])
+@pytest.mark.parametrize("rows,vocab,dtype", STREAMED)
+def test_masked_rows_of_large_logits(g, rows, vocab, dtype, tau, low):
+    """Nothing is lost where a mask hides a thread's first vectors and the logits that are left are large."""
+    fill = {"inf": -float("inf"), "lowest": torch.finfo(dtype).min, "far": -400.0 * tau}[low]
+    x = torch.full((rows, vocab), fill, dtype=dtype, device="cuda")
+    width = 1024 * (8 if dtype == torch.bfloat16 else 4)  # two vectors a thread
+    t = torch.arange(rows, device="cuda")
+    pairs = torch.tensor(PAIRS, device="cuda")[t % len(PAIRS)] * tau
+    first, late = 5 + t * 7 % (width - 50), width + 10 + t * 13 % (min(width, vocab - width) - 50)
+    x[t, first] = pairs[:, 0].to(dtype)
+    x[t, late] = pairs[:, 1].to(dtype)
+    labels = torch.where(t % 2 == 0, first, late)
+    labels[::9] = -100
+    check_all(g, x, labels, tau)
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", STREAMED)
+def test_masked_start_of_the_rows(g, rows, vocab, dtype):
+    """All of the first vectors but one entry ruled out, the rest ten nats below it."""
+    width = 1024 * (8 if dtype == torch.bfloat16 else 4)
+    x = torch.full((rows, vocab), 33.25, dtype=dtype, device="cuda")
+    x[:, :width] = -float("inf")
+    t = torch.arange(rows, device="cuda")
+    x[t, 3 + t] = 43.5
+    labels = torch.where(t % 2 == 0, 3 + t, width + 20 + t)
+    labels[::5] = -1
+    check_all(g, x, labels, 1.0)
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", STREAMED)
+def test_forced_tokens(g, rows, vocab, dtype):
+    """A token at the type's highest value has all of its row's probability, wherever in the row it is."""
+    x, labels = normal(rows, vocab, dtype, seed=6)
+    t = torch.arange(rows, device="cuda")
+    labels = t * 131 % vocab
+    x[t, labels] = torch.finfo(dtype).max
+    assert not g.ar_token_logp(x, labels).any()
+    old = torch.zeros(rows, device="cuda")
+    stats, lp, d = g.ar_policy_loss(x, labels, old, old + 1)
+    assert not lp.any() and not d.any() and abs(float(stats[0]) + 1) < 1e-6

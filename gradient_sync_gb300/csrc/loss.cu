@@ -672,6 +672,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) rows_kernel(LossParam
   if (MODE == kPrefBackward) {
     const float2 z = p.row_lse[t];  // the sign of 1 / sum tells the scale
     const float coef = p.few ? few_coefficient<THREADS>(p, few, t, first) : p.row_a[t];
+    if (coef == 0.0f) {  // outside every sequence, mostly: zeros, whatever the row holds
+      write_zeros<BF16, THREADS>(d, int(p.vocab), rank, ranks);
+      return;
+    }
     write_gradient<BF16, THREADS>(slice, d, raw, edge, label, coef * p.inv_temp, z.y < 0.0f ? 1.0f : p.k, z.x,
                                   fabsf(z.y));
     return;
@@ -747,6 +751,7 @@ struct StreamRow {
 };
 struct StreamResult {
   float k, shift, g, up;
+  int zeros;  // the gradient is zeros, whatever the row holds
 };
 struct StreamShared {
   uint64_t full[kStreamChunks], empty[kStreamChunks];
@@ -972,6 +977,22 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
         return true;
       }
       const bool aligned = reinterpret_cast<uintptr_t>(d) % 16 == 0;
+      if (q.zeros) {  // the row's chunks are passed over (with a test at each vector instead, a call took 3 % longer)
+        for (int v = r.v0; v < r.v1; v += kVecsChunk) {
+          if (!SUM && !mbar_wait(&sh.full[written], write_phase, kWaitPolls, abort, status)) return false;
+          for (int u = v + tid; p.d != nullptr && u < min(v + kVecsChunk, r.v1); u += kStep) {
+            if (aligned) {
+              __stcs(reinterpret_cast<uint4*>(d) + u, make_uint4(0, 0, 0, 0));
+            } else {
+              for (int w = 0; w < W; ++w) store_one<BF16>(d, int64_t(u) * W + w, 0.0f);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.empty[written]);
+          advance(written, write_phase);
+        }
+        return true;
+      }
       const int own = int(r.label) - r.head;  // the label's place among the vectors' elements
       const Pair kk = pair_of(q.k, q.k), ss = pair_of(-q.shift, -q.shift), gg = pair_of(q.g, q.g);
 #pragma unroll 1
@@ -1081,7 +1102,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
       some = look_up(n + 1, next);
       const StreamRow r = now.r;
       const int64_t t = r.t;
-      StreamResult q = {p.k, 0.0f, 0.0f, 0.0f};
+      StreamResult q = {p.k, 0.0f, 0.0f, 0.0f, 0};
       float terms[3] = {0.0f, 0.0f, 0.0f}, lp = 0.0f;
       const float edge_value = now.edge_value, weight = now.weight;
       const char* x = row_of(t);
@@ -1095,6 +1116,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
           q.k = z.y < 0.0f ? 1.0f : p.k;
           q.shift = z.x;
           q.g = -q.up * fabsf(z.y);
+          q.zeros = weight == 0.0f;
         } else {
           ok = !__any_sync(~0u, !wait(sh.sum_full, n, kStreamRows));
           if (!ok) break;
@@ -1132,9 +1154,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
           if (MODE == kPolicy) {
             const PolicyTerm term = policy_term(p, lp, weight, mean, now.adv, now.old, now.ref);
             for (int c = 0; c < 3; ++c) terms[c] = term.terms[c];
-            q.up = r.label < p.vocab ? term.up : weight == 0.0f ? 0.0f : nan;
+            q.zeros = weight == 0.0f;  // outside every sequence
+            q.up = q.zeros ? 0.0f : r.label < p.vocab ? term.up : nan;
             q.g = -q.up * inv_sum;
-            if (weight == 0.0f) q.k = q.shift = q.g = q.up = 0.0f;  // outside every sequence: zeros
           }
         }
       } else if (SUM) {
@@ -1157,7 +1179,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(LossParams p)
             const int zero = rank == 0 ? RowSpan<W, ES>(d, int(p.vocab)).edge(lane) : -1;
             if (zero >= 0) store_one<BF16>(d, zero, 0.0f);
           } else if (edge >= 0) {
-            const float v = exp2_approx(fmaf(edge_value, q.k, -q.shift)) * q.g;
+            const float v = q.zeros ? 0.0f : exp2_approx(fmaf(edge_value, q.k, -q.shift)) * q.g;
             store_one<BF16>(d, edge, r.label == edge ? v + q.up : v);
           }
         }

@@ -1,0 +1,46 @@
+"""The losses on a GB300 where parts of them are infinite, not a number, or multiplied by nothing."""
+
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+# (rows, vocab, type): a few rows, more than a few, a cluster a row, streamed rows in clusters of 1 and 2
+SIZES = [(20, 60, torch.float32), (24, 61, torch.bfloat16), (600, 60, torch.float32), (24, 32000, torch.float32),
+         (640, 16500, torch.bfloat16), (640, 20003, torch.float32)]
+
+
+@pytest.fixture(scope="module")
+def g():
+    from gradient_sync_gb300 import build
+
+    build.build()
+    import gradient_sync_gb300 as g
+
+    return g
+
+
+def normal(rows, vocab, dtype, seed=0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    x = (torch.randn(rows, vocab, generator=gen, device="cuda") * 2).to(dtype)
+    return x, torch.randint(0, vocab, (rows,), generator=gen, device="cuda")
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", SIZES)
+def test_rows_outside_the_sequences(g, rows, vocab, dtype):
+    """Labelled rows of no sequence have no gradient, whatever they hold."""
+    x, labels = normal(rows, vocab, dtype)
+    x[:, 3::7] = -float("inf")
+    labels = torch.where(labels % 7 == 3, labels - 1, labels)
+    x[0], x[1, 2], x[2] = float("nan"), float("inf"), -float("inf")
+    x[rows - 1, vocab - 1] = float("nan")
+    start = torch.tensor([3, 7, 7, 11, rows - 2], device="cuda")
+    old = torch.nan_to_num(g.ar_token_logp(x, labels)) - 0.1
+    for call in (lambda **kw: g.ar_policy_loss(x, labels, old, torch.ones_like(old), start, **kw),
+                 lambda **kw: g.ar_policy_loss(x, labels, old, torch.ones_like(old), start, reduction="sequence", **kw),
+                 lambda **kw: g.ar_preference_loss(x, labels, old, start, **kw)):
+        stats, *_, d = call()
+        assert torch.isfinite(stats).all() and torch.isfinite(d).all()
+        assert not d[:3].any() and not d[rows - 2:].any() and d[3:rows - 2].any()

@@ -139,3 +139,28 @@ def test_forced_tokens(g, rows, vocab, dtype):
     old = torch.zeros(rows, device="cuda")
     stats, lp, d = g.ar_policy_loss(x, labels, old, old + 1)
     assert not lp.any() and not d.any() and abs(float(stats[0]) + 1) < 1e-6
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", STREAMED)
+def test_rows_outside_the_sequences(g, rows, vocab, dtype):
+    """Labelled rows of no sequence have no gradient, whatever they hold."""
+    x, labels = normal(rows, vocab, dtype, seed=4)
+    x[:, 3::7] = -float("inf")
+    x[1], x[2, 7], x[3] = float("nan"), float("inf"), -float("inf")
+    x[rows - 2, vocab - 1], x[rows - 1] = float("nan"), torch.finfo(dtype).min
+    start = torch.tensor([5, 300, 300, 400, rows - 10], device="cuda")
+    labels[:5] = labels[rows - 10:] = 4
+    labels = torch.where(labels % 7 == 3, labels + 1, labels)  # none ruled out
+    labels[labels >= vocab] = 0
+    lp = g.ar_token_logp(x, labels)
+    check_logp(lp[5:rows - 2], log_probs(x[5:rows - 2], labels[5:rows - 2], 1.0)[0])
+    assert torch.isnan(lp[1:4]).all() and torch.isnan(lp[rows - 2])
+    other = torch.nan_to_num(lp, 0.0)
+    calls = [lambda y, **kw: g.ar_policy_loss(y, labels, other - 0.1, other + 5, start, reduction=r, **kw)
+             for r in ("token", "sequence")] + [lambda y, **kw: g.ar_preference_loss(y, labels, other + 0.1, start, **kw)]
+    for call in calls:
+        *stats, _, d = call(x)
+        assert torch.isfinite(stats[0]).all() and torch.isfinite(d).all()
+        assert not d[:5].any() and not d[rows - 10:].any() and d[5:rows - 10].any()
+        own = x.clone()
+        assert torch.equal(call(own, dlogits=own)[-1], d)

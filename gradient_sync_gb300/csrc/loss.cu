@@ -318,8 +318,8 @@ __device__ __forceinline__ PolicyTerm policy_term(const LossParams& p, float lp,
   PolicyTerm r = {{-w * (free < held || free != free ? free : held), 0.0f, held < free ? w : 0.0f}, 0.0f};
   if (p.ref_logp != nullptr) {
     const float back = ref - lp, grow = expm1f(back);
-    r.terms[1] = w * (grow - back);
-    slope -= p.kl * grow;
+    r.terms[1] = w * (grow == INFINITY ? grow : grow - back);
+    if (p.kl > 0.0f) slope -= p.kl * grow;  // (a coefficient of 0: no part of the loss, infinite or not)
   }
   r.up = w * slope * p.grad_scale * p.inv_temp;
   if (weight == 0.0f) r = {{0.0f, 0.0f, 0.0f}, 0.0f};  // outside every sequence
@@ -1199,7 +1199,7 @@ __global__ void __launch_bounds__(1024) stats_kernel(LossParams p) {
   float out[3];
   sum_columns<1024, 3>(p.row_terms, p.rows, p.rows, out);
   if (threadIdx.x == 0) {
-    p.stats[0] = out[0] + p.kl * out[1];
+    p.stats[0] = p.kl > 0.0f ? out[0] + p.kl * out[1] : out[0];
     p.stats[1] = out[0];
     p.stats[2] = out[1];
     p.stats[3] = out[2];

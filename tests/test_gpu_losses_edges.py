@@ -44,3 +44,21 @@ def test_rows_outside_the_sequences(g, rows, vocab, dtype):
         stats, *_, d = call()
         assert torch.isfinite(stats).all() and torch.isfinite(d).all()
         assert not d[:3].any() and not d[rows - 2:].any() and d[3:rows - 2].any()
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", SIZES)
+def test_divergence_that_is_only_reported(g, rows, vocab, dtype):
+    """With a coefficient of 0 the KL term is a statistic: where it leaves fp32's range, loss and gradient stay."""
+    x, labels = normal(rows, vocab, dtype)
+    at = torch.arange(rows, device="cuda")
+    x[at[:5], labels[:5]] = -200.0
+    x[at[5:7], labels[5:7]] = -float("inf")
+    adv = torch.where(at % 2 == 0, 1.0, -0.5)
+    old = torch.full((rows,), -5.0, device="cuda")
+    ref = torch.full((rows,), -1.0, device="cuda")
+    start = torch.tensor([0, rows // 2, rows], device="cuda")
+    want = g.ar_policy_loss(x, labels, old, adv, start)
+    got = g.ar_policy_loss(x, labels, old, adv, start, ref_logp=ref)
+    assert torch.isfinite(want[0]).all() and torch.isfinite(want[2]).all()
+    assert torch.equal(got[0][[0, 1, 3]], want[0][[0, 1, 3]]) and float(got[0][2]) == math.inf
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])

@@ -311,7 +311,8 @@ struct PolicyTerm {
 };
 __device__ __forceinline__ PolicyTerm policy_term(const LossParams& p, float lp, float weight, float mean, float adv,
                                                   float old, float ref) {
-  const float ratio = expf(lp - old), free = ratio * adv;
+  const float ratio = expf(lp - old);
+  const float free = adv == 0.0f && ratio == INFINITY ? 0.0f : ratio * adv;  // (beyond fp32's range, not infinite)
   const float held = (ratio < p.lo ? p.lo : ratio > p.hi ? p.hi : ratio) * adv;  // NaN stays NaN
   const float w = weight * mean;
   float slope = free <= held ? -free : free > held ? 0.0f : free;

@@ -62,3 +62,22 @@ def test_divergence_that_is_only_reported(g, rows, vocab, dtype):
     assert torch.isfinite(want[0]).all() and torch.isfinite(want[2]).all()
     assert torch.equal(got[0][[0, 1, 3]], want[0][[0, 1, 3]]) and float(got[0][2]) == math.inf
     assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", SIZES)
+def test_tokens_without_advantage(g, rows, vocab, dtype):
+    """An advantage of 0 has no surrogate and no slope, however far the ratio is from 1."""
+    x, labels = normal(rows, vocab, dtype)
+    at = torch.arange(rows, device="cuda")
+    lp = g.ar_token_logp(x, labels)
+    old = torch.where(at % 3 == 0, lp - 150.0, lp)  # ratios beyond fp32's range
+    adv = torch.where(at % 3 == 0, 0.0, 1.0)
+    stats, _, d = g.ar_policy_loss(x, labels, old, adv)
+    n = int((at % 3 != 0).sum())
+    assert abs(float(stats[0]) + n / rows) < 1e-4 and float(stats[0]) == float(stats[1]) and float(stats[3]) == 0.0
+    assert not d[at % 3 == 0].any() and torch.isfinite(d).all() and d[1].any()
+    # with an advantage such a ratio is held by the clip, or makes the loss infinite
+    stats, _, d = g.ar_policy_loss(x, labels, old, torch.ones_like(old), clip_high=0.25)
+    assert abs(float(stats[0]) + (n + 1.25 * (rows - n)) / rows) < 1e-4
+    assert not d[at % 3 == 0].any() and torch.isfinite(d).all()
+    assert float(g.ar_policy_loss(x, labels, old, -torch.ones_like(old))[0][0]) == math.inf

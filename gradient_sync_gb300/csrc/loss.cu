@@ -582,7 +582,8 @@ __device__ __forceinline__ PairTerms pair_terms(const LossParams& p, const Two (
   } else {
     // log1p(e^-|z|) serves both signs of z
     const float tail = log1pf(expf(-fabsf(z))), up = z > 0.0f ? z : 0.0f, down = z < 0.0f ? -z : 0.0f;
-    loss = (1.0f - p.smooth) * (tail + down) + p.smooth * (tail + up);
+    loss = (1.0f - p.smooth) * (tail + down);
+    if (p.smooth > 0.0f) loss += p.smooth * (tail + up);  // (up may be infinite)
     slope = -(1.0f - p.smooth) / (1.0f + expf(z)) + p.smooth / (1.0f + expf(-z));
     if (z != z) loss = slope = z;
   }

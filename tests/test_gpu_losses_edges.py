@@ -81,3 +81,25 @@ def test_tokens_without_advantage(g, rows, vocab, dtype):
     assert abs(float(stats[0]) + (n + 1.25 * (rows - n)) / rows) < 1e-4
     assert not d[at % 3 == 0].any() and torch.isfinite(d).all()
     assert float(g.ar_policy_loss(x, labels, old, -torch.ones_like(old))[0][0]) == math.inf
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", SIZES)
+def test_rejected_answers_that_are_ruled_out(g, rows, vocab, dtype):
+    """-log sigmoid(z) at z = +inf is 0: a rejected answer of probability 0 adds nothing without smoothing."""
+    x, labels = normal(rows, vocab, dtype)
+    at = torch.arange(rows, device="cuda")
+    start = torch.tensor([0, 5, 10, 13, rows], device="cuda")
+    lp = g.ar_token_logp(x, labels)
+    clean = g.ar_preference_loss(x, labels, lp, start, denominator=2.0)
+    x[at[7], labels[7]] = -float("inf")
+    stats, ratios, _, d = g.ar_preference_loss(x, labels, lp, start, denominator=2.0)
+    # the other pair has ratios of 0, or rounding: half of log 2
+    assert abs(float(clean[0][0]) - math.log(2)) < 1e-2 and abs(float(stats[0]) - math.log(2) / 2) < 1e-2
+    assert float(ratios[1]) == -math.inf and float(stats[2]) == -math.inf and float(stats[3]) >= 0.5
+    assert not d[:10].any() and torch.equal(d[10:], clean[3][10:])
+    # the other way round the loss has no bound, and the slope is the steepest
+    x[at[2], labels[2]] = -float("inf")
+    x[at[7], labels[7]] = 0.0
+    stats, ratios, _, d = g.ar_preference_loss(x, labels, lp, start, denominator=2.0, beta=0.5)
+    assert float(stats[0]) == math.inf and float(ratios[0]) == -math.inf and torch.isfinite(d).all()
+    assert abs(float(d[2, labels[2]]) + 0.25) < 1e-3 and abs(float(d[7].float().clamp(min=0).sum())) < 0.26

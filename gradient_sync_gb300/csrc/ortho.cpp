@@ -175,8 +175,8 @@ ar_status ar_ortho_plan(const ar_ortho_desc* desc, ar_ortho_plan_t** out) try {
   }
   if (at / 128 > INT32_MAX) return AR_EUNSUPPORTED;
   p.part_off = at;
-  p.sync_off = at + 4 * parts;
-  p.bytes = at + (4 * (parts + 1 + n) + 255) / 256 * 256;
+  p.sync_off = at + 8 * parts;
+  p.bytes = at + (8 * parts + 4 * (1 + n) + 255) / 256 * 256;
   p.order.resize(n);
   std::iota(p.order.begin(), p.order.end(), 0);
   std::stable_sort(p.order.begin(), p.order.end(), [&](int a, int b) { return p.mats[a].nb > p.mats[b].nb; });

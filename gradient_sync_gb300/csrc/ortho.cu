@@ -45,6 +45,70 @@ namespace {
 
 // ---------------------------------------------------------------- squares
 
+// Sums of squares over all of fp32's range: elements above 2^40 are squared as
+// u 2^-85, those below 2^-40 as u 2^85, and the three sums kept apart. With up
+// to 2^35 elements none overflows, and what an underflow takes from one is
+// nothing beside the element that chose it.
+enum Band : int { kLow = 0, kMiddle = 1, kHigh = 2 };
+constexpr float kHighFrom = 0x1p40f, kLowTo = 0x1p-40f, kHighScale = 0x1p-85f, kLowScale = 0x1p85f;
+
+struct Squares {
+  float low = 0.0f, middle = 0.0f, high = 0.0f;
+  // Adds eight elements, or one, by the largest of them; without a branch, so that loads stay ahead.
+  template <int N>
+  __device__ __forceinline__ void add(const float (&u)[N]) {
+    float top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) top = fmaxf(top, fabsf(u[k]));
+    const bool is_high = top > kHighFrom, is_low = top < kLowTo;  // (zeros, and nothing but NaN, are low)
+    const float scale = is_high ? kHighScale : is_low ? kLowScale : 1.0f;
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) sum = fmaf(u[k] * scale, u[k] * scale, sum);
+    high += is_high ? sum : 0.0f;
+    low += is_low ? sum : 0.0f;
+    middle += is_high || is_low ? 0.0f : sum;
+  }
+  __device__ __forceinline__ void add(float value, int band) {
+    if (band == kMiddle) middle += value;
+    else if (band == kHigh) high += value;
+    else low += value;
+  }
+  // Over the threads of a CTA of 256, in a fixed order; the result in thread 0 (`all`: in all threads).
+  __device__ __forceinline__ void reduce(bool all) {
+    __shared__ float4 parts[8];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) middle += __shfl_xor_sync(~0u, middle, o);
+    if (__any_sync(~0u, low != 0.0f || high != 0.0f)) {  // (not in most calls)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        low += __shfl_xor_sync(~0u, low, o);
+        high += __shfl_xor_sync(~0u, high, o);
+      }
+    }
+    if (threadIdx.x % 32 == 0) parts[threadIdx.x / 32] = make_float4(low, middle, high, 0.0f);
+    __syncthreads();
+    if (!all && threadIdx.x != 0) return;
+    low = middle = high = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      const float4 q = parts[w];
+      low += q.x, middle += q.y, high += q.z;
+    }
+  }
+  // The sum as value / scale^2 for the scale of one band; a NaN in any is in the value.
+  __device__ __forceinline__ float joined(int& band) const {
+    band = high > 0.0f ? kHigh : middle > 0.0f ? kMiddle : kLow;
+    if (low + middle + high != low + middle + high) return __int_as_float(0x7fffffff);
+    if (band == kHigh) return high + middle * kHighScale * kHighScale;
+    if (band == kMiddle) return middle + low / kLowScale / kLowScale;
+    return low;
+  }
+};
+__device__ __forceinline__ float scale_of(int band) {
+  return band == kHigh ? kHighScale : band == kLow ? kLowScale : 1.0f;
+}
+
 // Eight consecutive elements (vec: aligned to 16 bytes), zeros beyond `n`.
 template <bool BF16>
 __device__ __forceinline__ void load8(const void* base, int64_t e, int n, bool vec, float (&f)[8]) {
@@ -77,7 +141,7 @@ __global__ void __launch_bounds__(256) squares_kernel(const __grid_constant__ Or
   if (item == 0)  // the products' counters
     for (int k = threadIdx.x; k <= p.n_mat; k += 256) reinterpret_cast<unsigned int*>(p.ws + p.sync_off)[k] = 0;
   const int64_t lo = int64_t(item - p.start[0][i]) * kOrthoChunk, hi = lo + kOrthoChunk < total ? lo + kOrthoChunk : total;
-  float sum = 0.0f;
+  Squares sum;
   if (io.vec_in) {  // eight elements of one row at a time
 #pragma unroll 4
     for (int64_t e = lo + threadIdx.x * 8; e < hi; e += 256 * 8) {
@@ -97,8 +161,7 @@ __global__ void __launch_bounds__(256) squares_kernel(const __grid_constant__ Or
         to[0] = make_float4(mom[0], mom[1], mom[2], mom[3]);
         to[1] = make_float4(mom[4], mom[5], mom[6], mom[7]);
       }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) sum = fmaf(u[k], u[k], sum);
+      sum.add(u);
     }
   } else {
     for (int64_t e = lo + threadIdx.x; e < hi; e += 256) {
@@ -110,17 +173,15 @@ __global__ void __launch_bounds__(256) squares_kernel(const __grid_constant__ Or
         io.m_out[r * io.m_out_ld + c] = mom;
         u = p.hyper.nesterov ? fmaf(p.hyper.mu, mom, u) : mom;
       }
-      sum = fmaf(u, u, sum);
+      const float one[1] = {u};
+      sum.add(one);
     }
   }
-  __shared__ float parts[8];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-  if (threadIdx.x % 32 == 0) parts[threadIdx.x / 32] = sum;
-  __syncthreads();
+  sum.reduce(false);
   if (threadIdx.x == 0) {
-    for (int w = 1; w < 8; ++w) sum += parts[w];
-    reinterpret_cast<float*>(p.ws + p.part_off)[mat.part + (item - p.start[0][i])] = sum;
+    int band;
+    const float value = sum.joined(band);
+    reinterpret_cast<float2*>(p.ws + p.part_off)[mat.part + (item - p.start[0][i])] = make_float2(value, float(band));
   }
 }
 
@@ -130,7 +191,6 @@ __global__ void __launch_bounds__(256) squares_kernel(const __grid_constant__ Or
 template <bool BF16>
 __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ OrthoTable p) {
   __shared__ float tile[64][129];  // [column of X][row of X], tall matrices
-  __shared__ float parts[8];
   grid_dependency_wait();
   grid_dependents_launch();
   const int item = blockIdx.x, i = find_matrix(p, item);
@@ -174,16 +234,13 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ Ortho
       update(gr, gc, gr < mat.m ? mat.n - gc : 0, v[q]);
     }
   }
-  const float* part = reinterpret_cast<const float*>(p.ws + p.part_off) + mat.part;
-  float sum = 0.0f;
-  for (int k = tid; k < mat.n_part; k += 256) sum += part[k];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-  if (tid % 32 == 0) parts[tid / 32] = sum;
-  __syncthreads();
-  sum = 0.0f;
-  for (int w = 0; w < 8; ++w) sum += parts[w];
-  const float scale = mat.sx / (sqrtf(sum) + p.eps);
+  const float2* part = reinterpret_cast<const float2*>(p.ws + p.part_off) + mat.part;
+  Squares sum;
+  for (int k = tid; k < mat.n_part; k += 256) sum.add(part[k].x, int(part[k].y));
+  sum.reduce(true);  // (the tile is written too)
+  int band;
+  const float norm = sqrtf(sum.joined(band)), first = scale_of(band);  // the norm times `first`, a power of two
+  const float scale = mat.sx / (norm + p.eps * first);
   char* hi = p.ws + mat.x + (int64_t(rb) * mat.nb + cb) * kBlockBytes;
   char* lo = hi + mat.x_bytes;
 #pragma unroll
@@ -194,7 +251,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ Ortho
       for (int k = 0; k < 8; ++k) v[q][k] = tile[c * 8 + k][r];
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[q][k] *= scale;
+    for (int k = 0; k < 8; ++k) v[q][k] = v[q][k] * first * scale;
     uint4 h, l;
     split_pair(v[q][0], v[q][1], h.x, l.x);
     split_pair(v[q][2], v[q][3], h.y, l.y);

@@ -653,7 +653,8 @@ ar_status ar_preference_loss(const ar_logits* logits, const float* ref_logp, con
  * multiplies three of the four combinations, about 22 bits throughout, at
  * about 3 times the work. AR_PRECISION_AUTO is SPLIT for AR_F32 results and
  * HALF for AR_BF16 results (whose own rounding is larger than HALF's error).
- * Momentum is fp32. A zero matrix gives zeros (with eps > 0); a NaN or an infinity anywhere
+ * Momentum is fp32. The norm is summed over all of fp32's range: finite elements of any size
+ * have their result. A zero matrix gives zeros (with eps > 0); a NaN or an infinity anywhere
  * in a matrix gives NaN throughout that matrix.                             */
 #define AR_MAX_MATRICES 192
 #define AR_MAX_ORTHO_STEPS 16

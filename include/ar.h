@@ -652,7 +652,8 @@ ar_status ar_preference_loss(const ar_logits* logits, const float* ref_logp, con
  * to 22 bits, but for the inputs of the last two steps); AR_PRECISION_SPLIT keeps operands as two fp16 numbers and
  * multiplies three of the four combinations, about 22 bits throughout, at
  * about 3 times the work. AR_PRECISION_AUTO is SPLIT for AR_F32 results and
- * HALF for AR_BF16 results (whose own rounding is larger than HALF's error).
+ * HALF for AR_BF16 results (whose own rounding is as large as HALF's error, but for
+ * matrices of a few rows, where single singular values count: 2 x 3 1.2e-2).
  * Momentum is fp32. The norm is summed over all of fp32's range: finite elements of any size
  * have their result. A zero matrix gives zeros (with eps > 0); a NaN or an infinity anywhere
  * in a matrix gives NaN throughout that matrix.                             */

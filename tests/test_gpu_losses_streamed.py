@@ -164,3 +164,16 @@ def test_rows_outside_the_sequences(g, rows, vocab, dtype):
         assert not d[:5].any() and not d[rows - 10:].any() and d[5:rows - 10].any()
         own = x.clone()
         assert torch.equal(call(own, dlogits=own)[-1], d)
+
+
+@pytest.mark.parametrize("tau", [0.1, 0.01])
+@pytest.mark.parametrize("fill", [None, -1e4, -float("inf")])
+@pytest.mark.parametrize("rows,vocab,dtype", STREAMED)
+def test_low_temperatures(g, rows, vocab, dtype, fill, tau):
+    """Logits hundreds apart over the temperature, and the same behind a mask that hides a thread's first vectors."""
+    x, labels = normal(rows, vocab, dtype, seed=7)
+    if fill is not None:
+        x[:, :1024 * (8 if dtype == torch.bfloat16 else 4)] = fill
+    best = x.topk(2, 1).indices  # (a log-probability of hundreds would bring in its own rounding)
+    labels = torch.where(labels < 0, labels, best[torch.arange(rows, device="cuda"), labels % 2])
+    check_all(g, x, labels, tau)

@@ -21,9 +21,15 @@ constexpr int kUnit = 16384;        // one operand unit: 128 rows x 64 of k
 // one sum 4.5e-5; every 4 steps 6.6e-6, 2.9e-6, 398 us, 2.65 ms; every 2 steps
 // 3.7e-6, 1.6e-6, 424 us, 2.81 ms; every step 2.2e-6, 1.1e-6, 497 us, 3.36 ms.
 // Elementary fp32 operations: 3.9e-6, 4.4e-6, growing with the length, so long
-// products are added up every 4 steps.
-constexpr int kLongSums = 64;
-__host__ __device__ constexpr int segment_steps(bool split, int ks) { return !split ? ks : ks < kLongSums ? 2 : 4; }
+// products are added up every 4 steps. Short ones, where fp32 operations round
+// least, are added up every step, but for A = X X^T, which gains nothing by it
+// (every 2 steps, every step and fp32 operations: 300 x 3000 3.4e-6, 2.2e-6,
+// 1.9e-6, 267 and 274 us; 130 x 4000 3.4e-6, 1.9e-6, 1.9e-6, 267 and 268 us;
+// eight of 512 x 2048 354 and 387 us).
+constexpr int kLongSums = 64, kShortSums = 8;
+__host__ __device__ constexpr int segment_steps(bool split, bool gram, int ks) {
+  return !split ? ks : !gram && ks <= kShortSums ? 1 : ks < kLongSums ? 2 : 4;
+}
 
 // ---------------------------------------------------------------- tensor core
 
@@ -764,7 +770,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
       taken(n);
       const int a_from = left_mn_from<S>(t), b_from = right_mn_from<S>(t);
       const uint32_t idesc = instr_desc(S::CTAS * 128, t.nu * 128);
-      const int segment = segment_steps(SPLIT, t.ks);
+      const int segment = segment_steps(SPLIT, t.op == kGram, t.ks);
       for (int k0 = 0; k0 < t.ks; k0 += segment, ++part) {
         const int acc = part & 1;
         if (part >= 2 && __any_sync(~0u, !mbar_wait(&acc_empty[acc], (part / 2 + 1) & 1, kWaitPolls, abort, p.status)))
@@ -860,7 +866,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, CLUSTER>::THREADS, 1)
       load_old(t, block0);
       float sum[SPLIT ? 64 : 1];
       uint32_t at = 0;  // this warp's accumulator
-      const int segment = segment_steps(SPLIT, t.ks);
+      const int segment = segment_steps(SPLIT, t.op == kGram, t.ks);
       for (int k0 = 0; k0 < t.ks; k0 += segment, ++part) {
         const int acc = part & 1;
         if (owed >= 0 && !mbar_test(&acc_full[acc], (part / 2) & 1)) report(false);

@@ -363,13 +363,16 @@ def _vector(t, dtype, n: int, what: str) -> int:
 
 
 def _row_major(t, what: str) -> int:
-    """The row stride of a 2-D device tensor whose rows are contiguous."""
-    if t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: a 2-D CUDA tensor with contiguous rows wanted, got shape {tuple(t.shape)}, "
-                         f"strides {t.stride()} on {t.device}")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:  # an expanded tensor, or rows inside one another
-        raise ValueError(f"{what}: rows that share no memory wanted, got shape {tuple(t.shape)}, strides {t.stride()}")
-    return max(t.stride(0), t.shape[1])  # (the stride of a single row means nothing)
+    """The row stride of a 2-D device tensor whose rows are contiguous and share no memory."""
+    if t.dim() == 2 and t.is_cuda:
+        (rows, cols), (ld, step) = t.shape, t.stride()
+        if step == 1 or cols <= 1:
+            if ld >= cols:
+                return ld
+            if rows <= 1:  # (the stride of a single row means nothing)
+                return cols
+    raise ValueError(f"{what}: a 2-D CUDA tensor with contiguous rows that share no memory wanted, got shape "
+                     f"{tuple(t.shape)}, strides {t.stride()} on {t.device}")
 
 
 def _logits(logits, labels, temperature):

@@ -15,11 +15,13 @@ using namespace ar;
 constexpr int64_t kMaxDim = 1 << 20;
 // Plans with at least this many 256 x 256 tiles of X run tiles of two CTAs,
 // which read less per product but pad row blocks to 256 and have fewer tiles.
-// Measured, one CTA against two: half precision 512 x 512 (4 tiles) 124 and
-// 153 us, 1536 x 1536 (36) 216 and 223, 1024 x 4096 (64) 266 and 254,
-// 2048 x 4096 (128) 422 and 380; split 256 x 256 (1) 143 and 137, 512 x 512
-// 187 and 173, 1024 x 1024 (16) 283 and 233, 2048 x 4096 1027 and 753.
-constexpr int64_t kPairTiles = 64, kPairTilesSplit = 2;
+// Measured, one CTA against two: half precision 512 x 512 (4 tiles) 126 and
+// 130 us, 1024 x 1024 (16) 169 and 162, 1536 x 1536 (36) 221 and 206,
+// 1024 x 4096 (64) 271 and 247, 2048 x 4096 (128) 427 and 370; split 256 x 256
+// (1) 149 and 140, 512 x 512 200 and 186, 1024 x 1024 (16) 284 and 233,
+// 2048 x 4096 1004 and 743. (A matrix of at most 128 rows leaves a pair's second
+// CTA without work, so that one tile alone stays with one CTA.)
+constexpr int64_t kPairTiles = 16, kPairTilesSplit = 2;
 constexpr float kDefault[3] = {3.4445f, -4.7750f, 2.0315f};
 
 size_t esize(ar_dtype d) { return d == AR_BF16 ? 2 : 4; }

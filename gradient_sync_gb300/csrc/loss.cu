@@ -279,7 +279,12 @@ __device__ __forceinline__ Lse thread_lse(const uint4 (&raw)[kVecs], float k) {
   return {c, s[0] + s[1]};
 }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+// (RUNS: nothing but that this thread's CTA runs is told, and no fence taken)
+template <bool RUNS = false>
+__device__ __forceinline__ void cluster_arrive() {
+  if (RUNS) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+  else asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void cluster_barrier() {
   cluster_arrive();
@@ -672,7 +677,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) rows_kernel(LossParam
     return;
   }
   // (all CTAs of a cluster have the same row: they return above together, or come here)
-  if (MODE != kPrefBackward && ranks > 1) cluster_arrive();  // waited for in row_sum, behind the loads
+  if (MODE != kPrefBackward && ranks > 1) cluster_arrive<true>();  // waited for in row_sum, behind the loads
   const Slice<BF16, THREADS> slice(x, int(p.vocab), rank, ranks);
   uint4 raw[kVecs];
   slice.load(raw, slice.v0);

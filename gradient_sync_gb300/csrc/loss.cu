@@ -7,7 +7,9 @@
 // and a loss that depends on the logits through lp alone has
 //   dL/dx_j = (dL/dlp) * ([j = y] - p_j) / tau,   p_j = exp(x_j / tau) / sum.
 //
-// All of it is kept in base 2: with k = log2(e) / tau and any shift c,
+// All of it is kept in base 2: with k = log2(e) / tau (rounded to fp32, which
+// moves lp by at most 2^-24 (x_y - mean x) / tau, mean over p, alike in every call:
+// differences of log-probabilities made here lose most of it) and any shift c,
 // e_j = 2^(x_j k - c) is one FMA and one exponential, and two partial sums
 // with shifts c1, c2 combine exactly by 2^(c1 - c2). Sums and shifts are fp32;
 // the few operations a row does once (lp itself) are in pairs of fp32, so that
@@ -25,12 +27,12 @@
 // first; each gradient row is written once), by launches and latency where
 // there are few. One GB300, copy bandwidth 6771 GB/s:
 //  stream_kernel  many long rows. 16384 x 32000 bf16, a quarter masked, policy
-//                 loss: 304 us in the kernel for 1.78 GB, 0.86 of the copy
+//                 loss: 298 us in the kernel for 1.77 GB, 0.88 of the copy
 //                 bandwidth (two exponentials an element: special function
-//                 unit 31 % busy, issue slots 55 %); 3001 x 32003 fp32: 113 us a call;
-//                 log-probabilities of 6007 x 50021 bf16: 77 us, 0.87.
+//                 unit 28 % busy, issue slots 51 %); 3001 x 32003 fp32: 112 us a call;
+//                 log-probabilities of 6007 x 50021 bf16: 78 us, 0.86.
 //  rows_kernel    a cluster of CTAs a row, the row in registers: 16 x 32000
-//                 fp32 log-probabilities 3.9 us in a graph of calls
+//                 fp32 log-probabilities 4.0 us in a graph of calls
 //  count_kernel, stats_kernel, pair_kernel  sequences; not needed where a call
 //                 has a few rows (64-token policy loss 11 us in a graph of calls)
 #include "loss.h"
@@ -1347,11 +1349,12 @@ cudaError_t active_clusters(const void* kernel, int cluster, size_t smem, int* w
 }
 
 // Calls with many long rows stream them; the others take a cluster a row.
-// Measured, a cluster a row against streaming (log-probabilities / policy loss):
-// 6000 rows of 24 KB 42 / 75 and 51 / 85 us, of 32 KB 43 / 82 and 53 / 91, of
-// 40 KB (where a row needs 512 threads) 91 / 140 and 59 / 113, of 56 KB 95 / 152
-// and 65 / 127; rows of 64 KB, 300 of them 7.0 / 20.8 and 7.4 / 22.2, 600 of them
-// 11.1 / 24.4 and 9.9 / 26.0, 1200 of them 22.0 / 41.2 and 17.5 / 35.1.
+// Measured, a cluster a row against streaming (log-probabilities / policy loss,
+// in a graph of calls): 6000 rows of 24 KB 41 / 73 and 60 / 96 us, of 32 KB
+// 43 / 81 and 61 / 98, of 40 KB (where a row needs 512 threads) 90 / 138 and
+// 62 / 111, of 56 KB 93 / 151 and 63 / 121; rows of 64 KB, 300 of them 5.9 / 12.5
+// and 5.5 / 11.7, 600 of them 10.2 / 20.9 and 8.5 / 17.9, 1200 of them 19.4 / 40.5
+// and 14.5 / 33.4.
 constexpr int64_t kStreamRowBytes = 32768, kStreamRowsAnSm = 4;
 
 template <bool BF16, int MODE>

@@ -33,10 +33,10 @@
 //
 // Kernels (three launches for all matrices of a call):
 //  squares_kernel  momentum update, partial sums of squares of the update. HBM:
-//                  114 us for one transformer layer's 67 M elements (fp32
-//                  gradients and momentum: 806 MB, 1.04 of the copy bandwidth)
-//  pack_kernel     X in blocks, scaled, transposed where tall. HBM: 124 us for
-//                  the same (805 MB, 0.96)
+//                  111 us for one transformer layer's 67 M elements (fp32
+//                  gradients and momentum: 806 MB, 1.07 of the copy bandwidth)
+//  pack_kernel     X in blocks, scaled, transposed where tall. HBM: 126 us for
+//                  the same (805 MB, 0.94)
 //  steps_kernel    every product of every step (ortho_steps.cuh)
 #include "ortho_table.cuh"
 

@@ -550,7 +550,8 @@ ar_status ar_compressed_allreduce(int n_ranks, size_t count, int block, ar_dtype
  *    entries of -inf (tokens that are ruled out) have probability 0.
  *  - sequences are given by n_seq + 1 non-decreasing row offsets in device
  *    memory; sequence s is rows [seq_start[s], seq_start[s+1]), and may be
- *    empty or have no labelled row. Rows outside every sequence do not count.
+ *    empty or have no labelled row. Rows outside every sequence do not count:
+ *    their gradient rows are zeros, whatever their logits hold.
  *  - device pointers are aligned to their element; rows of logits and of
  *    gradients may lie further apart than vocab. The gradient may be written
  *    over the logits (same address and row stride); otherwise outputs must
@@ -584,7 +585,8 @@ typedef enum {
 
 typedef struct {
   float clip_low, clip_high; /* the ratio is clipped to [1 - low, 1 + high] */
-  float kl_coef;             /* beta >= 0; > 0 needs ref_logp */
+  float kl_coef;             /* beta >= 0; > 0 needs ref_logp; at 0 the term is
+                                a statistic and no part of L, even where infinite */
   ar_loss_mean mean;
   float denominator;         /* > 0: replaces the counted denominator of the
                                 mean (labelled tokens or sequences), e.g. by

@@ -37,6 +37,9 @@ LOSS_MEANS = {"token": 0, "sequence": 1}
 PREFERENCE_FORMS = {"sigmoid": 0, "square": 1}
 PRECISIONS = {"auto": 0, "half": 1, "split": 2}
 ADJUSTS = {"none": 0, "shape": 1, "rms": 2}
+NORM_KINDS = {"l2": 0, "max": 1}
+VERIFY_MODES = {"sample": 0, "greedy": 1}
+AR_MAX_TENSORS = 65536
 AR_MAX_MATRICES = 192
 KERNEL_NAMES = {v: k for k, v in KERNELS.items()}
 
@@ -415,14 +418,15 @@ def _gradient(logits, dlogits, grad: bool, stream):
     return dlogits, dlogits.data_ptr(), _row_major(dlogits, "dlogits")
 
 
-def _output(t, n: int, like, what: str, stream):
-    """An fp32 vector to write to, and its address."""
+def _output(t, n: int, like, what: str, stream, dtype=None):
+    """A vector (of fp32 by default) to write to, and its address."""
     import torch
 
+    dtype = dtype or torch.float32
     if t is None:
-        t = _empty(n, torch.float32, like, stream)
+        t = _empty(n, dtype, like, stream)
         return t, t.data_ptr()
-    return t, _vector(t, torch.float32, n, what)
+    return t, _vector(t, dtype, n, what)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -608,6 +612,222 @@ def ar_muon_step(plan: OrthoPlan, params, grads, momenta, lr: float, momentum: f
     d = _lib.ArMuonDesc(float(lr), float(momentum), float(weight_decay), int(bool(nesterov)),
                         ADJUSTS.get(adjust, adjust), float(grad_scale))
     _check(_lib.load().ar_muon_step(plan.handle, d, p, g, m, po, mo, room, _stream(stream)), "ar_muon_step")
+
+
+# ---------------------------------------------------------------- gradients
+
+
+def _dense(t) -> bool:
+    """Whether the elements lie one behind the other in some order of the dimensions."""
+    if t.is_contiguous():
+        return True
+    step = 1
+    for stride, size in sorted(zip(t.stride(), t.shape)):
+        if size == 1:
+            continue
+        if stride != step:
+            return False
+        step *= size
+    return True
+
+
+class TensorList:
+    """Tensors of the calls below, marshalled once. Pass it in place of a list when the same
+    tensors are used again and again, as an optimiser does every step: the per-call cost is then
+    independent of their number. It keeps the tensors alive; they may be written to, not moved.
+
+    Tensors are float32 or bfloat16 CUDA tensors of one device whose elements lie one behind the other
+    (any order of the dimensions). None stands for a tensor that is not there (masters only)."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        n = len(self.tensors)
+        if n == 0:
+            raise ValueError("a list of at least one tensor wanted")
+        self.c = (_lib.ArTensor * n)()
+        self.counts, self.layouts, self.device = [], [], None
+        for i, t in enumerate(self.tensors):
+            if t is None:
+                self.c[i].data, self.c[i].count, self.c[i].dtype = None, 0, AR_F32
+                self.counts.append(None)
+                self.layouts.append(None)
+                continue
+            if not t.is_cuda or not _dense(t):
+                raise ValueError(f"[{i}]: a CUDA tensor whose elements lie one behind the other wanted, got shape "
+                                 f"{tuple(t.shape)}, strides {t.stride()} on {t.device}")
+            if self.device is None:
+                self.device, self.like = t.device, t
+            elif t.device != self.device:
+                raise ValueError(f"[{i}]: tensors of one device wanted, got {self.device} and {t.device}")
+            self.c[i].data, self.c[i].count, self.c[i].dtype = t.data_ptr(), t.numel(), _dtype_of(t)
+            self.counts.append(t.numel())
+            # what an element's place depends on, where it is not simply its index
+            self.layouts.append(None if t.is_contiguous() else (tuple(t.shape), t.stride()))
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def _tensors(x, what: str, like: TensorList | None = None):
+    """A TensorList of `x` (None stays None), laid out like another one."""
+    if x is None:
+        return None
+    if not isinstance(x, TensorList):
+        try:
+            x = TensorList(x)
+        except ValueError as e:
+            raise ValueError(f"{what}{e}") from None
+    if like is None:
+        if any(v is None for v in x.counts):
+            raise ValueError(f"{what}: None in place of a tensor")
+        return x
+    if x.device is not None and x.device != like.device:
+        raise ValueError(f"{what}: tensors on {like.device} wanted, got {x.device}")
+    if x.counts != like.counts or x.layouts != like.layouts:
+        optional = what.startswith("masters")
+        same = len(x) == len(like) and all(
+            (a is None and optional) or (a == b and c == d)
+            for a, b, c, d in zip(x.counts, like.counts, x.layouts, like.layouts))
+        if not same:
+            raise ValueError(f"{what}: as many tensors wanted, with the same numbers of elements in the same order")
+    return x
+
+
+def _here(tensors: TensorList):
+    """Refuses tensors of another device than the one that the call would run on."""
+    import torch
+
+    if torch.cuda.is_initialized() and tensors.device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on {tensors.device}, but the current device is cuda:{torch._C._cuda_getDevice()}")
+
+
+@functools.lru_cache(maxsize=1024)
+def _grad_workspace(n: int) -> int:
+    b = _lib.c_size_t()
+    _check(_lib.load().ar_grad_workspace(n, b), "ar_grad_workspace")
+    return b.value
+
+
+def ar_grad_workspace(grads) -> int:
+    """Device bytes that ar_grad_norm and ar_grad_clip need for a list of tensors (or for so many)."""
+    return _grad_workspace(grads if isinstance(grads, int) else len(grads))
+
+
+def _norm_call(grads, max_norm, kind, eps, grad_scale, stats, norms, workspace, stream):
+    grads = _tensors(grads, "grads")
+    _here(grads)
+    n, like = len(grads), grads.like
+    stats, stats_at = _output(stats, 4, like, "stats", stream)
+    norms, norms_at = _output(norms, n, like, "norms", stream)
+    workspace, room = _room(workspace, _grad_workspace(n), like, stream)
+    desc = _lib.ArNormDesc(NORM_KINDS.get(kind, kind), max_norm, eps, grad_scale)
+    return grads, n, desc, stats, stats_at, norms, norms_at, workspace, room
+
+
+def ar_grad_norm(grads, max_norm: float = float("inf"), kind="l2", eps: float = 1e-6, grad_scale: float = 1.0,
+                 stats=None, norms=None, workspace=None, stream=None):
+    """Global norm of a list of gradients (or a TensorList) and its clipping coefficient (see
+    include/ar.h). Returns (stats [norm, coefficient, clipped, finite], norms of the tensors), fp32 on
+    the device; `ar_adamw_step(clip=stats)` reads them there."""
+    grads, n, desc, stats, stats_at, norms, norms_at, workspace, room = _norm_call(
+        grads, max_norm, kind, eps, grad_scale, stats, norms, workspace, stream)
+    _check(_lib.load().ar_grad_norm(grads.c, n, desc, stats_at, norms_at, room, _stream(stream)), "ar_grad_norm")
+    return stats, norms
+
+
+def ar_grad_clip(grads, max_norm: float, outs=None, kind="l2", eps: float = 1e-6, grad_scale: float = 1.0,
+                 stats=None, norms=None, workspace=None, stream=None):
+    """The same, and the gradients times grad_scale and the coefficient: in place unless `outs`.
+    Returns (stats, norms, outs)."""
+    grads, n, desc, stats, stats_at, norms, norms_at, workspace, room = _norm_call(
+        grads, max_norm, kind, eps, grad_scale, stats, norms, workspace, stream)
+    to = _tensors(outs, "outs", grads)
+    _check(_lib.load().ar_grad_clip(grads.c, n, None if to is None else to.c, desc, stats_at, norms_at, room,
+                                    _stream(stream)), "ar_grad_clip")
+    return stats, norms, (grads if to is None else to).tensors
+
+
+def ar_adamw_step(params, grads, exp_avgs, exp_avg_sqs, lr: float, step, betas=(0.9, 0.999), eps: float = 1e-8,
+                  weight_decay: float = 0.0, grad_scale: float = 1.0, clip=None, masters=None, params_out=None,
+                  exp_avgs_out=None, exp_avg_sqs_out=None, masters_out=None, stream=None):
+    """One AdamW step on lists of tensors or TensorLists (see include/ar.h), in place unless *_out
+    lists are given.
+
+    `params` and `grads` float32 or bfloat16, moments float32. `step` counts from 1: an int, or a
+    device int64 tensor of one element that is read when the step runs. `clip`: the stats of
+    ar_grad_norm (same grad_scale). `masters`: float32 weights behind the parameters, None for a
+    parameter that has none."""
+    import torch
+
+    p = _tensors(params, "params")
+    _here(p)
+    g = _tensors(grads, "grads", p)
+    m, v = _tensors(exp_avgs, "exp_avgs", p), _tensors(exp_avg_sqs, "exp_avg_sqs", p)
+    w, wo = _tensors(masters, "masters", p), _tensors(masters_out, "masters_out", p)
+    po = _tensors(params_out, "params_out", p)
+    mo, vo = _tensors(exp_avgs_out, "exp_avgs_out", p), _tensors(exp_avg_sqs_out, "exp_avg_sqs_out", p)
+    at = 0
+    if isinstance(step, torch.Tensor):
+        at, step = _vector(step.reshape(-1), torch.int64, 1, "step"), 0
+    desc = _lib.ArAdamwDesc(lr, betas[0], betas[1], eps, weight_decay, grad_scale, step, at)
+    scale = None if clip is None else _vector(clip, torch.float32, 4, "clip")
+    c = [None if x is None else x.c for x in (p, g, m, v, w, po, mo, vo, wo)]
+    _check(_lib.load().ar_adamw_step(desc, len(p), *c, scale, _stream(stream)), "ar_adamw_step")
+
+
+# ---------------------------------------------------------------- drafts
+
+
+@functools.lru_cache(maxsize=1024)
+def ar_verify_workspace(n_drafts: int, n_seq: int, vocab: int) -> int:
+    """Device bytes that ar_verify_drafts needs."""
+    b = _lib.c_size_t()
+    _check(_lib.load().ar_verify_workspace(int(n_drafts), int(n_seq), int(vocab), b), "ar_verify_workspace")
+    return b.value
+
+
+def ar_verify_drafts(target, drafts, uniforms=None, draft_start=None, draft_logits=None, temperature: float = 1.0,
+                     draft_temperature=None, mode="sample", accepted=None, tokens=None, logp=None, workspace=None,
+                     stream=None):
+    """Keep as many drafted tokens as leave the tokens distributed as the target's own, and draw
+    the one behind them (see include/ar.h).
+
+    `target` [n_drafts + n_seq, vocab] and `draft_logits` [n_drafts, vocab] (None: no distributions)
+    float32 or bfloat16, any row stride; `drafts` int64 [n_drafts]; `uniforms` fp32 in [0, 1), one a row of
+    the target (None in greedy mode); `draft_start` int64 [n_seq + 1] offsets of the sequences' drafts
+    (None: one sequence). `draft_temperature` is `temperature` by default. Returns (accepted [n_seq],
+    tokens, logp), the last two laid out like the target's rows: tokens behind the drawn one are -1
+    with log-probability 0."""
+    import torch
+
+    ld = _row_major(target, "target")
+    rows, vocab = target.shape
+    n_drafts = drafts.shape[0] if drafts.dim() == 1 else -1
+    n_seq = rows - n_drafts
+    if n_drafts < 0 or n_seq < 1:
+        raise ValueError(f"drafts: one row of the target a draft and one more a sequence wanted, got "
+                         f"{tuple(drafts.shape)} drafts and {rows} rows")
+    drafts_at = _vector(drafts, torch.int64, n_drafts, "drafts")
+    mode = VERIFY_MODES.get(mode, mode)
+    if uniforms is None and mode != VERIFY_MODES["greedy"]:
+        raise ValueError("uniforms: wanted, but in greedy mode")
+    u = 0 if uniforms is None else _vector(uniforms, torch.float32, rows, "uniforms")
+    start = 0 if draft_start is None else _vector(draft_start, torch.int64, n_seq + 1, "draft_start")
+    d = _lib.ArVerifyDesc(vocab=vocab, drafts=drafts_at, uniforms=u, draft_start=start, n_drafts=n_drafts, n_seq=n_seq,
+                          mode=mode)
+    d.target = _lib.ArScoreRows(target.data_ptr(), rows, ld, _dtype_of(target), temperature)
+    if draft_logits is not None:
+        if tuple(draft_logits.shape) != (n_drafts, vocab):
+            raise ValueError(f"draft_logits: {(n_drafts, vocab)} wanted, got {tuple(draft_logits.shape)}")
+        d.draft = _lib.ArScoreRows(draft_logits.data_ptr(), n_drafts, _row_major(draft_logits, "draft_logits"),
+                                   _dtype_of(draft_logits),
+                                   temperature if draft_temperature is None else draft_temperature)
+    accepted, accepted_at = _output(accepted, n_seq, target, "accepted", stream, torch.int64)
+    tokens, tokens_at = _output(tokens, rows, target, "tokens", stream, torch.int64)
+    logp, logp_at = _output(logp, rows, target, "logp", stream)
+    workspace, room = _room(workspace, ar_verify_workspace(n_drafts, n_seq, vocab), target, stream)
+    _check(_lib.load().ar_verify_drafts(d, accepted_at, tokens_at, logp_at, room, _stream(stream)), "ar_verify_drafts")
+    return accepted, tokens, logp
 
 
 # ---------------------------------------------------------------- status

@@ -59,6 +59,32 @@ class ArMuonDesc(ctypes.Structure):
                 ("adjust", c_int), ("grad_scale", c_float)]
 
 
+class ArTensor(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("count", ctypes.c_int64), ("dtype", c_int)]
+
+
+class ArNormDesc(ctypes.Structure):
+    _fields_ = [("kind", c_int), ("max_norm", ctypes.c_double), ("eps", ctypes.c_double), ("grad_scale", c_float)]
+
+
+class ArAdamwDesc(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("grad_scale", c_float),
+                ("step", ctypes.c_int64), ("device_step", c_void_p)]
+
+
+class ArScoreRows(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("rows", ctypes.c_int64), ("ld", ctypes.c_int64), ("dtype", c_int),
+                ("temperature", c_float)]
+
+
+class ArVerifyDesc(ctypes.Structure):
+    _fields_ = [("target", ArScoreRows), ("draft", ArScoreRows), ("vocab", ctypes.c_int64), ("drafts", c_void_p),
+                ("uniforms", c_void_p), ("draft_start", c_void_p), ("n_drafts", ctypes.c_int64),
+                ("n_seq", ctypes.c_int64), ("mode", c_int)]
+
+
+TENSORP = ctypes.POINTER(ArTensor)
 MATRIXP = ctypes.POINTER(ArMatrix)
 
 # name -> (restype, argtypes), in the order of include/ar.h
@@ -102,6 +128,14 @@ SIGNATURES = {
     "ar_orthogonalize": (c_int, [c_void_p, MATRIXP, MATRIXP, c_void_p, c_void_p]),
     "ar_muon_step": (c_int, [c_void_p, ctypes.POINTER(ArMuonDesc), MATRIXP, MATRIXP, MATRIXP, MATRIXP, MATRIXP,
                              c_void_p, c_void_p]),
+    "ar_grad_workspace": (c_int, [c_int, SIZEP]),
+    "ar_grad_norm": (c_int, [TENSORP, c_int, ctypes.POINTER(ArNormDesc), c_void_p, c_void_p, c_void_p, c_void_p]),
+    "ar_grad_clip": (c_int, [TENSORP, c_int, TENSORP, ctypes.POINTER(ArNormDesc), c_void_p, c_void_p, c_void_p,
+                             c_void_p]),
+    "ar_adamw_step": (c_int, [ctypes.POINTER(ArAdamwDesc), c_int, TENSORP, TENSORP, TENSORP, TENSORP, TENSORP,
+                              TENSORP, TENSORP, TENSORP, TENSORP, c_void_p, c_void_p]),
+    "ar_verify_workspace": (c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, SIZEP]),
+    "ar_verify_drafts": (c_int, [ctypes.POINTER(ArVerifyDesc), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
     "ar_device_status": (c_int, [c_int]),
     "ar_plan_query": (c_int, [c_void_p]),
     "ar_selftest_wait_timeout": (c_int, [ctypes.c_uint, c_void_p]),

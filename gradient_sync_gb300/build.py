@@ -21,10 +21,10 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libar_gb300.so")
 
 CUDA_SOURCES = ["fused.cu", "fused_tma.cu", "step.cu", "pack.cu", "noalloc.cu", "compress.cu", "loss.cu", "ortho.cu",
-                "ortho_steps1.cu", "ortho_steps2.cu"]
-CXX_SOURCES = ["api.cpp", "loss.cpp", "ortho.cpp"]
+                "ortho_steps1.cu", "ortho_steps2.cu", "grads.cu", "verify.cu"]
+CXX_SOURCES = ["api.cpp", "loss.cpp", "ortho.cpp", "grads.cpp", "verify.cpp"]
 HEADERS = ["internal.h", "common.cuh", "bulk.cuh", "loss.h", "ortho.h", "ortho_table.cuh",
-           "ortho_steps.cuh"]
+           "ortho_steps.cuh", "grads.h", "verify.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # Per-file nvcc flags (none at present).

@@ -1,0 +1,230 @@
+// Host side of the gradient norm, clipping and AdamW: argument checks and
+// launches (see include/ar.h).
+#include <algorithm>
+#include <cmath>
+#include <new>
+#include <vector>
+
+#include "grads.h"
+#include "internal.h"
+
+namespace {
+
+using namespace ar;
+
+constexpr int64_t kMaxCount = int64_t(1) << 40;
+
+int64_t esize(ar_dtype d) { return d == AR_BF16 ? 2 : 4; }
+bool aligned(const void* p, size_t a) { return p != nullptr && reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+bool valid(const ar_tensor& t) {
+  if (t.count < 0 || t.count > kMaxCount || (t.dtype != AR_F32 && t.dtype != AR_BF16)) return false;
+  return t.count == 0 || aligned(t.data, size_t(esize(t.dtype)));
+}
+bool valid(const ar_tensor* t, int n) {
+  return t != nullptr && std::all_of(t, t + n, [](const ar_tensor& v) { return valid(v); });
+}
+
+// Memory that a call reads or writes.
+struct Range {
+  uintptr_t lo, hi;
+  bool write;
+};
+Range range(const void* p, int64_t bytes, bool write) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return {a, a + uintptr_t(bytes), write};
+}
+Range range(const ar_tensor& t, bool write) { return range(t.data, t.count * esize(t.dtype), write); }
+
+// No written range overlaps another one. (Lists are mostly in the order of
+// their addresses already; those that are not are sorted.)
+bool apart(std::vector<Range>& v) {
+  v.erase(std::remove_if(v.begin(), v.end(), [](const Range& r) { return r.lo >= r.hi; }), v.end());
+  const auto by_lo = [](const Range& a, const Range& b) { return a.lo < b.lo; };
+  if (!std::is_sorted(v.begin(), v.end(), by_lo)) std::sort(v.begin(), v.end(), by_lo);
+  uintptr_t written = 0, any = 0;  // the ends so far
+  for (const Range& r : v) {
+    if (r.lo < written || (r.write && r.lo < any)) return false;
+    any = std::max(any, r.hi);
+    if (r.write) written = std::max(written, r.hi);
+  }
+  return true;
+}
+
+ar_status device_ready() {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return AR_ECUDA;
+  volatile unsigned int* word = nullptr;
+  if (host_status_word(dev, &word) != cudaSuccess) return AR_ECUDA;
+  return *word != 0 ? AR_ETIMEOUT : AR_OK;
+}
+
+ar_status from_cuda(cudaError_t e) { return e == cudaSuccess ? AR_OK : AR_ECUDA; }
+
+ar_status count_ok(int n) { return n < 1 ? AR_EINVAL : n > AR_MAX_TENSORS ? AR_EUNSUPPORTED : AR_OK; }
+
+ar_status grad_norm(const ar_tensor* grads, int n, const ar_tensor* outs, bool clip, const ar_norm_desc* desc,
+                    float* stats, float* norms, void* workspace, void* stream) {
+  if (grads == nullptr || desc == nullptr) return AR_EINVAL;
+  ar_status s = count_ok(n);
+  if (s != AR_OK) return s;
+  if (desc->kind != AR_NORM_L2 && desc->kind != AR_NORM_MAX) return AR_EINVAL;
+  if (!(desc->max_norm > 0.0) || !(desc->eps >= 0.0) || !std::isfinite(desc->eps) || !std::isfinite(desc->grad_scale))
+    return AR_EINVAL;
+  if (!aligned(stats, 4) || !aligned(workspace, 16) || (norms != nullptr && !aligned(norms, 4))) return AR_EINVAL;
+  if (!valid(grads, n) || (outs != nullptr && !valid(outs, n))) return AR_EINVAL;
+  std::vector<GradTensor> t(n);
+  std::vector<Range> ranges;
+  ranges.reserve(size_t(2 * n + 3));
+  for (int i = 0; i < n; ++i) {
+    const ar_tensor& in = grads[i];
+    const ar_tensor& out = outs != nullptr ? outs[i] : in;
+    if (out.count != in.count || out.dtype != in.dtype) return AR_EINVAL;
+    t[i] = {static_cast<const char*>(in.data), static_cast<char*>(out.data), in.count, in.dtype == AR_BF16};
+    if (!clip || out.data != in.data) ranges.push_back(range(in, false));
+    if (clip) ranges.push_back(range(out, true));
+  }
+  ranges.push_back(range(stats, 16, true));
+  ranges.push_back(range(norms, norms != nullptr ? 4 * int64_t(n) : 0, true));
+  ranges.push_back(range(workspace, kGradWorkspace, true));
+  if (!apart(ranges)) return AR_EINVAL;
+  if ((s = device_ready()) != AR_OK) return s;
+  GradJob job = {};
+  job.kind = desc->kind;
+  job.max_norm = desc->max_norm;
+  job.eps = desc->eps;
+  job.grad_scale = desc->grad_scale;
+  job.stats = stats;
+  job.norms = norms;
+  job.groups = static_cast<double*>(workspace);
+  job.partials = reinterpret_cast<double*>(static_cast<char*>(workspace) + kGradPartials);
+  return from_cuda(launch_grad_norm(t.data(), n, clip, job, static_cast<cudaStream_t>(stream)));
+}
+
+// Elements between a multiple of 8 and the first one; 255 where the arrays do
+// not agree (16-byte accesses need a multiple of 4 of fp32, of 8 of bf16).
+struct Phase {
+  int of8 = -1, of4 = -1;
+  bool alike = true;
+  void add(const void* p, bool bf16) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p) / (bf16 ? 2 : 4);
+    if (bf16) {
+      alike = alike && (of8 < 0 || of8 == int(at % 8));
+      of8 = int(at % 8);
+    }
+    alike = alike && (of4 < 0 || of4 == int(at % 4));
+    of4 = int(at % 4);
+  }
+  uint8_t value() const { return !alike ? 255 : uint8_t(of8 >= 0 ? of8 : of4); }
+};
+
+}  // namespace
+
+extern "C" {
+
+ar_status ar_grad_workspace(int n_tensors, size_t* bytes) {
+  if (bytes == nullptr) return AR_EINVAL;
+  const ar_status s = count_ok(n_tensors);
+  if (s == AR_OK) *bytes = size_t(kGradWorkspace);
+  return s;
+}
+
+ar_status ar_grad_norm(const ar_tensor* grads, int n_tensors, const ar_norm_desc* desc, float* stats, float* norms,
+                       void* workspace, void* stream) try {
+  return grad_norm(grads, n_tensors, nullptr, false, desc, stats, norms, workspace, stream);
+} catch (const std::bad_alloc&) {
+  return AR_ENOMEM;
+}
+
+ar_status ar_grad_clip(const ar_tensor* grads, int n_tensors, const ar_tensor* outs, const ar_norm_desc* desc,
+                       float* stats, float* norms, void* workspace, void* stream) try {
+  return grad_norm(grads, n_tensors, outs, true, desc, stats, norms, workspace, stream);
+} catch (const std::bad_alloc&) {
+  return AR_ENOMEM;
+}
+
+ar_status ar_adamw_step(const ar_adamw_desc* desc, int n_tensors, const ar_tensor* params, const ar_tensor* grads,
+                        const ar_tensor* exp_avgs, const ar_tensor* exp_avg_sqs, const ar_tensor* masters,
+                        const ar_tensor* params_out, const ar_tensor* exp_avgs_out, const ar_tensor* exp_avg_sqs_out,
+                        const ar_tensor* masters_out, const float* clip, void* stream) try {
+  if (desc == nullptr) return AR_EINVAL;
+  ar_status s = count_ok(n_tensors);
+  if (s != AR_OK) return s;
+  if (!std::isfinite(desc->lr) || !std::isfinite(desc->weight_decay) || !(desc->eps >= 0.0) || !std::isfinite(desc->eps) ||
+      !(desc->beta1 >= 0.0 && desc->beta1 < 1.0) || !(desc->beta2 >= 0.0 && desc->beta2 < 1.0) ||
+      !std::isfinite(desc->grad_scale))
+    return AR_EINVAL;
+  if (desc->device_step == nullptr ? desc->step < 1 : !aligned(desc->device_step, 8)) return AR_EINVAL;
+  if (clip != nullptr && !aligned(clip, 4)) return AR_EINVAL;
+  if (masters == nullptr && masters_out != nullptr) return AR_EINVAL;
+  if (params_out == nullptr) params_out = params;
+  if (exp_avgs_out == nullptr) exp_avgs_out = exp_avgs;
+  if (exp_avg_sqs_out == nullptr) exp_avg_sqs_out = exp_avg_sqs;
+  if (masters_out == nullptr) masters_out = masters;
+  const int n = n_tensors;
+  for (const ar_tensor* list : {params, grads, exp_avgs, exp_avg_sqs, params_out, exp_avgs_out, exp_avg_sqs_out})
+    if (!valid(list, n)) return AR_EINVAL;
+  std::vector<AdamEntry> e(n);
+  std::vector<Range> ranges;
+  ranges.reserve(size_t(9 * n + 2));
+  bool in_place = true;
+  const auto pair = [&](const ar_tensor& in, const ar_tensor& out) {
+    if (in.data != out.data) {
+      ranges.push_back(range(in, false));
+      in_place = false;
+    }
+    ranges.push_back(range(out, true));
+  };
+  for (int i = 0; i < n; ++i) {
+    const ar_tensor &p = params[i], &g = grads[i], &m = exp_avgs[i], &v = exp_avg_sqs[i], &po = params_out[i],
+                    &mo = exp_avgs_out[i], &vo = exp_avg_sqs_out[i];
+    for (const ar_tensor* t : {&g, &m, &v, &po, &mo, &vo})
+      if (t->count != p.count) return AR_EINVAL;
+    if (po.dtype != p.dtype) return AR_EINVAL;
+    for (const ar_tensor* t : {&m, &v, &mo, &vo})
+      if (t->dtype != AR_F32) return AR_EINVAL;
+    const bool has_master = masters != nullptr && masters[i].data != nullptr && p.count > 0;
+    if (masters != nullptr && (masters_out[i].data != nullptr) != (masters[i].data != nullptr)) return AR_EINVAL;
+    if (has_master)
+      for (const ar_tensor* t : {&masters[i], &masters_out[i]})
+        if (!valid(*t) || t->count != p.count || t->dtype != AR_F32) return AR_EINVAL;
+    const ar_tensor &w = has_master ? masters[i] : p, &wo = has_master ? masters_out[i] : po;
+    e[i] = {g.data, w.data, static_cast<const float*>(m.data), static_cast<const float*>(v.data), wo.data,
+            has_master ? po.data : nullptr, static_cast<float*>(mo.data), static_cast<float*>(vo.data), p.count, 0,
+            uint8_t(g.dtype == AR_BF16), uint8_t(w.dtype == AR_BF16), uint8_t(p.dtype == AR_BF16), 0};
+    Phase ph;
+    ph.add(g.data, g.dtype == AR_BF16);
+    for (const void* f : {static_cast<const void*>(m.data), static_cast<const void*>(v.data),
+                          static_cast<const void*>(mo.data), static_cast<const void*>(vo.data)})
+      ph.add(f, false);
+    ph.add(w.data, w.dtype == AR_BF16);
+    ph.add(wo.data, w.dtype == AR_BF16);
+    if (has_master) ph.add(po.data, p.dtype == AR_BF16);
+    e[i].phase = ph.value();
+    ranges.push_back(range(g, false));
+    pair(m, mo);
+    pair(v, vo);
+    pair(w, wo);
+    if (has_master) ranges.push_back(range(po, true));
+  }
+  if (clip != nullptr) ranges.push_back(range(clip, 16, false));
+  if (desc->device_step != nullptr) ranges.push_back(range(desc->device_step, 8, false));
+  if (!apart(ranges)) return AR_EINVAL;
+  if ((s = device_ready()) != AR_OK) return s;
+  AdamJob job = {};
+  job.rates = {float(desc->beta1), float(desc->beta2), float(1.0 - desc->beta1), float(1.0 - desc->beta2), 0.0f, 0.0f,
+               float(desc->eps), float(1.0 - desc->lr * desc->weight_decay)};
+  adam_rates(desc->lr, desc->beta1, desc->beta2, std::max<int64_t>(desc->step, 1), job.rates);
+  job.device_step = desc->device_step;
+  job.lr = desc->lr;
+  job.beta1 = desc->beta1;
+  job.beta2 = desc->beta2;
+  job.clip = clip;
+  job.grad_scale = desc->grad_scale;
+  job.in_place = in_place;
+  return from_cuda(launch_adamw(e.data(), n, job, static_cast<cudaStream_t>(stream)));
+} catch (const std::bad_alloc&) {
+  return AR_ENOMEM;
+}
+
+}  // extern "C"

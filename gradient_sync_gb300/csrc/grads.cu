@@ -1,0 +1,552 @@
+// The global norm of many gradient tensors, clipping, and the AdamW step.
+//
+// norm:   N = sqrt(sum over all tensors of |s g|^2), or the largest |s g|;
+//         c = min(1, max_norm / (N + eps))
+// clip:   out = (c s) g
+// AdamW:  M' = b1 M + (1 - b1) G, V' = b2 V + (1 - b2) G^2, G = (c s) g,
+//         W' = (1 - lr wd) W - lr / (1 - b1^t) M' / (sqrt(V' / (1 - b2^t)) + eps)
+//
+// All of it is bound by HBM where there is much, by launches where there is
+// little: two to six operations an element against 2 to 32 bytes.
+//
+// A list of tensors is one sequence of granules, 16 aligned bytes each, and a
+// warp takes a stretch of it: whatever the tensors' sizes, every warp has equal
+// work, and a tensor's sum is that of the stretches it lies in. A stretch and a
+// tensor meet at most once, so that the sum of warp w over tensor i has a place
+// of its own, w + i, and nothing is added in an order that timing could change.
+#include "grads.h"
+
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace ar {
+namespace {
+
+constexpr int kNormThreads = 512;
+constexpr int kLoads = 8;  // 16-byte loads in flight a thread
+
+__device__ __forceinline__ uint4 load16(const char* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
+// Sum of squares of a batch in 64 bits, from memory again: squares of fp32
+// numbers are exact there and within range.
+template <bool BF16>
+__device__ __noinline__ double squares_wide(const char* base, int64_t g, int64_t hi) {
+  double s = 0.0;
+#pragma unroll 1
+  for (int i = 0; i < kLoads && g < hi; ++i, g += 32) {
+    const uint4 r = load16(base + 16 * g);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const double a = BF16 ? double(bf16lo(w[j])) : double(__uint_as_float(w[j])), b = BF16 ? double(bf16hi(w[j])) : 0.0;
+      s += a * a + b * b;
+    }
+  }
+  return s;
+}
+
+// The sum of squares of a batch, the granules g, g + 32, ... below hi: fp32
+// within it (at most 64 terms), 64 bits beyond. Where fp32 squares could have
+// overflowed, or have been lost below its range, the batch is summed in 64 bits.
+template <bool BF16>
+__device__ __forceinline__ double squares(const uint4 (&r)[kLoads], const char* base, int64_t g, int64_t hi) {
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = BF16 ? bf16lo(w[j]) : __uint_as_float(w[j]);
+      s[j] = fmaf(a, a, s[j]);
+      if (BF16) s[j] = fmaf(bf16hi(w[j]), bf16hi(w[j]), s[j]);
+      any |= w[j];
+    }
+  }
+  const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+  if (sum > 1e-25f && sum < 1e37f) return double(sum);
+  if ((any & (BF16 ? 0x7fff7fffu : 0x7fffffffu)) == 0) return 0.0;
+  return squares_wide<BF16>(base, g, hi);
+}
+
+// Magnitudes as integers order like the numbers, NaN above infinity.
+template <bool BF16>
+__device__ __forceinline__ uint32_t largest(const uint4 (&r)[kLoads], uint32_t top) {
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (BF16) {
+        top = max(top, (w[j] << 16) & 0x7fffffffu);
+        top = max(top, w[j] & 0x7fff0000u);
+      } else {
+        top = max(top, w[j] & 0x7fffffffu);
+      }
+    }
+  }
+  return top;
+}
+
+// A tensor as granules: `lead` elements of the first one lie before it.
+struct Span {
+  const char* base;  // of granule 0
+  int64_t count, granules, full;  // granules below `full` end inside the tensor
+  int es, lead;
+  __device__ Span(const char* p, int64_t count_kind) {
+    count = count_kind >> 1;
+    es = (count_kind & 1) ? 2 : 4;
+    const int off = int(reinterpret_cast<uintptr_t>(p) & 15);
+    base = p - off;
+    lead = off / es;
+    granules = ((lead + count) * es + 15) >> 4;
+    full = ((lead + count) * es) >> 4;
+  }
+  // The elements that are not in whole granules, one a lane (-1: none).
+  __device__ int64_t edge(int64_t g0, int64_t g1, int lane) const {
+    const int per = 16 / es;
+    const int64_t head = lead > 0 ? min(count, int64_t(per - lead)) : 0;
+    const int64_t tail = max(head, full * per - lead);
+    if (lane < per) return g0 == 0 && lane < head ? lane : -1;
+    const int64_t e = tail + lane - per;
+    return g1 == granules && e < count && lane < 2 * per ? e : -1;
+  }
+};
+
+__device__ __forceinline__ float element(const char* p, int64_t e, int es) {
+  return es == 2 ? bf16_to_f32(reinterpret_cast<const uint16_t*>(p)[e]) : reinterpret_cast<const float*>(p)[e];
+}
+
+// The entry that granule g lies in.
+template <class Table>
+__device__ __forceinline__ int entry_of(const Table& t, int64_t g) {
+  int lo = 0, hi = t.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (t.e[mid].first <= g) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Granules a warp: a multiple of 32, so that its loads are whole lines.
+__host__ __device__ inline int64_t stretch(int64_t granules, int64_t warps) {
+  return (granules + warps * 32 - 1) / (warps * 32) * 32;
+}
+
+template <bool BF16>
+__device__ __forceinline__ double squares_of(const char* base, int64_t lo, int64_t hi, int lane) {
+  double sum = 0.0;
+  int64_t g = lo + lane;
+  uint4 r[kLoads];
+  for (; g + 32 * (kLoads - 1) < hi; g += 32 * kLoads) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) r[i] = load16(base + 16 * (g + 32 * i));
+    sum += squares<BF16>(r, base, g, hi);
+  }
+  if (g < hi) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) r[i] = g + 32 * i < hi ? load16(base + 16 * (g + 32 * i)) : make_uint4(0, 0, 0, 0);
+    sum += squares<BF16>(r, base, g, hi);
+  }
+  return sum;
+}
+
+template <bool BF16>
+__device__ __forceinline__ double largest_of(const char* base, int64_t lo, int64_t hi, int lane) {
+  uint32_t top = 0;
+  uint4 r[kLoads];
+  for (int64_t g = lo + lane; g < hi; g += 32 * kLoads) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) r[i] = g + 32 * i < hi ? load16(base + 16 * (g + 32 * i)) : make_uint4(0, 0, 0, 0);
+    top = largest<BF16>(r, top);
+  }
+  return double(__uint_as_float(top));
+}
+
+// The larger one; a NaN where either is.
+__device__ __forceinline__ double larger(double a, double b) { return a >= b || a != a ? a : b; }
+
+template <bool MAX>
+__device__ __forceinline__ double warp_join(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const double u = __shfl_xor_sync(~0u, v, o);
+    v = MAX ? larger(v, u) : v + u;
+  }
+  return v;
+}
+
+// Every warp's sum over each tensor that its stretch meets.
+template <int CAP, bool MAX>
+__global__ void __launch_bounds__(kNormThreads) norm_kernel(const __grid_constant__ GradTable<CAP> t, GradJob job) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int lane = threadIdx.x % 32;
+  const int64_t warps = int64_t(gridDim.x) * (kNormThreads / 32);
+  const int64_t w = int64_t(blockIdx.x) * (kNormThreads / 32) + threadIdx.x / 32;
+  const int64_t per = stretch(t.granules, warps);
+  const int64_t lo = w * per, hi = min(t.granules, lo + per);
+  if (lo >= hi) return;
+  for (int i = entry_of(t, lo); i < t.n && t.e[i].first < hi; ++i) {
+    const Span s(t.e[i].in, t.e[i].count);
+    const int64_t g0 = max(lo - t.e[i].first, int64_t(0)), g1 = min(hi - t.e[i].first, s.granules);
+    if (g0 >= g1) continue;
+    const int64_t a = max(g0, int64_t(s.lead > 0)), b = min(g1, s.full);
+    double v;
+    if (MAX) v = s.es == 2 ? largest_of<true>(s.base, a, b, lane) : largest_of<false>(s.base, a, b, lane);
+    else v = s.es == 2 ? squares_of<true>(s.base, a, b, lane) : squares_of<false>(s.base, a, b, lane);
+    const int64_t e = s.edge(g0, g1, lane);
+    if (e >= 0) {
+      const double x = double(element(t.e[i].in, e, s.es));
+      v = MAX ? larger(v, fabs(x)) : v + x * x;
+    }
+    v = warp_join<MAX>(v);
+    if (lane == 0) job.partials[w + i] = v;
+  }
+}
+
+__device__ __forceinline__ void write_stats(const GradJob& job, double total) {
+  const double scale = fabs(double(job.grad_scale));
+  const double norm = (job.kind == AR_NORM_MAX ? total : sqrt(total)) * scale;
+  const bool finite = isfinite(total);
+  const double ratio = job.max_norm / (norm + job.eps);
+  const float c = !finite ? 0.0f : ratio < 1.0 ? float(ratio) : 1.0f;
+  job.stats[0] = float(norm);
+  job.stats[1] = c;
+  job.stats[2] = c < 1.0f ? 1.0f : 0.0f;
+  job.stats[3] = finite ? 1.0f : 0.0f;
+}
+
+// One CTA: the tensors' norms from the warps' sums; behind the last launch of a
+// call, the statistics.
+template <int CAP, bool MAX>
+__global__ void __launch_bounds__(1024) finish_kernel(const __grid_constant__ GradTable<CAP> t, GradJob job, int64_t warps,
+                                                      int group, int groups) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  extern __shared__ double part[];
+  __shared__ double sums[32];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t per = stretch(t.granules, warps);
+  const int used = int(t.granules > 0 ? (t.granules - 1) / per + t.n : 0);
+  for (int i = threadIdx.x; i < used; i += 1024) part[i] = job.partials[i];
+  __syncthreads();
+  const float scale = fabsf(job.grad_scale);
+  double mine = 0.0;
+  for (int i = warp; i < t.n; i += 32) {
+    const int64_t first = t.e[i].first, end = i + 1 < t.n ? t.e[i + 1].first : t.granules;
+    double v = 0.0;
+    if (end > first)
+      for (int j = int(first / per) + i + lane; j <= int((end - 1) / per) + i; j += 32) v = MAX ? larger(v, part[j]) : v + part[j];
+    v = warp_join<MAX>(v);
+    if (lane == 0 && job.norms != nullptr) job.norms[i] = float((MAX ? v : sqrt(v)) * scale);
+    mine = MAX ? larger(mine, v) : mine + v;
+  }
+  if (lane == 0) sums[warp] = mine;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double total = 0.0;
+    for (int i = 0; i < 32; ++i) total = MAX ? larger(total, sums[i]) : total + sums[i];
+    if (group + 1 < groups) {
+      job.groups[group] = total;
+    } else {
+      for (int i = 0; i < group; ++i) total = MAX ? larger(total, job.groups[i]) : total + job.groups[i];
+      write_stats(job, total);
+    }
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 scaled(const uint4& r, float f) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    o[j] = BF16 ? pack_bf16x2(bf16lo(w[j]) * f, bf16hi(w[j]) * f) : __float_as_uint(__uint_as_float(w[j]) * f);
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+__device__ __forceinline__ void store_element(char* p, int64_t e, int es, float v) {
+  if (es == 2) reinterpret_cast<uint16_t*>(p)[e] = f32_to_bf16(v);
+  else reinterpret_cast<float*>(p)[e] = v;
+}
+
+// Granules [lo, hi) of a tensor, times f; `zero`: zeros, whatever they hold.
+template <bool BF16>
+__device__ __forceinline__ void scale_granules(const char* base, char* out, int64_t lo, int64_t hi, int lane, float f,
+                                               bool zero) {
+  // From the end: what the norm read last is still in the L2.
+  for (int64_t n = (hi - lo + 32 * kLoads - 1) / (32 * kLoads); n > 0; --n) {
+    const int64_t g = lo + (n - 1) * 32 * kLoads + lane;
+    uint4 r[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      r[i] = g + 32 * i < hi && !zero ? load16(base + 16 * (g + 32 * i)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      if (g + 32 * i < hi) __stcs(reinterpret_cast<uint4*>(out + 16 * (g + 32 * i)), scaled<BF16>(r[i], f));
+  }
+}
+
+// The scaled gradients, stretch by stretch as the norm read them.
+template <int CAP>
+__global__ void __launch_bounds__(kNormThreads) scale_kernel(const __grid_constant__ GradTable<CAP> t, GradJob job) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int lane = threadIdx.x % 32;
+  const int64_t warps = int64_t(gridDim.x) * (kNormThreads / 32);
+  const int64_t w = int64_t(blockIdx.x) * (kNormThreads / 32) + threadIdx.x / 32;
+  const int64_t per = stretch(t.granules, warps);
+  const int64_t lo = w * per, hi = min(t.granules, lo + per);
+  if (lo >= hi) return;
+  const bool zero = job.stats[3] == 0.0f;
+  const float f = zero ? 0.0f : job.stats[1] * job.grad_scale;
+  for (int i = entry_of(t, hi - 1); i >= 0; --i) {
+    const GradEntry& e = t.e[i];
+    const Span s(e.in, e.count);
+    const int64_t g0 = max(lo - e.first, int64_t(0)), g1 = min(hi - e.first, s.granules);
+    if (g0 < g1 && !(f == 1.0f && e.in == e.out)) {
+      if (((e.in - e.out) & 15) == 0) {
+        const int64_t a = max(g0, int64_t(s.lead > 0)), b = min(g1, s.full);
+        char* out = e.out - s.lead * s.es;
+        if (s.es == 2) scale_granules<true>(s.base, out, a, b, lane, f, zero);
+        else scale_granules<false>(s.base, out, a, b, lane, f, zero);
+        const int64_t x = s.edge(g0, g1, lane);
+        if (x >= 0) store_element(e.out, x, s.es, zero ? 0.0f : element(e.in, x, s.es) * f);
+      } else {
+        const int p = 16 / s.es;
+        const int64_t from = max(g0 * p - s.lead, int64_t(0)), to = min(g1 * p - s.lead, s.count);
+#pragma unroll 8
+        for (int64_t x = from + lane; x < to; x += 32)
+          store_element(e.out, x, s.es, zero ? 0.0f : element(e.in, x, s.es) * f);
+      }
+    }
+    if (e.first <= lo) break;
+  }
+}
+
+// ---------------------------------------------------------------- AdamW
+
+constexpr int kAdamThreads = 256;
+
+__device__ __forceinline__ void load8(const void* p, int64_t e, bool bf16, float (&x)[8]) {
+  if (bf16) {
+    const uint4 r = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + e));
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[2 * j] = bf16lo(w[j]), x[2 * j + 1] = bf16hi(w[j]);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 r = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(p) + e + 4 * h));
+      x[4 * h] = r.x, x[4 * h + 1] = r.y, x[4 * h + 2] = r.z, x[4 * h + 3] = r.w;
+    }
+  }
+}
+__device__ __forceinline__ void store8(void* p, int64_t e, bool bf16, const float (&x)[8]) {
+  if (bf16) {
+    __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + e),
+           make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      __stcs(reinterpret_cast<float4*>(static_cast<float*>(p) + e + 4 * h),
+             make_float4(x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]));
+  }
+}
+__device__ __forceinline__ float load1(const void* p, int64_t e, bool bf16) {
+  return element(static_cast<const char*>(p), e, bf16 ? 2 : 4);
+}
+__device__ __forceinline__ void store1(void* p, int64_t e, bool bf16, float v) {
+  store_element(static_cast<char*>(p), e, bf16 ? 2 : 4, v);
+}
+
+struct AdamStep {
+  AdamRates r;
+  float factor;
+  bool skip;
+  __device__ __forceinline__ void operator()(float g, float& w, float& m, float& v) const {
+    if (skip) return;
+    g *= factor;
+    m = fmaf(r.beta1, m, r.rest1 * g);
+    v = fmaf(r.beta2, v, r.rest2 * (g * g));
+    w = fmaf(w, r.keep, -(r.rate * m) / fmaf(sqrtf(v), r.inv_root, r.eps));
+  }
+};
+
+__device__ __forceinline__ void adam_one(const AdamEntry& e, int64_t x, const AdamStep& step) {
+  float w = load1(e.w, x, e.w_bf16), m = e.m[x], v = e.v[x];
+  step(load1(e.g, x, e.g_bf16), w, m, v);
+  e.m_out[x] = m;
+  e.v_out[x] = v;
+  store1(e.w_out, x, e.w_bf16, w);
+  if (e.p_out != nullptr) store1(e.p_out, x, e.p_bf16, w);
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamTable<CAP> t, AdamJob job) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  AdamStep step = {job.rates, job.grad_scale, false};
+  if (job.device_step != nullptr) {
+    __shared__ AdamRates rates;
+    if (threadIdx.x == 0) {
+      rates = job.rates;
+      adam_rates(job.lr, job.beta1, job.beta2, max(*job.device_step, int64_t(1)), rates);
+    }
+    __syncthreads();
+    step.r = rates;
+  }
+  if (job.clip != nullptr) {
+    step.factor = job.clip[1] * job.grad_scale;
+    step.skip = job.clip[3] == 0.0f;
+    if (step.skip && job.in_place) return;
+  }
+  for (int tile = blockIdx.x; tile < t.tiles; tile += gridDim.x) {
+    const int at = entry_of(t, tile);
+    const AdamEntry& e = t.e[at];
+    const int64_t from = int64_t(tile - e.first) * kAdamTile;
+    if (e.phase == 255) {
+      const int64_t to = min(e.count, from + kAdamTile);
+      for (int64_t x = from + threadIdx.x; x < to; x += kAdamThreads) adam_one(e, x, step);
+      continue;
+    }
+    // groups of 8 elements at multiples of 8 in memory
+#pragma unroll
+    for (int i = 0; i < kAdamTile / (8 * kAdamThreads); ++i) {
+      const int64_t x = from + 8 * (i * kAdamThreads + int(threadIdx.x)) - e.phase;
+      if (x >= 0 && x + 8 <= e.count) {
+        float g[8], w[8], m[8], v[8];
+        load8(e.g, x, e.g_bf16, g);
+        load8(e.w, x, e.w_bf16, w);
+        load8(e.m, x, false, m);
+        load8(e.v, x, false, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) step(g[j], w[j], m[j], v[j]);
+        store8(e.m_out, x, false, m);
+        store8(e.v_out, x, false, v);
+        store8(e.w_out, x, e.w_bf16, w);
+        if (e.p_out != nullptr) store8(e.p_out, x, e.p_bf16, w);
+      } else {
+        for (int64_t y = max(x, int64_t(0)); y < min(x + 8, e.count); ++y) adam_one(e, y, step);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- launches
+
+// Launched so that it may be scheduled while the kernel before it drains; every
+// kernel here waits for that one before it touches memory.
+template <class... Params, class... Args>
+cudaError_t launch(void (*kernel)(Params...), int64_t grid, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+int64_t granules_of(const GradTensor& t) {
+  const int64_t es = t.bf16 ? 2 : 4, off = int64_t(reinterpret_cast<uintptr_t>(t.in) & 15);
+  return t.count == 0 ? 0 : (off + t.count * es + 15) / 16;
+}
+
+template <int CAP>
+void fill(GradTable<CAP>& t, const GradTensor* g, int n) {
+  t.n = n;
+  t.granules = 0;
+  for (int i = 0; i < n; ++i) {
+    t.e[i] = {g[i].in, g[i].out, t.granules, g[i].count * 2 + (g[i].bf16 ? 1 : 0)};
+    t.granules += granules_of(g[i]);
+  }
+}
+
+// CTAs for a list: every warp has at least 2 granules a lane, every SM two CTAs.
+int64_t norm_ctas(int64_t granules) {
+  const int64_t warps = kNormThreads / 32, most = std::min<int64_t>(2 * device_sms(), kMaxGradWarps / warps);
+  return std::max<int64_t>(1, std::min<int64_t>(most, (granules + warps * 64 - 1) / (warps * 64)));
+}
+
+template <int CAP>
+cudaError_t launch_norm_group(const GradTensor* g, int n, const GradJob& job, int group, int groups, cudaStream_t stream) {
+  GradTable<CAP> t;
+  fill(t, g, n);
+  const int64_t ctas = norm_ctas(t.granules), warps = ctas * (kNormThreads / 32);
+  const bool max = job.kind == AR_NORM_MAX;
+  cudaError_t err = cudaSuccess;
+  if (t.granules > 0)
+    err = launch(max ? norm_kernel<CAP, true> : norm_kernel<CAP, false>, ctas, kNormThreads, 0, stream, t, job);
+  if (err != cudaSuccess) return err;
+  return launch(max ? finish_kernel<CAP, true> : finish_kernel<CAP, false>, 1, 1024, size_t(8 * (warps + n)), stream, t, job,
+                warps, group, groups);
+}
+
+template <int CAP>
+cudaError_t launch_scale_group(const GradTensor* g, int n, const GradJob& job, cudaStream_t stream) {
+  GradTable<CAP> t;
+  fill(t, g, n);
+  if (t.granules == 0) return cudaSuccess;
+  return launch(scale_kernel<CAP>, norm_ctas(t.granules), kNormThreads, 0, stream, t, job);
+}
+
+template <int CAP>
+cudaError_t launch_adam_group(const AdamEntry* e, int n, const AdamJob& job, cudaStream_t stream) {
+  AdamTable<CAP> t;
+  t.n = n;
+  int64_t tiles = 0;
+  for (int i = 0; i < n; ++i) {
+    t.e[i] = e[i];
+    t.e[i].first = int32_t(tiles);
+    if (e[i].count > 0) tiles += (e[i].count + (e[i].phase == 255 ? 0 : e[i].phase) + kAdamTile - 1) / kAdamTile;
+  }
+  if (tiles == 0) return cudaSuccess;
+  if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
+  t.tiles = int(tiles);
+  const int64_t ctas = std::min<int64_t>(tiles, 4 * device_sms());
+  return launch(adamw_kernel<CAP>, ctas, kAdamThreads, 0, stream, t, job);
+}
+
+}  // namespace
+
+cudaError_t launch_grad_norm(const GradTensor* g, int n, bool clip, const GradJob& job, cudaStream_t stream) {
+  const int groups = (n + kGradCap - 1) / kGradCap;
+  cudaError_t err = cudaSuccess;
+  for (int k = 0; k < groups && err == cudaSuccess; ++k) {
+    const int from = k * kGradCap, m = std::min(kGradCap, n - from);
+    GradJob part = job;
+    if (job.norms != nullptr) part.norms = job.norms + from;
+    err = n <= kGradCapSmall ? launch_norm_group<kGradCapSmall>(g, n, part, 0, 1, stream)
+                             : launch_norm_group<kGradCap>(g + from, m, part, k, groups, stream);
+  }
+  for (int k = groups - 1; clip && k >= 0 && err == cudaSuccess; --k) {
+    const int from = k * kGradCap, m = std::min(kGradCap, n - from);
+    err = n <= kGradCapSmall ? launch_scale_group<kGradCapSmall>(g, n, job, stream)
+                             : launch_scale_group<kGradCap>(g + from, m, job, stream);
+  }
+  return err;
+}
+
+cudaError_t launch_adamw(const AdamEntry* e, int n, const AdamJob& job, cudaStream_t stream) {
+  cudaError_t err = cudaSuccess;
+  for (int from = 0; from < n && err == cudaSuccess; from += kAdamCap)
+    err = n <= kAdamCapSmall ? launch_adam_group<kAdamCapSmall>(e, n, job, stream)
+                             : launch_adam_group<kAdamCap>(e + from, std::min(kAdamCap, n - from), job, stream);
+  return err;
+}
+
+}  // namespace ar

@@ -1,0 +1,108 @@
+// Declarations shared by the host side of the gradient norm, clipping and AdamW
+// (grads.cpp) and their kernels (grads.cu). Not part of the public ABI.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "../../include/ar.h"
+
+namespace ar {
+
+// Tensors of one launch: their table is a kernel argument (at most 32764 bytes
+// of those), so that neither a copy nor device memory of its own is needed and
+// a captured launch is complete in itself. Short lists take a short table.
+constexpr int kGradCap = 768, kGradCapSmall = 48;
+constexpr int kAdamCap = 360, kAdamCapSmall = 40;
+constexpr int kMaxGradWarps = 4864;  // warps of a norm launch: 32 an SM
+
+struct GradEntry {
+  const char* in;
+  char* out;      // clipping only
+  int64_t first;  // granules (16 aligned bytes) of the tensors before this one
+  int64_t count;  // elements * 2 + (1: bf16)
+};
+
+template <int CAP>
+struct GradTable {
+  int n;
+  int64_t granules;  // of all entries
+  GradEntry e[CAP];
+};
+
+// What the launches of one call have in common.
+struct GradJob {
+  int kind;  // ar_norm_kind
+  double max_norm, eps;
+  float grad_scale;
+  float* stats;
+  float* norms;      // may be null
+  double* groups;    // workspace: the sum (or maximum) of every launch's tensors
+  double* partials;  // workspace: [warps + tensors] of one launch
+};
+
+// Byte offsets of the workspace's parts, and its size.
+constexpr int kGradGroups = (AR_MAX_TENSORS + kGradCap - 1) / kGradCap;
+constexpr int64_t kGradPartials = (8 * kGradGroups + 255) / 256 * 256;
+constexpr int64_t kGradWorkspace = kGradPartials + 8 * (kMaxGradWarps + kGradCap);
+
+// A tensor of a call, as checked.
+struct GradTensor {
+  const char* in;
+  char* out;
+  int64_t count;
+  bool bf16;
+};
+
+struct AdamEntry {
+  const void* g;
+  const void* w;  // weights: the master, or the parameter
+  const float* m;
+  const float* v;
+  void* w_out;
+  void* p_out;  // the parameter beside a master; else null
+  float* m_out;
+  float* v_out;
+  int64_t count;
+  int32_t first;   // tiles of the tensors before this one
+  uint8_t g_bf16, w_bf16, p_bf16;
+  uint8_t phase;   // elements between a multiple of 8 and the first one, alike in all arrays; 255: not alike
+};
+
+template <int CAP>
+struct AdamTable {
+  int n;
+  int tiles;
+  AdamEntry e[CAP];
+};
+
+struct AdamRates {
+  float beta1, beta2, rest1, rest2;  // rest = 1 - beta
+  float rate;                        // lr / (1 - beta1^t)
+  float inv_root;                    // 1 / sqrt(1 - beta2^t)
+  float eps, keep;                   // keep = 1 - lr * weight_decay
+};
+
+struct AdamJob {
+  AdamRates rates;             // for a step that the host knows
+  const int64_t* device_step;  // null: it does
+  double lr, beta1, beta2;     // for one that it does not
+  const float* clip;           // null: none
+  float grad_scale;
+  bool in_place;               // every output is its input
+};
+
+constexpr int kAdamTile = 4096;  // elements
+
+// 1 - beta^t and what a step makes of it.
+__host__ __device__ inline void adam_rates(double lr, double beta1, double beta2, int64_t t, AdamRates& r) {
+  const double c1 = -expm1(double(t) * log(beta1)), c2 = -expm1(double(t) * log(beta2));
+  r.rate = float(lr / c1);
+  r.inv_root = float(1.0 / sqrt(c2));
+}
+
+cudaError_t launch_grad_norm(const GradTensor* t, int n, bool clip, const GradJob& job, cudaStream_t stream);
+cudaError_t launch_adamw(const AdamEntry* e, int n, const AdamJob& job, cudaStream_t stream);
+
+}  // namespace ar

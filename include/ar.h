@@ -728,6 +728,155 @@ ar_status ar_muon_step(const ar_ortho_plan_t* plan, const ar_muon_desc* desc, co
                        const ar_matrix* grads, const ar_matrix* momenta, const ar_matrix* params_out,
                        const ar_matrix* momenta_out, void* workspace, void* stream);
 
+/* ---------------------------------------------------------------- gradients
+ * Between the exchange and the weights: the global norm of many gradient
+ * tensors, the coefficient that clips it, and the AdamW step, for parameters
+ * that the orthogonalised step is not for (embeddings, heads, gains). The norm
+ * stays on the device: a step reads the coefficient that a norm call wrote, so
+ * that clipping costs no pass of its own.
+ *
+ * Every list may mix types; a tensor is `count` elements one behind the other,
+ * aligned to its element (16-byte alignment is not needed; lists whose
+ * addresses agree modulo 8 elements are the fastest). Lists of any length up to
+ * AR_MAX_TENSORS run in launches of some hundred tensors each. The addresses
+ * are part of the launches: a captured graph keeps no other host memory.       */
+#define AR_MAX_TENSORS 65536
+
+typedef struct {
+  void* data;     /* device; may be NULL where count is 0 */
+  int64_t count;  /* 0..2^40 */
+  ar_dtype dtype;
+} ar_tensor;
+
+typedef enum {
+  AR_NORM_L2 = 0, /* sqrt of the sum of squares over all elements of all tensors */
+  AR_NORM_MAX = 1 /* largest magnitude */
+} ar_norm_kind;
+
+typedef struct {
+  ar_norm_kind kind;
+  double max_norm;   /* > 0; infinity: the coefficient of finite gradients is 1 */
+  double eps;        /* >= 0 */
+  float grad_scale;  /* multiplies every gradient first, e.g. 1 / ranks after a sum */
+} ar_norm_desc;
+
+/* Device bytes (16-byte aligned) that the two calls below need for n_tensors
+ * tensors, whatever their sizes. Calls that overlap on the GPU need
+ * workspaces of their own. AR_EINVAL: NULL, n_tensors < 1; AR_EUNSUPPORTED:
+ * more than AR_MAX_TENSORS. */
+ar_status ar_grad_workspace(int n_tensors, size_t* bytes);
+
+/* stats[4] (device, fp32), of the scaled gradients:
+ *   [0] the norm N over all tensors, [1] the coefficient
+ *   c = min(1, max_norm / (N + eps)), [2] 1 where c < 1, else 0,
+ *   [3] 1 where every element is finite, else 0: c is 0 then.
+ * norms [n_tensors] (device, fp32; NULL: not wanted): each tensor's norm.
+ * Sums of squares are kept in 64 bits and cover all of fp32's range, whatever
+ * the elements' size; c is worked out in 64 bits. A NaN makes N NaN, else an
+ * infinity makes it infinite. The order of the sums depends on the list alone:
+ * equal calls give equal bits. */
+ar_status ar_grad_norm(const ar_tensor* grads, int n_tensors, const ar_norm_desc* desc, float* stats, float* norms,
+                       void* workspace, void* stream);
+
+/* The same, and outs[i] = c * grad_scale * grads[i], rounded to its type
+ * (one fp32 product by the fp32 factor); zeros where an element anywhere is
+ * not finite, so that a step with such gradients adds nothing to moments and
+ * weights but their decay. outs: the same counts and types; NULL, or an out
+ * at its gradient's own address: in place (where the factor is 1, nothing is
+ * written then). Otherwise no out overlaps another one or any gradient. */
+ar_status ar_grad_clip(const ar_tensor* grads, int n_tensors, const ar_tensor* outs, const ar_norm_desc* desc,
+                       float* stats, float* norms, void* workspace, void* stream);
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay; /* betas in [0, 1); eps >= 0 */
+  float grad_scale;          /* multiplies the gradients, as in ar_norm_desc */
+  int64_t step;              /* t >= 1, where device_step is NULL */
+  const int64_t* device_step; /* device: t is read there when the kernels run (a
+                                 captured step advances it itself); t < 1 counts as 1 */
+} ar_adamw_desc;
+
+/* One AdamW step on n_tensors tensors, in fp32:
+ *   G  = c * grad_scale * gradient      (c = clip[1], 1 where clip is NULL)
+ *   M' = beta1 M + (1 - beta1) G;  V' = beta2 V + (1 - beta2) G^2
+ *   W' = (1 - lr weight_decay) W - lr / (1 - beta1^t) M' / (sqrt(V' / (1 - beta2^t)) + eps)
+ * clip (device): the stats of ar_grad_norm or ar_grad_clip with the same
+ * grad_scale (after ar_grad_clip the outs are scaled already: NULL then);
+ * where it says that an element was not finite, the step is skipped: every
+ * output is its input.
+ * params fp32 or bf16, each as it is; moments fp32. masters (NULL, or a list in
+ * which a tensor without a master has data NULL): fp32 weights W that are
+ * updated in the parameters' place; the parameter itself is not read then, and
+ * written with W' rounded once. The four *_out lists may be NULL, or name the inputs
+ * themselves: in place. Otherwise no two arrays of the call overlap, but for
+ * gradients with one another. masters_out needs masters. */
+ar_status ar_adamw_step(const ar_adamw_desc* desc, int n_tensors, const ar_tensor* params, const ar_tensor* grads,
+                        const ar_tensor* exp_avgs, const ar_tensor* exp_avg_sqs, const ar_tensor* masters,
+                        const ar_tensor* params_out, const ar_tensor* exp_avgs_out,
+                        const ar_tensor* exp_avg_sqs_out, const ar_tensor* masters_out, const float* clip,
+                        void* stream);
+
+/* ---------------------------------------------------------------- drafts
+ * Rollouts with drafted tokens: a cheap policy q proposes tokens, the target p
+ * scores all of them at once, and this call keeps as many as leave the tokens
+ * distributed as p's own. Sequence s has the drafted tokens
+ * draft_start[s] .. draft_start[s + 1] - 1, K_s of them (0 too), and K_s + 1 rows of
+ * target logits: row draft_start[s] + s + j is the distribution p_j of the token
+ * in draft j's place, j = K_s that of the token behind them all. Per sequence, with
+ * draft x_j, its uniform number u_j (that of its row) and the last row's u:
+ *   draft j stands while  u_j < p_j(x_j) / q_j(x_j);  a = the first that does
+ *   not, or K_s
+ *   one token is drawn behind the standing ones, from w = max(p_a - q_a, 0), or
+ *   w = p_a where a = K_s: the first i whose w_0 + .. + w_i passes u * sum(w)
+ * (the speculative sampling of Leviathan et al. 2023 and Chen et al. 2023). p and
+ * q are softmaxes of logits / temperature. Weights below 2^-125 of the largest
+ * count as 0. Sums that decide a draw are kept to 64 bits, their terms to fp32.  */
+typedef enum {
+  AR_VERIFY_SAMPLE = 0, /* as above; without draft logits q_j is 1 at x_j */
+  AR_VERIFY_GREEDY = 1  /* draft j stands while it is the first largest logit of its
+                           row, and the token drawn is the first largest of row a:
+                           no uniforms, no draft logits */
+} ar_verify_mode;
+
+typedef struct {
+  const void* data; /* device; row t at data + t * ld elements */
+  int64_t rows, ld; /* ld >= vocab */
+  ar_dtype dtype;
+  float temperature; /* > 0 */
+} ar_score_rows;
+
+typedef struct {
+  ar_score_rows target;       /* rows = n_drafts + n_seq */
+  ar_score_rows draft;        /* rows = n_drafts; data NULL: no draft distributions */
+  int64_t vocab;              /* 1..2^30, of both */
+  const int64_t* drafts;      /* device, [n_drafts] */
+  const float* uniforms;      /* device, [n_drafts + n_seq], in [0, 1); greedy: not read */
+  const int64_t* draft_start; /* device, [n_seq + 1], ascending; NULL: one sequence */
+  int64_t n_drafts;           /* >= 0 */
+  int64_t n_seq;              /* >= 1 */
+  ar_verify_mode mode;
+} ar_verify_desc;
+
+/* Device bytes (16-byte aligned) that the call below needs. Calls that overlap
+ * on the GPU need workspaces of their own. */
+ar_status ar_verify_workspace(int64_t n_drafts, int64_t n_seq, int64_t vocab, size_t* bytes);
+
+/* accepted [n_seq] (int64): a. tokens [n_drafts + n_seq] (int64), laid out like
+ * the target's rows: the standing drafts, the drawn token, then -1. logp
+ * [n_drafts + n_seq] (fp32): the tokens' log-probabilities under the target,
+ * 0 where the token is -1: with the tokens as labels, the old_logp of
+ * ar_policy_loss. Rows outside every sequence are neither read nor written;
+ * offsets outside [0, n_drafts], or descending, are clamped.
+ * A draft outside the vocabulary never stands. A row with a NaN, a +infinity
+ * or nothing but -infinity is no distribution: no draft stands there, and the
+ * token drawn from it is -1 with log-probability NaN. A residue w without
+ * weight (p = q but for rounding) is replaced by p. Uniforms outside [0, 1) count as
+ * the nearest number inside, NaN as 0 (and a NaN's draft falls).
+ * AR_EINVAL: NULL or misaligned pointers, bad sizes, types or temperatures,
+ * rows that do not match, outputs that overlap anything; AR_EUNSUPPORTED:
+ * n_drafts + n_seq >= 2^31 or vocab > 2^30. */
+ar_status ar_verify_drafts(const ar_verify_desc* desc, int64_t* accepted, int64_t* tokens, float* logp,
+                           void* workspace, void* stream);
+
 /* ---------------------------------------------------------------- status */
 
 /* Every device-side wait in the library is bounded. One that runs out (for
@@ -738,7 +887,8 @@ ar_status ar_muon_step(const ar_ortho_plan_t* plan, const ar_muon_desc* desc, co
  * "Collective communication"). From then on the executing calls
  * (ar_execute, ar_execute_host, ar_execute_noalloc, ar_bind,
  * ar_execute_bound, ar_bucket_allreduce, ar_token_logp, ar_policy_loss,
- * ar_preference_loss, ar_orthogonalize, ar_muon_step) on that device return AR_ETIMEOUT
+ * ar_preference_loss, ar_orthogonalize, ar_muon_step, ar_grad_norm,
+ * ar_grad_clip, ar_adamw_step, ar_verify_drafts) on that device return AR_ETIMEOUT
  * and enqueue nothing, until ar_device_status(1) clears the word. */
 
 /* Read (and clear, if clear != 0) the calling device's sticky status word.

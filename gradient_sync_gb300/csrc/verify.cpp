@@ -106,6 +106,7 @@ ar_status ar_verify_drafts(const ar_verify_desc* d, int64_t* accepted, int64_t* 
   p.tokens = tokens;
   p.logp = logp;
   p.results = static_cast<RowResult*>(workspace);
+  p.fallen = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + verify_fallen(d->n_drafts, d->n_seq));
   if ((s = device_ready()) != AR_OK) return s;
   return launch_verify(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? AR_OK : AR_ECUDA;
 }

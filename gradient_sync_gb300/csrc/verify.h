@@ -39,10 +39,17 @@ struct VerifyParams {
   int64_t* tokens;
   float* logp;
   RowResult* results;  // workspace, [n_drafts + n_seq]
+  int32_t* fallen;     // workspace, [n_seq]: a draft that fell, by its place; null: not kept
+  int ranks;           // CTAs a row
+  int64_t pitch;       // rows are visited this far apart
 };
 
-inline int64_t verify_bytes(int64_t n_drafts, int64_t n_seq) {
+// Byte offset of `fallen` in the workspace, and its size.
+inline int64_t verify_fallen(int64_t n_drafts, int64_t n_seq) {
   return (int64_t(sizeof(RowResult)) * (n_drafts + n_seq) + 255) / 256 * 256;
+}
+inline int64_t verify_bytes(int64_t n_drafts, int64_t n_seq) {
+  return verify_fallen(n_drafts, n_seq) + (4 * n_seq + 255) / 256 * 256;
 }
 
 cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream);

@@ -28,6 +28,7 @@
 
 #include <algorithm>
 
+#include "bulk.cuh"
 #include "common.cuh"
 
 namespace ar {
@@ -37,6 +38,8 @@ constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 constexpr int kMaxRanks = 8;  // CTAs of a cluster
 
 enum Mode : int { kLookup = 0, kDrafted = 1, kGreedy = 2 };  // drafts without distributions, with them, greedy
+
+constexpr uint32_t kPolls = 1u << 22;  // of a copy, each of which may suspend the thread for a while
 
 extern __shared__ __align__(16) char held[];
 
@@ -102,11 +105,22 @@ struct alignas(16) Post {
 };
 enum Phase : int { kSums = 0, kTops = 1, kSumsAgain = 2, kExact = 3, kTotals = 4, kTotalsAgain = 5, kPhases = 6 };
 
+// A sum s * 2^c.
+struct Sum {
+  int c;
+  float s;
+};
+
 struct Shared {
   Post posts[kPhases][kRowWarps];
-  Post all[kMaxRanks * kRowWarps];
+  uint64_t full[kRowWarps];  // a warp's part of the rows is in shared memory
+  int abort;
   int skip;
+  int odd;    // scores so large that their bias has to be taken off first: 1: the target's, 2: the draft's
   int stands;
+  float bias_x, bias_y;
+  Sum zx, zy;
+  float rho, rho_low;
   int owner;  // of a draw's border: rank * kRowWarps + warp, -1: no weight
   double before, target;
   Two parts[kRowWarps];
@@ -144,25 +158,25 @@ __device__ __forceinline__ int peer_int(const int* p, int rank) {
   return v;
 }
 
-// All warps' posts of a phase, in sh.all. A phase's posts are written once.
-__device__ __forceinline__ void exchange(Shared& sh, int phase, int ranks) {
+// A phase's posts are written once, then read by every CTA's first warp, two a lane.
+__device__ __forceinline__ void posted(int ranks) {
   if (ranks > 1) cluster_barrier();
   else __syncthreads();
-  const int t = threadIdx.x;
-  if (t < ranks * kRowWarps)
-    sh.all[t] = ranks > 1 ? peer_post(&sh.posts[phase][t % kRowWarps], t / kRowWarps) : sh.posts[phase][t];
-  __syncthreads();
+}
+__device__ __forceinline__ Post post_at(const Shared& sh, int phase, int i, int ranks) {
+  const Post* p = &sh.posts[phase][i % kRowWarps];
+  return ranks > 1 ? peer_post(p, i / kRowWarps) : *p;
 }
 
-// One CTA's part of a row of scores: from shared memory, where it has been
-// copied to, or from the row itself.
+// A row of scores as a warp sees it: its part in shared memory, where it has
+// been copied to, or the row itself.
 template <bool BF16, bool HOLD>
 struct Scores {
   static constexpr int ES = BF16 ? 2 : 4, W = 16 / ES;
   const char* row;
   int n;
-  int lead;   // elements between 16 aligned bytes and the first one
-  int shift;  // HOLD: element i is at held + shift + i * ES
+  int lead;      // elements between 16 aligned bytes and the first one
+  int shift;     // HOLD: element i is at held + shift + i * ES
   bool aligned;  // groups of 8 start on 16 aligned bytes
   float bias;    // taken off every score: 0, or the maximum where scores are so large that x k has no fraction
   __device__ Scores(const VerifyRows& r, int64_t at, int64_t vocab) {
@@ -173,25 +187,23 @@ struct Scores {
     aligned = true;
     bias = 0.0f;
   }
-  // Copies the elements [from, to) that the row has, whole 16 aligned bytes at a time, to held + offset.
-  __device__ void stage(int from, int to, int offset) {
-    const int before = (from + lead + 8) % W;  // (from >= -7)
-    shift = offset - (from - before) * ES;
-    for (int i = from - before + int(threadIdx.x) * W; i < to; i += kRowThreads * W) {
-      if (i >= 0 && i + W <= n) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                         uint32_t(__cvta_generic_to_shared(held + shift + i * ES))),
-                     "l"(row + int64_t(i) * ES)
-                     : "memory");
-      } else {
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          if (i + j < 0 || i + j >= n) continue;
-          if (BF16) *reinterpret_cast<uint16_t*>(held + shift + (i + j) * ES) = reinterpret_cast<const uint16_t*>(row)[i + j];
-          else *reinterpret_cast<float*>(held + shift + (i + j) * ES) = reinterpret_cast<const float*>(row)[i + j];
-        }
-      }
-    }
+  __device__ __forceinline__ void place(int from, int offset) { shift = offset - (from - (from + lead + 8) % W) * ES; }
+  // Copies the elements [from, to) to where place() has put them, -inf for those that the row does not have: whole 16
+  // aligned bytes by one bulk copy (its size is returned), the others by the lanes. (from >= -7)
+  __device__ uint32_t copy(int from, int to, int lane, uint64_t* bar) const {
+    const int head = lead > 0 ? W - lead : 0, tail = max(head, (lead + n) / W * W - lead);
+    const int a = max(from - (from + lead + 8) % W, head), b = min(to + (W - (to + lead) % W) % W, tail);
+    const int few = lane < W ? (lane < head ? lane : -1) : tail + lane - W;  // edges: elements 0 .. head - 1, tail .. n - 1
+    if (lane < 2 * W && few >= max(from, 0) && few < min(to, n)) put(few, one(few));
+    if (lane < 8 && from + lane < 0) put(from + lane, -INFINITY);
+    if (lane < 8 && to - 1 - lane >= n) put(to - 1 - lane, -INFINITY);
+    if (b <= a) return 0;
+    if (lane == 0) bulk_load(held + shift + a * ES, row + int64_t(a) * ES, uint32_t(b - a) * ES, bar);
+    return uint32_t(b - a) * ES;
+  }
+  __device__ __forceinline__ void put(int i, float x) const {
+    if (BF16) *reinterpret_cast<uint16_t*>(held + shift + i * ES) = uint16_t(__float_as_uint(x) >> 16);
+    else *reinterpret_cast<float*>(held + shift + i * ES) = x;
   }
   __device__ __forceinline__ const char* at(int i) const { return HOLD ? held + shift + i * ES : row + int64_t(i) * ES; }
   __device__ __forceinline__ float one(int i) const {  // from the row
@@ -206,7 +218,7 @@ struct Scores {
     }
   }
   __device__ __forceinline__ void load_as_is(int i, float (&x)[8]) const {
-    if (i >= 0 && i + 8 <= n && aligned) {
+    if (aligned && (HOLD || (i >= 0 && i + 8 <= n))) {
       if (BF16) {
         const uint4 r = *reinterpret_cast<const uint4*>(at(i));
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -223,7 +235,7 @@ struct Scores {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         x[j] = -INFINITY;
-        if (i + j >= 0 && i + j < n)
+        if (HOLD || (i + j >= 0 && i + j < n))
           x[j] = BF16 ? bf16_to_f32(*reinterpret_cast<const uint16_t*>(at(i + j))) : *reinterpret_cast<const float*>(at(i + j));
       }
     }
@@ -253,29 +265,23 @@ __device__ __forceinline__ float top_of(const S& s, const Piece& p, int lane) {
   return top;
 }
 
-// 2^d for an integer d <= 0, exactly (0 below the normal numbers).
-__device__ __forceinline__ float pow2(float d) {
-  const int e = int(fmaxf(d, -127.0f)) + 127;
-  return e > 0 ? __int_as_float(e << 23) : 0.0f;
-}
+// 2^d for d <= 0, exactly (0 below the normal numbers).
+__device__ __forceinline__ float pow2(int d) { return d > -127 ? __int_as_float((d + 127) << 23) : 0.0f; }
 
-// A sum s * 2^c, c an integer, s in [1/2, 1) (0: c is -inf). NaN: a score was NaN
-// or +inf; +inf: scores so large that their bias has to be taken off first.
-struct Sum {
-  float c, s;
-};
-__device__ __forceinline__ Sum normalized(float c, float s) {
+// Sums: kNone for a part that is all -inf (s = 0). s is NaN where a score was NaN
+// or +inf, +inf (at kOdd, above all shifts) where a bias has to be taken off first.
+constexpr int kNone = -(1 << 28), kOdd = 1 << 28;
+__device__ __forceinline__ Sum normalized(int c, float s) {  // s a normal number: to [1/2, 1)
   const int bits = __float_as_int(s);
-  return {c + float((bits >> 23) - 126), __int_as_float((bits & 0x007fffff) | 0x3f000000)};
+  return {c + (bits >> 23) - 126, __int_as_float((bits & 0x007fffff) | 0x3f000000)};
 }
-__device__ __forceinline__ Sum join(Sum a, Sum b) {
-  const float c = fmaxf(a.c, b.c), z = c == -INFINITY ? 0.0f : c;
-  return {c, a.s * pow2(a.c - z) + b.s * pow2(b.c - z)};
-}
+// The sum over a warp's lanes.
 __device__ __forceinline__ Sum warp_join(Sum v) {
+  const int c = __reduce_max_sync(~0u, v.c);
+  float s = v.s * pow2(v.c - c);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = join(v, {__shfl_xor_sync(~0u, v.c, o), __shfl_xor_sync(~0u, v.s, o)});
-  return v;
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+  return {c, s};
 }
 
 // Sums that the first group's shift does not serve: with the thread's maximum.
@@ -287,15 +293,15 @@ __device__ __noinline__ Sum careful_sum(const S s, const Piece p, int lane, floa
     s.load(8 * g + p.first, x);
     for (int j = 0; j < 8; ++j) top = fmaxf(top, x[j]), nan |= x[j] != x[j];
   }
-  if (nan || top == INFINITY) return {0.0f, __int_as_float(0x7fc00000)};
-  if (top == -INFINITY) return {-INFINITY, 0.0f};
-  if (!(fabsf(top * k) < 4194304.0f)) return {1e30f, INFINITY};  // (above all shifts)
+  if (nan || top == INFINITY) return {0, __int_as_float(0x7fc00000)};
+  if (top == -INFINITY) return {kNone, 0.0f};
+  if (!(fabsf(top * k) < 4194304.0f)) return {kOdd, INFINITY};
   const float c = ceilf(top * k);
   for (int g = p.lo + lane; g < p.hi; g += 32) {
     s.load(8 * g + p.first, x);
     for (int j = 0; j < 8; ++j) sum += exp2_approx(fmaf(x[j], k, -c));
   }
-  return normalized(c, sum);
+  return normalized(int(c), sum);
 }
 
 // The sum over a thread's groups, in one pass: the shift is the first group's. TOP: and the largest score with
@@ -305,11 +311,20 @@ struct Top {
   int at;
 };
 __device__ __forceinline__ Top larger(Top a, Top b) { return b.x > a.x || (b.x == a.x && b.at < a.at) ? b : a; }
+__device__ __forceinline__ Top largest(Top v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = larger(v, {__shfl_xor_sync(~0u, v.x, o), __shfl_xor_sync(~0u, v.at, o)});
+  return v;
+}
+__device__ __forceinline__ Sum joined(Sum a, Sum b) {
+  const int c = max(a.c, b.c);
+  return {c, a.s * pow2(a.c - c) + b.s * pow2(b.c - c)};
+}
 template <bool TOP, class S>
 __device__ __forceinline__ Sum fast_sum(const S& s, const Piece& p, int lane, float k, Top& top) {
   int g = p.lo + lane;
   if (TOP) top = {-INFINITY, INT32_MAX};
-  if (g >= p.hi) return {-INFINITY, 0.0f};
+  if (g >= p.hi) return {kNone, 0.0f};
   float x[8];
   s.load(8 * g + p.first, x);
   float m = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
@@ -345,7 +360,7 @@ __device__ __forceinline__ Sum fast_sum(const S& s, const Piece& p, int lane, fl
     for (int j = 7; j >= 0; --j)
       if (x[j] == top.x) top.at = 8 * best + p.first + j;
   }
-  if (sum.hi > 7.9e-31f && sum.hi < 1.2e30f) return normalized(c, sum.hi);
+  if (sum.hi > 7.9e-31f && sum.hi < 1.2e30f) return normalized(int(c), sum.hi);
   return careful_sum(s, p, lane, k);
 }
 
@@ -375,7 +390,7 @@ __device__ __forceinline__ Two exact_sum(const S& s, const Piece& p, int lane, c
 }
 
 // log2 of a sum, in two parts.
-__device__ __forceinline__ Two log2_of(Sum v) { return two_sum(v.c, log2f(v.s)); }
+__device__ __forceinline__ Two log2_of(Sum v) { return two_sum(float(v.c), log2f(v.s)); }
 // x k less such a logarithm, in two parts. (k as the sum has it, without what fp32 leaves of it.)
 __device__ __forceinline__ Two log2_p(float x, float k, Two log2_z) {
   const float p = x * k;
@@ -491,6 +506,8 @@ __device__ __forceinline__ int64_t start_of(const VerifyParams& p, int64_t s) {
 
 template <bool XB, bool YB, int MODE, bool HOLD>
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ VerifyParams p) {
+  using X = Scores<XB, HOLD>;
+  using Y = Scores<YB, HOLD>;
   grid_dependency_wait();
   grid_dependents_launch();
   __shared__ Shared sh;
@@ -500,6 +517,9 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
   const int64_t item = int64_t(blockIdx.x) / ranks, across = (p.n_drafts + p.n_seq + p.pitch - 1) / p.pitch;
   const int64_t row = item % across * p.pitch + item / across;
   if (row >= p.n_drafts + p.n_seq) return;
+  if (HOLD && threadIdx.x < kRowWarps) mbar_init(&sh.full[threadIdx.x], 1);
+  if (threadIdx.x == 0) sh.abort = 0;
+  if (HOLD) mbar_init_fence();
   // the sequence: the last one whose first row is not behind this one
   int64_t s = -1;
   for (int64_t base = 0; base < p.n_seq; base += kRowThreads) {
@@ -527,16 +547,27 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
   }
   const bool behind = place == count;  // the row behind all drafts
   const bool drafted = MODE == kDrafted && !behind;
-  Scores<XB, HOLD> x(p.target, row, p.vocab);
-  Scores<YB, HOLD> y(drafted ? p.draft : p.target, drafted ? first + place : row, p.vocab);
-  // this CTA's part, in groups that start on 16 aligned bytes of the target's row
+  X x(p.target, row, p.vocab);
+  Y y(drafted ? p.draft : p.target, drafted ? first + place : row, p.vocab);
+  if (drafted) y.aligned = ((y.lead - x.lead) & (Y::W - 1)) == 0;
+  // this CTA's part, in groups that start on 16 aligned bytes of the target's row, and its warps' (whole rounds)
   const int groups = int((x.lead + p.vocab + 7) / 8), per = (groups + ranks - 1) / ranks;
-  const int g0 = min(groups, rank * per), g1 = min(groups, g0 + per), per_warp = (g1 - g0 + kRowWarps - 1) / kRowWarps;
-  const Piece piece = {min(g1, g0 + warp * per_warp), min(g1, g0 + (warp + 1) * per_warp), -x.lead};
-  if (drafted) y.aligned = ((y.lead - x.lead) & (y.W - 1)) == 0;
-  if (HOLD) {
-    x.stage(8 * g0 - x.lead, 8 * g1 - x.lead, 0);
-    if (drafted) y.stage(8 * g0 - x.lead, 8 * g1 - x.lead, (g1 - g0) * 8 * x.ES);
+  const int g0 = min(groups, rank * per), g1 = min(groups, g0 + per);
+  const int per_warp = (g1 - g0 + 32 * kRowWarps - 1) / (32 * kRowWarps) * 32;
+  const auto piece_of = [&](int w) { return Piece{min(g1, g0 + w * per_warp), min(g1, g0 + (w + 1) * per_warp), -x.lead}; };
+  const Piece piece = piece_of(warp);
+  // shared memory: the target's part, then the draft's, each warp's with up to 16 bytes on both sides
+  const auto place_rows = [&](int w) {
+    const Piece q = piece_of(w);
+    x.place(8 * q.lo + q.first, (q.lo - g0) * 8 * X::ES);
+    if (drafted) y.place(8 * q.lo + q.first, (g1 - g0) * 8 * X::ES + (q.lo - g0) * 8 * Y::ES + w * 32);
+  };
+  if (HOLD) place_rows(warp);
+  if (HOLD && piece.lo < piece.hi) {
+    const int from = 8 * piece.lo + piece.first, to = 8 * piece.hi + piece.first;
+    uint32_t bytes = x.copy(from, to, lane, &sh.full[warp]);
+    if (drafted) bytes += y.copy(from, to, lane, &sh.full[warp]);
+    if (lane == 0) mbar_arrive_expect_tx(&sh.full[warp], bytes);
   }
   // what thread 0 needs for the decision
   int64_t token = -1;
@@ -551,131 +582,156 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
       u_draft = p.uniforms[row];
     }
   }
-  if (HOLD) {
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
+  bool copied = true;
+  if (HOLD && piece.lo < piece.hi) {
+    const StatusRef status = {p.status_word, p.status_host};
+    copied = mbar_wait(&sh.full[warp], 0, kPolls, &sh.abort, status);
+    __syncwarp();
   }
 
   // the sums, once more where the scores turn out to be too large as they are
-  const float kx = p.target.k, kx_low = p.target.k_low, ky = p.draft.k, ky_low = p.draft.k_low;
-  Sum zx, zy;
-  Top top;
-  for (int again = 0;; ++again) {
-    Top none;
-    zx = warp_join(fast_sum<MODE == kGreedy>(x, piece, lane, kx, top));
-    zy = {0.0f, 0.5f};
+  const float kx = p.target.k, ky = p.draft.k;
+  for (int again = 0; again < 2; ++again) {
+    Top top, none;
+    Sum zx = warp_join(fast_sum<MODE == kGreedy>(x, piece, lane, kx, top)), zy = {0, 0.5f};
     if (drafted) zy = warp_join(fast_sum<false>(y, piece, lane, ky, none));
-    if (MODE == kGreedy) {
+    if (MODE == kGreedy) top = largest(top);
+    if (lane == 0)
+      sh.posts[2 * again][warp] = MODE == kGreedy ? Post{__int_as_float(zx.c), zx.s, top.x, __int_as_float(top.at)}
+                                                  : Post{__int_as_float(zx.c), zx.s, __int_as_float(zy.c), zy.s};
+    posted(ranks);
+    if (warp == 0) {
+      Sum ax[2], ay[2];
+      Top at[2];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = larger(top, {__shfl_xor_sync(~0u, top.x, o), __shfl_xor_sync(~0u, top.at, o)});
-      if (lane == 0) sh.posts[2 * again][warp] = {zx.c, zx.s, top.x, __int_as_float(top.at)};
-    } else if (lane == 0) {
-      sh.posts[2 * again][warp] = {zx.c, zx.s, zy.c, zy.s};
-    }
-    exchange(sh, 2 * again, ranks);
-    zx = zy = {-INFINITY, 0.0f};
-    top = {-INFINITY, INT32_MAX};
-    for (int i = lane; i < ranks * kRowWarps; i += 32) {
-      const Post v = sh.all[i];
-      zx = join(zx, {v.a, v.b});
-      if (MODE == kGreedy) top = larger(top, {v.c, __float_as_int(v.d)});
-      else zy = join(zy, {v.c, v.d});
-    }
-    zx = warp_join(zx);
-    if (MODE == kDrafted) zy = warp_join(zy);
-    if (MODE == kGreedy) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = larger(top, {__shfl_xor_sync(~0u, top.x, o), __shfl_xor_sync(~0u, top.at, o)});
-    }
-    if (!(zx.s == INFINITY || zy.s == INFINITY) || again > 0) break;
-    float mx = top_of(x, piece, lane), my = drafted ? top_of(y, piece, lane) : 0.0f;
-    if (lane == 0) sh.posts[kTops][warp] = {mx, my, 0.0f, 0.0f};
-    exchange(sh, kTops, ranks);
-    for (int i = 0; i < ranks * kRowWarps; ++i) mx = fmaxf(mx, sh.all[i].a), my = fmaxf(my, sh.all[i].b);
-    if (zx.s == INFINITY) x.bias = mx;
-    if (zy.s == INFINITY) y.bias = my;
-  }
-  // (a sum of s in [1/2, 1) at a shift above every part's: no weight is above 1)
-  const bool ok = zx.s > 0.0f && (!drafted || zy.s > 0.0f);  // neither NaN nor nothing
-  if (threadIdx.x == 0) {
-    RowResult* result = p.results + row;
-    const Two log2_zx = log2_of(zx);
-    sh.log2_z = log2_zx;
-    bool fell = true;
-    sh.stands = 1;  // 1: no draw follows
-    if (!ok) {
-      if (rank == 0) *result = {-1, __int_as_float(0x7fc00000), 0.0f, 0, 0};
-    } else if (MODE == kGreedy) {
-      const float lp = to_e(log2_p(top.x, kx, log2_zx));
-      fell = token != top.at;
-      if (rank == 0) *result = {top.at, lp, lp, int32_t(!behind && !fell), 0};
-    } else {
-      sh.stands = 0;
-      if (xt > -INFINITY) {
-        const Two lp = log2_p(xt - x.bias, kx, log2_zx);
-        Two gap = lp;
-        if (drafted) {
-          const Two lq = log2_p(yt - y.bias, ky, log2_of(zy));
-          gap = add(lp, {-lq.hi, -lq.lo});
-        }
-        // (a draft that its own distribution gives nothing stands)
-        const bool stands = u_draft <= 0.0f || (drafted && yt == -INFINITY) ||
-                            fminf(u_draft, 0.99999994f) < exp2f(gap.hi) * fmaf(gap.lo, 0.69314718f, 1.0f);
-        if (stands && u_draft == u_draft) {
-          sh.stands = 1;
-          fell = false;
-          if (rank == 0) *result = {-1, 0.0f, to_e(lp), 1, 0};
+      for (int h = 0; h < 2; ++h) {
+        const int i = lane + 32 * h;
+        ax[h] = ay[h] = {kNone, 0.0f};
+        at[h] = {-INFINITY, INT32_MAX};
+        if (i < ranks * kRowWarps) {
+          const Post v = post_at(sh, 2 * again, i, ranks);
+          ax[h] = {__float_as_int(v.a), v.b};
+          if (MODE == kGreedy) at[h] = {v.c, __float_as_int(v.d)};
+          else ay[h] = {__float_as_int(v.c), v.d};
         }
       }
+      zx = warp_join(joined(ax[0], ax[1]));
+      if (MODE == kDrafted) zy = warp_join(joined(ay[0], ay[1]));
+      if (MODE == kGreedy) top = largest(larger(at[0], at[1]));
+      const int odd = again > 0 ? 0 : (zx.s == INFINITY ? 1 : 0) | (drafted && zy.s == INFINITY ? 2 : 0);
+      // neither NaN nor nothing
+      const bool ok = zx.s > 0.0f && zx.s < INFINITY && (!drafted || (zy.s > 0.0f && zy.s < INFINITY));
+      if (lane == 0) sh.odd = odd;
+      if (lane == 0 && odd == 0) {
+        RowResult* result = p.results + row;
+        bool fell = true;
+        sh.stands = 1;  // 1: no draw follows
+        if (!ok) {
+          if (rank == 0) *result = {-1, __int_as_float(0x7fc00000), 0.0f, 0, 0};
+        } else {
+          sh.zx = zx = normalized(zx.c, zx.s);
+          const Two log2_zx = log2_of(zx);
+          sh.log2_z = log2_zx;
+          if (MODE == kGreedy) {
+            const float lp = to_e(log2_p(top.x, kx, log2_zx));
+            fell = token != top.at;
+            if (rank == 0) *result = {top.at, lp, lp, int32_t(!behind && !fell), 0};
+          } else {
+            sh.stands = 0;
+            if (drafted) sh.zy = zy = normalized(zy.c, zy.s);
+            if (xt > -INFINITY) {
+              const Two lp = log2_p(xt - x.bias, kx, log2_zx);
+              Two gap = lp;
+              if (drafted) {
+                const Two lq = log2_p(yt - y.bias, ky, log2_of(zy));
+                gap = add(lp, {-lq.hi, -lq.lo});
+              }
+              // (a draft that its own distribution gives nothing stands)
+              const bool stands = u_draft <= 0.0f || (drafted && yt == -INFINITY) ||
+                                  fminf(u_draft, 0.99999994f) < exp2f(gap.hi) * fmaf(gap.lo, 0.69314718f, 1.0f);
+              if (stands && u_draft == u_draft) {
+                sh.stands = 1;
+                fell = false;
+                if (rank == 0) *result = {-1, 0.0f, to_e(lp), 1, 0};
+              }
+            }
+          }
+        }
+        if (p.fallen != nullptr && rank == 0 && !behind && fell) atomicMin(p.fallen + s, int(place));
+      }
     }
-    if (p.fallen != nullptr && rank == 0 && !behind && fell) atomicMin(p.fallen + s, int(place));
+    __syncthreads();
+    if (sh.odd == 0) break;
+    const float mx = top_of(x, piece, lane), my = drafted ? top_of(y, piece, lane) : 0.0f;
+    if (lane == 0) sh.posts[kTops][warp] = {mx, my, 0.0f, 0.0f};
+    posted(ranks);
+    if (threadIdx.x == 0) {
+      float bx = mx, by = my;
+      for (int i = 0; i < ranks * kRowWarps; ++i) {
+        const Post v = post_at(sh, kTops, i, ranks);
+        bx = fmaxf(bx, v.a), by = fmaxf(by, v.b);
+      }
+      sh.bias_x = sh.odd & 1 ? bx : 0.0f;
+      sh.bias_y = sh.odd & 2 ? by : 0.0f;
+    }
+    __syncthreads();
+    x.bias = sh.bias_x;
+    y.bias = sh.bias_y;
   }
-  __syncthreads();
   if (MODE != kGreedy && !sh.stands) {
-    Draw<Scores<XB, HOLD>, Scores<YB, HOLD>> d = {x, y, {kx, kx_low, zx.c}, {ky, ky_low, zy.c}, 0.0f, 0.0f,
-                                                  inside ? int(token) : -1, behind ? kNothing : drafted ? kRow : kToken};
+    Draw<X, Y> d = {x, y, {kx, p.target.k_low, float(sh.zx.c)}, {ky, p.draft.k_low, drafted ? float(sh.zy.c) : 0.0f}, 0.0f, 0.0f,
+                    inside ? int(token) : -1, behind ? kNothing : drafted ? kRow : kToken};
     if (drafted) {
       const Two a = warp_sum(exact_sum(x, piece, lane, d.wx)), b = warp_sum(exact_sum(y, piece, lane, d.wy));
       if (lane == 0) sh.posts[kExact][warp] = {a.hi, a.lo, b.hi, b.lo};
-      exchange(sh, kExact, ranks);
-      Two c = {0.0f, 0.0f}, e = {0.0f, 0.0f};
-      for (int i = lane; i < ranks * kRowWarps; i += 32) {
-        const Post v = sh.all[i];
-        c = add(c, {v.a, v.b});
-        e = add(e, {v.c, v.d});
+      posted(ranks);
+      if (warp == 0) {
+        Two c = {0.0f, 0.0f}, e = {0.0f, 0.0f};
+        for (int i = lane; i < ranks * kRowWarps; i += 32) {
+          const Post v = post_at(sh, kExact, i, ranks);
+          c = add(c, {v.a, v.b});
+          e = add(e, {v.c, v.d});
+        }
+        c = warp_sum(c);
+        e = warp_sum(e);
+        // the quotient of both pairs: a rounded one, and what it leaves
+        const float rho = c.hi / e.hi;
+        if (lane == 0) sh.rho = rho, sh.rho_low = ((fmaf(-rho, e.hi, c.hi) + c.lo) - rho * e.lo) / e.hi;
       }
-      c = warp_sum(c);
-      e = warp_sum(e);
-      // the quotient of both pairs: a rounded one, and what it leaves
-      d.rho = c.hi / e.hi;
-      d.rho_low = ((fmaf(-d.rho, e.hi, c.hi) + c.lo) - d.rho * e.lo) / e.hi;
+      __syncthreads();
+      d.rho = sh.rho;
+      d.rho_low = sh.rho_low;
     }
     const float u = fminf(fmaxf(u_draw == u_draw ? u_draw : 0.0f, 0.0f), 0.99999994f);
     for (int again = 0; again < 2; ++again) {
       const Two total = d.total(piece, lane);
       if (lane == 0) sh.posts[kTotals + again][warp] = {total.hi, total.lo, 0.0f, 0.0f};
-      exchange(sh, kTotals + again, ranks);
+      posted(ranks);
       if (warp == 0) {
-        const int most = ranks * kRowWarps;
-        const double v0 = 2 * lane < most ? wide({sh.all[2 * lane].a, sh.all[2 * lane].b}) : 0.0;
-        const double v1 = 2 * lane + 1 < most ? wide({sh.all[2 * lane + 1].a, sh.all[2 * lane + 1].b}) : 0.0;
-        double all = v0 + v1, before = 0.0;
+        double v[2] = {0.0, 0.0}, before = 0.0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (2 * lane + h < ranks * kRowWarps) {
+            const Post t = post_at(sh, kTotals + again, 2 * lane + h, ranks);
+            v[h] = wide({t.a, t.b});
+          }
+        double all = v[0] + v[1];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(~0u, all, o);
         const double target = double(u) * all;
-        const int owner = part_of(v0, v1, 0.0, target, lane, before);
+        const int owner = part_of(v[0], v[1], 0.0, target, lane, before);
         if (lane == 0) sh.owner = owner, sh.before = before, sh.target = target;
       }
       __syncthreads();
       if (sh.owner >= 0) break;
-      __syncthreads();
       d.less = kNothing;  // no residue: from p itself
     }
     if (sh.owner >= 0 && sh.owner / kRowWarps == rank) {
       // the owner's piece, once more over all warps, then the round of the warp that has the border
-      const int w = sh.owner % kRowWarps, lo = min(g1, g0 + w * per_warp), hi = min(g1, g0 + (w + 1) * per_warp);
-      const int per_part = ((hi - lo + kRowWarps - 1) / kRowWarps + 31) / 32 * 32;
-      const Piece part = {min(hi, lo + warp * per_part), min(hi, lo + (warp + 1) * per_part), piece.first};
+      const Piece q = piece_of(sh.owner % kRowWarps);
+      if (HOLD) place_rows(sh.owner % kRowWarps);
+      const int per_part = ((q.hi - q.lo + kRowWarps - 1) / kRowWarps + 31) / 32 * 32;
+      const Piece part = {min(q.hi, q.lo + warp * per_part), min(q.hi, q.lo + (warp + 1) * per_part), q.first};
       const Two total = d.total(part, lane);
       if (lane == 0) sh.parts[warp] = total;
       __syncthreads();
@@ -687,6 +743,10 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         if (lane == 0 && found >= 0)
           p.results[row] = {found, to_e(log2_p(x.one(found) - x.bias, kx, sh.log2_z)), 0.0f, 0, 0};
       }
+    }
+  }
+  if (!copied) {  // (recorded; the copy may still be under way, and shared memory has to stay until it is not)
+    for (uint32_t i = 0; i < kPolls && !mbar_try_wait(&sh.full[warp], 0); ++i) {
     }
   }
   if (ranks > 1) cluster_barrier();  // no CTA goes while another may still read from it
@@ -764,11 +824,11 @@ void (*rows_kernel_of(const VerifyParams& p))(VerifyParams) {
 }
 
 // Shared memory of a CTA: its part of the target's row in whole groups, and
-// the draft's elements of the same places with up to 16 bytes in front.
+// the draft's elements of the same places, each warp's with up to 16 bytes on both sides.
 int64_t part_bytes(const VerifyParams& p, int ranks) {
   const int64_t groups = (p.vocab + 14) / 8, per = (groups + ranks - 1) / ranks;
   const int64_t x = per * 8 * (p.target.bf16 ? 2 : 4);
-  return p.draft.data == nullptr ? x : x + per * 8 * (p.draft.bf16 ? 2 : 4) + 32;
+  return p.draft.data == nullptr ? x : x + per * 8 * (p.draft.bf16 ? 2 : 4) + 32 * kRowWarps;
 }
 
 constexpr int64_t kMostHeld = 220 << 10;   // what a CTA can have, less its static part
@@ -799,8 +859,8 @@ cudaError_t launch_verify(const VerifyParams& q, cudaStream_t stream) {
   p.pitch = waves ? (rows + p.n_seq - 1) / p.n_seq : 1;
   if ((rows + p.pitch) * p.ranks > 0x7fffffff) p.pitch = 1;
   if (!waves) p.fallen = nullptr;
-  cudaError_t err = cudaSuccess;
-  if (waves) err = launch_after(clear_kernel, p, (p.n_seq + 255) / 256, 256, 1, 0, stream);
+  cudaError_t err = status_ref(&p.status_word, &p.status_host);
+  if (err == cudaSuccess && waves) err = launch_after(clear_kernel, p, (p.n_seq + 255) / 256, 256, 1, 0, stream);
   const int64_t items = (rows + p.pitch - 1) / p.pitch * p.pitch;
   if (err == cudaSuccess) err = launch_after(kernel, p, items * p.ranks, kRowThreads, p.ranks, smem, stream);
   if (err == cudaSuccess) err = launch_after(tokens_kernel, p, (p.n_seq + 7) / 8, 256, 1, 0, stream);

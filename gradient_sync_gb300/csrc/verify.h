@@ -42,6 +42,8 @@ struct VerifyParams {
   int32_t* fallen;     // workspace, [n_seq]: a draft that fell, by its place; null: not kept
   int ranks;           // CTAs a row
   int64_t pitch;       // rows are visited this far apart
+  unsigned int* status_word;  // where waits that ran out are recorded
+  unsigned int* const* status_host;
 };
 
 // Byte offset of `fallen` in the workspace, and its size.

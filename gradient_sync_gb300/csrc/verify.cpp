@@ -63,7 +63,7 @@ extern "C" {
 ar_status ar_verify_workspace(int64_t n_drafts, int64_t n_seq, int64_t vocab, size_t* bytes) {
   if (bytes == nullptr) return AR_EINVAL;
   const ar_status s = sizes_ok(n_drafts, n_seq, vocab);
-  if (s == AR_OK) *bytes = size_t(verify_bytes(n_drafts, n_seq));
+  if (s == AR_OK) *bytes = size_t(verify_layout(n_drafts, n_seq).bytes);
   return s;
 }
 
@@ -85,8 +85,9 @@ ar_status ar_verify_drafts(const ar_verify_desc* d, int64_t* accepted, int64_t* 
   if ((d->n_drafts > 0 && !aligned(d->drafts, 8)) || (!greedy && !aligned(d->uniforms, 4))) return AR_EINVAL;
   if (d->draft_start == nullptr ? d->n_seq != 1 : !aligned(d->draft_start, 8)) return AR_EINVAL;
   if (!aligned(accepted, 8) || !aligned(tokens, 8) || !aligned(logp, 4) || !aligned(workspace, 16)) return AR_EINVAL;
+  const VerifyLayout layout = verify_layout(d->n_drafts, d->n_seq);
   const Range outs[] = {range(accepted, 8 * d->n_seq), range(tokens, 8 * rows), range(logp, 4 * rows),
-                        range(workspace, verify_bytes(d->n_drafts, d->n_seq))};
+                        range(workspace, layout.bytes)};
   const Range ins[] = {x, y, range(d->drafts, 8 * d->n_drafts), range(greedy ? nullptr : d->uniforms, 4 * rows),
                        range(d->draft_start, 8 * (d->n_seq + 1))};
   for (int i = 0; i < 4; ++i) {
@@ -105,8 +106,10 @@ ar_status ar_verify_drafts(const ar_verify_desc* d, int64_t* accepted, int64_t* 
   p.accepted = accepted;
   p.tokens = tokens;
   p.logp = logp;
-  p.results = static_cast<RowResult*>(workspace);
-  p.fallen = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + verify_fallen(d->n_drafts, d->n_seq));
+  char* base = static_cast<char*>(workspace);
+  p.sums = reinterpret_cast<RowSums*>(base);
+  p.done = reinterpret_cast<int32_t*>(base + layout.done);
+  p.fallen = reinterpret_cast<int32_t*>(base + layout.fallen);
   if ((s = device_ready()) != AR_OK) return s;
   return launch_verify(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? AR_OK : AR_ECUDA;
 }

@@ -3,45 +3,42 @@
 // For a row of target logits x, p_i = w_i / Z with
 //   w_i = 2^(x_i k - c), k = log2(e) / temperature, Z = sum w_i,
 // for any integer c (sums with other shifts join without rounding), and alike q
-// for the draft's row. The draft t of the row stands while
-// u < p_t / q_t. Where it falls, a token is drawn from max(p_i - q_i, 0),
-// that is from w_i - v_i (Z / Z') where positive (v, Z' the draft's): the first index whose
-// running sum passes u times the total.
+// for the draft's row. The draft t of the row stands while u < p_t / q_t. Where it
+// falls, a token is drawn from max(p_i - q_i, 0), that is from w_i - v_i (Z / Z')
+// where positive (v, Z' the draft's): the first index whose running sum passes u
+// times the total.
 //
-// rows_kernel: a cluster of up to 8 CTAs takes a row of the target with its row of
-// the draft, copies both to shared memory, and works from there: sums, decision,
-// and, where the draft falls, the draw. Each row is read from HBM once; rows
-// too long for eight SMs' shared memory are read again by every pass. The rows of a sequence
-// run side by side, and each leaves what the sequence would need of it (stands or
-// not, the token drawn, both log-probabilities). Rows behind a draft that fell are
-// not needed: where a call has more rows than run at once, rows are visited by
-// their place in their sequence, and one that starts after such a fall is skipped.
-// tokens_kernel, a warp a sequence, finds the first draft that falls and writes
-// the tokens. Results do not depend on which rows were skipped.
+//  sums_kernel  Z and Z' of every row, in parts of a row, a CTA each: one pass, no CTA
+//               waits for another. Where a call has more rows than run at once, they are visited
+//               by their place in their sequence; the last CTA of a row to finish
+//               decides about its draft, and rows behind one that fell are not
+//               read any more. Bound by HBM for many rows.
+//  draw_kernel  a cluster of up to 8 CTAs a sequence: joins the parts, finds the first draft
+//               that falls, draws from that row alone (read two or three times, from
+//               the L2 where it is still there), writes the tokens.
+// Results do not depend on which rows were skipped: none before the first fall is.
 //
 // A draw has to put u on the right side of borders that may lie anywhere, also
 // between tokens of 1e-6 and less. So its weights are to fp32's last place (the
 // fast ones of the sums that only decide about drafts are not): the exponent is
-// carried with what fp32 leaves of it, the draft's weight is subtracted in one fused operation with a two-part factor, and sums
-// are pairs of fp32 numbers (fp64 adds are slow here), borders 64 bits.
+// carried with what fp32 leaves of it, the draft's weight is subtracted in one
+// fused operation with a two-part factor, sums beyond 32 terms are pairs of fp32
+// numbers (fp64 adds are slow here), borders 64 bits.
 #include "verify.h"
 
 #include <algorithm>
 
-#include "bulk.cuh"
 #include "common.cuh"
 
 namespace ar {
 namespace {
 
 constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
-constexpr int kMaxRanks = 8;  // CTAs of a cluster
+constexpr int kMaxRanks = 8;  // CTAs of a cluster of draw_kernel
+constexpr int kDrawCtas = 3;  // CTAs of draw_kernel an SM
+constexpr int kRounds = 2;    // of a warp, loaded together
 
 enum Mode : int { kLookup = 0, kDrafted = 1, kGreedy = 2 };  // drafts without distributions, with them, greedy
-
-constexpr uint32_t kPolls = 1u << 22;  // of a copy, each of which may suspend the thread for a while
-
-extern __shared__ __align__(16) char held[];
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -73,6 +70,11 @@ __device__ __forceinline__ Pair add2(Pair a, Pair b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
 __device__ __forceinline__ Pair exp2_pair(Pair a) {
   const float2 y = floats_of(a);
   return pair_of(exp2_approx(y.x), exp2_approx(y.y));
@@ -99,32 +101,400 @@ __device__ __forceinline__ Two warp_sum(Two v) {
   return v;
 }
 
-// What every warp of a cluster tells the others in one phase.
-struct alignas(16) Post {
-  float a, b, c, d;
-};
-enum Phase : int { kSums = 0, kTops = 1, kSumsAgain = 2, kExact = 3, kTotals = 4, kTotalsAgain = 5, kPhases = 6 };
+// ---------------------------------------------------------------- rows
 
-// A sum s * 2^c.
+// A row of scores, in groups of 8 that start on 16 aligned bytes of the target's row.
+template <bool BF16>
+struct Scores {
+  static constexpr int ES = BF16 ? 2 : 4, W = 16 / ES;
+  static constexpr int kVecs = 8 / W;  // 16-byte vectors of a group
+  const char* row;
+  int n;
+  int lead;      // elements between 16 aligned bytes and the first one
+  bool aligned;  // groups start on 16 aligned bytes of this row too
+  float bias;    // taken off every score: 0, or the maximum where scores are so large that x k has no fraction
+  __device__ __forceinline__ Scores(const VerifyRows& r, int at, int64_t vocab) {
+    row = r.data + int64_t(at) * r.ld * ES;
+    n = int(vocab);
+    lead = int(reinterpret_cast<uintptr_t>(row) / ES & (W - 1));
+    aligned = true;
+    bias = 0.0f;
+  }
+  __device__ __forceinline__ float one(int i) const {
+    return BF16 ? bf16_to_f32(reinterpret_cast<const uint16_t*>(row)[i]) : reinterpret_cast<const float*>(row)[i];
+  }
+  // The group at element i as it lies in memory; -inf for elements outside the row.
+  __device__ __forceinline__ void fetch(int i, uint4 (&r)[kVecs]) const {
+    if (aligned && i >= 0 && i + 8 <= n) {
+#pragma unroll
+      for (int h = 0; h < kVecs; ++h) r[h] = __ldg(reinterpret_cast<const uint4*>(row + int64_t(i) * ES) + h);
+    } else {
+      edge(i, r);
+    }
+  }
+  __device__ __forceinline__ void edge(int i, uint4 (&r)[kVecs]) const {
+    uint32_t w[4 * kVecs];
+#pragma unroll
+    for (int j = 0; j < 4 * kVecs; ++j) w[j] = BF16 ? 0xFF80FF80u : 0xFF800000u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (i + j < 0 || i + j >= n) continue;
+      if (BF16) w[j / 2] = (w[j / 2] & (j % 2 ? 0x0000FFFFu : 0xFFFF0000u)) | uint32_t(reinterpret_cast<const uint16_t*>(row)[i + j]) << (16 * (j % 2));
+      else w[j % (4 * kVecs)] = reinterpret_cast<const uint32_t*>(row)[i + j];
+    }
+#pragma unroll
+    for (int h = 0; h < kVecs; ++h) r[h] = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+  }
+  static __device__ __forceinline__ void nothing(uint4 (&r)[kVecs]) {
+    const uint32_t w = BF16 ? 0xFF80FF80u : 0xFF800000u;
+#pragma unroll
+    for (int h = 0; h < kVecs; ++h) r[h] = make_uint4(w, w, w, w);
+  }
+  // Its scores, less the bias.
+  __device__ __forceinline__ void scores(const uint4 (&r)[kVecs], float (&x)[8]) const {
+#pragma unroll
+    for (int h = 0; h < kVecs; ++h) {
+      const uint32_t w[4] = {r[h].x, r[h].y, r[h].z, r[h].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (BF16) x[2 * j] = bf16lo(w[j]), x[(2 * j + 1) % 8] = bf16hi(w[j]);
+        else x[4 * h + j] = __uint_as_float(w[j]);
+      }
+    }
+    if (bias != 0.0f) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] -= bias;
+    }
+  }
+  __device__ __forceinline__ void load(int i, float (&x)[8]) const {
+    uint4 r[kVecs];
+    fetch(i, r);
+    scores(r, x);
+  }
+};
+
+// Groups of 8 elements: element 8 g + first is group g's first.
+struct Piece {
+  int lo, hi, first;
+};
+
+// ---------------------------------------------------------------- sums
+
+// 2^d for d <= 0, exactly (0 below the normal numbers).
+__device__ __forceinline__ float pow2(int d) { return d > -127 ? __int_as_float((d + 127) << 23) : 0.0f; }
+
+// A sum s * 2^c. kNone: of nothing but -inf (s = 0). kLow: of scores so low that x k
+// has no fraction (beside any others they are nothing). At kOdd, above all shifts, s = +inf: of scores
+// so high. s is NaN where a score was NaN or +inf.
 struct Sum {
   int c;
   float s;
 };
+constexpr int kNone = -(1 << 28), kLow = -(1 << 27), kOdd = 1 << 28;
+constexpr float kFraction = 4194304.0f;  // 2^22
+__device__ __forceinline__ Sum normalized(int c, float s) {  // s a normal number: to [1/2, 1)
+  const int bits = __float_as_int(s);
+  return {c + (bits >> 23) - 126, __int_as_float((bits & 0x007fffff) | 0x3f000000)};
+}
+// The sum over a warp's lanes.
+__device__ __forceinline__ Sum warp_join(Sum v) {
+  const int c = __reduce_max_sync(~0u, v.c);
+  float s = v.s * pow2(v.c - c);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+  return {c, s};
+}
+
+struct Top {
+  float x;
+  int at;
+};
+__device__ __forceinline__ Top larger(Top a, Top b) { return b.x > a.x || (b.x == a.x && b.at < a.at) ? b : a; }
+__device__ __forceinline__ Top largest(Top v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = larger(v, {__shfl_xor_sync(~0u, v.x, o), __shfl_xor_sync(~0u, v.at, o)});
+  return v;
+}
+__device__ __forceinline__ float max8(const float (&x)[8]) {
+  return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+}
+
+// Sums that the first group's shift does not serve: with the thread's maximum.
+template <class S>
+__device__ __noinline__ Sum careful_sum(const S s, const Piece p, int start, int step, float k) {
+  float top = -INFINITY, sum = 0.0f, x[8];
+  bool nan = false;
+  for (int g = p.lo + start; g < p.hi; g += step) {
+    s.load(8 * g + p.first, x);
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, x[j]), nan |= x[j] != x[j];
+  }
+  if (nan || top == INFINITY) return {0, __int_as_float(0x7fc00000)};
+  if (top == -INFINITY) return {kNone, 0.0f};
+  if (top * k >= kFraction) return {kOdd, INFINITY};
+  if (top * k <= -kFraction) return {kLow, 0.5f};
+  const float c = ceilf(top * k);
+  for (int g = p.lo + start; g < p.hi; g += step) {
+    s.load(8 * g + p.first, x);
+    float t = 0.0f;
+    for (int j = 0; j < 8; ++j) t += exp2_approx(fmaf(x[j], k, -c));
+    sum += t;
+  }
+  return normalized(int(c), sum);
+}
+
+// The sum over every step-th group from the start-th, in one pass: the shift is the first group's. TOP: and the
+// largest score with its first place.
+template <bool TOP, class S>
+__device__ __forceinline__ Sum fast_sum(const S& s, const Piece& p, int start, int step, float k, Top& top) {
+  constexpr int kDeep = 8 / S::kVecs;  // groups of 8 loads in flight
+  int g = p.lo + start;
+  if (TOP) top = {-INFINITY, INT32_MAX};
+  if (g >= p.hi) return {kNone, 0.0f};
+  float c = 0.0f;
+  const Pair kk = pair_of(k, k);
+  Pair cc = kk;
+  int best = g;
+  bool begun = false;
+  Two sum = {0.0f, 0.0f};
+#pragma unroll 1
+  for (; g < p.hi; g += kDeep * step) {
+    uint4 raw[kDeep][S::kVecs];
+#pragma unroll
+    for (int r = 0; r < kDeep; ++r) {
+      S::nothing(raw[r]);
+      if (g + r * step < p.hi) s.fetch(8 * (g + r * step) + p.first, raw[r]);
+    }
+    if (!begun) {
+      float x[8];
+      s.scores(raw[0], x);
+      const float m = max8(x);
+      c = fabsf(m * k) < kFraction ? ceilf(m * k) : 0.0f;
+      cc = pair_of(-c, -c);
+      begun = true;
+    }
+    Pair a = pair_of(0.0f, 0.0f), b = a;
+#pragma unroll
+    for (int r = 0; r < kDeep; ++r) {
+      float x[8];
+      s.scores(raw[r], x);
+      if (TOP) {
+        const float m = max8(x);
+        if (m > top.x) top.x = m, best = g + r * step;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; j += 4) {
+        a = add2(a, exp2_pair(fma2(pair_of(x[j], x[j + 1]), kk, cc)));
+        b = add2(b, exp2_pair(fma2(pair_of(x[j + 2], x[j + 3]), kk, cc)));
+      }
+    }
+    const float2 v = floats_of(add2(a, b));
+    sum = add(sum, {v.x + v.y, 0.0f});
+  }
+  if (TOP) {
+    float y[8];
+    s.load(8 * best + p.first, y);
+#pragma unroll
+    for (int j = 7; j >= 0; --j)
+      if (y[j] == top.x) top.at = 8 * best + p.first + j;
+  }
+  if (sum.hi > 7.9e-31f && sum.hi < 1.2e30f) return normalized(int(c), sum.hi);
+  return careful_sum(s, p, start, step, k);
+}
+
+// ---------------------------------------------------------------- decisions
+
+// log2 of a sum, in two parts.
+__device__ __forceinline__ Two log2_of(Sum v) { return two_sum(float(v.c), log2f(v.s)); }
+// x k less such a logarithm, in two parts. (k as the sum has it, without what fp32 leaves of it.)
+__device__ __forceinline__ Two log2_p(float x, float k, Two log2_z) {
+  const float p = x * k;
+  return add(two_sum(p, -log2_z.hi), {fmaf(x, k, -p) - log2_z.lo, 0.0f});
+}
+__device__ __forceinline__ float to_e(Two v) {  // times log 2
+  return fmaf(v.hi, 0.693147182f, fmaf(v.hi, -1.90465421e-9f, v.lo * 0.693147182f));
+}
+
+// What a warp or CTA tells others: two numbers of two rows.
+struct alignas(16) Post {
+  float a, b, c, d;
+};
+__device__ __forceinline__ Post post_of(float4 v) { return {v.x, v.y, v.z, v.w}; }
+
+// A place in a sequence: its row of the target, and where the sequence is.
+struct Place {
+  int row, s, first, count, j;
+  __device__ __forceinline__ bool behind() const { return j == count; }  // the row behind all drafts
+};
+
+struct Verdict {
+  int stands;  // 1: the draft stands; 0: it falls, or there is none; -1: a row is no distribution; 2: scores are odd
+  float logp;  // of the draft that stands; greedy: of the largest
+  int best;    // greedy
+  Sum zx, zy;
+  float bias_x, bias_y;
+};
+
+__device__ __forceinline__ int start_of(const VerifyParams& p, int64_t s) {
+  if (p.draft_start == nullptr) return s == 0 ? 0 : int(p.n_drafts);
+  return int(min(max(p.draft_start[s], int64_t(0)), p.n_drafts));
+}
+
+// A row's sum with its maximum taken off, by one warp.
+template <class S>
+__device__ __noinline__ Sum odd_sum(S s, float k, int lane, float& bias) {
+  const Piece p = {0, (s.lead + s.n + 7) / 8, -s.lead};
+  float top = -INFINITY;
+  for (int g = lane; g < p.hi; g += 32) {
+    float x[8];
+    s.load(8 * g + p.first, x);
+    top = fmaxf(top, max8(x));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  s.bias = bias = top;
+  return warp_join(careful_sum(s, p, lane, 32, k));
+}
+
+// One warp's verdict on a draft from the parts of its rows' sums. ODD: scores too high or low are worked out
+// here (slowly, from the rows); else such a row has no verdict.
+template <bool XB, bool YB, int MODE, bool ODD>
+__device__ __forceinline__ Verdict decide(const VerifyParams& p, const Place& at, int lane) {
+  const bool drafted = MODE == kDrafted && !at.behind();
+  Scores<XB> x(p.target, at.row, p.vocab);
+  Scores<YB> y(drafted ? p.draft : p.target, drafted ? at.first + at.j : at.row, p.vocab);
+  // (these loads are independent of the parts')
+  const int64_t token = at.behind() ? -1 : p.drafts[at.first + at.j];
+  float u = 0.0f, xt = -INFINITY, yt = -INFINITY;
+  if (MODE != kGreedy && token >= 0 && token < p.vocab) {
+    u = p.uniforms[at.row];
+    xt = x.one(int(token));
+    if (drafted) yt = y.one(int(token));
+  }
+  Post v = {__int_as_float(kNone), 0.0f, MODE == kGreedy ? -INFINITY : __int_as_float(kNone), MODE == kGreedy ? __int_as_float(INT32_MAX) : 0.0f};
+  if (lane < p.parts) v = post_of(__ldcg(reinterpret_cast<const float4*>(p.sums + int64_t(at.row) * p.parts + lane)));
+  Sum zx = warp_join({__float_as_int(v.a), v.b}), zy = {0, 0.5f};
+  Top top = {v.c, __float_as_int(v.d)};
+  if (MODE == kGreedy) top = largest(top);
+  if (drafted) zy = warp_join({__float_as_int(v.c), v.d});
+  Verdict r = {-1, 0.0f, top.at, {0, 0.5f}, {0, 0.5f}, 0.0f, 0.0f};
+  if (zx.s == INFINITY || zx.c == kLow || zy.s == INFINITY || zy.c == kLow) {
+    if (!ODD) {
+      r.stands = 2;
+      return r;
+    }
+    if (zx.s == INFINITY || zx.c == kLow) zx = odd_sum(x, p.target.k, lane, r.bias_x);
+    if (drafted && (zy.s == INFINITY || zy.c == kLow)) zy = odd_sum(y, p.draft.k, lane, r.bias_y);
+  }
+  // neither NaN nor nothing
+  if (!(zx.s > 0.0f && zx.s < INFINITY && zy.s > 0.0f && zy.s < INFINITY)) return r;
+  r.zx = zx = normalized(zx.c, zx.s);
+  r.zy = zy = normalized(zy.c, zy.s);
+  const Two log2_zx = log2_of(zx);
+  r.stands = 0;
+  if (MODE == kGreedy) {
+    r.stands = !at.behind() && token == top.at;
+    r.logp = to_e(log2_p(top.x - r.bias_x, p.target.k, log2_zx));
+    return r;
+  }
+  if (!(xt > -INFINITY)) return r;
+  const Two lp = log2_p(xt - r.bias_x, p.target.k, log2_zx);
+  Two gap = lp;
+  if (drafted) {
+    const Two lq = log2_p(yt - r.bias_y, p.draft.k, log2_of(zy));
+    gap = add(lp, {-lq.hi, -lq.lo});
+  }
+  // (a draft that its own distribution gives nothing stands; a NaN falls)
+  if (u == u && (u <= 0.0f || (drafted && yt == -INFINITY) ||
+                 fminf(u, 0.99999994f) < exp2f(gap.hi) * fmaf(gap.lo, 0.69314718f, 1.0f)))
+    r.stands = 1;
+  r.logp = to_e(lp);
+  return r;
+}
+
+template <bool XB, bool YB, int MODE>
+__global__ void __launch_bounds__(kRowThreads, 4) sums_kernel(const __grid_constant__ VerifyParams p) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  __shared__ Place found;
+  __shared__ int skip;
+  __shared__ Post posts[kRowWarps];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int part = int(blockIdx.x) & (p.parts - 1);
+  const int64_t row = int64_t(blockIdx.x >> p.part_bits) * p.pitch + blockIdx.y;
+  if (row >= p.n_drafts + p.n_seq) return;
+  // the row's sequence, by the thread that has it
+  int any = 0;
+  for (int64_t base = 0; base < p.n_seq && !any; base += kRowThreads) {
+    const int64_t i = base + threadIdx.x;
+    bool here = false;
+    if (i < p.n_seq) {
+      const int first = start_of(p, i), count = max(start_of(p, i + 1) - first, 0);
+      here = first + i <= row && row <= first + i + count;
+      if (here) {
+        found = {int(row), int(i), first, count, int(row - first - i)};
+        skip = p.fallen != nullptr && *const_cast<volatile int*>(p.fallen + i) < row - first - i;
+      }
+    }
+    any = __syncthreads_or(here);
+  }
+  if (!any || skip) return;
+  const Place at = found;
+  const bool drafted = MODE == kDrafted && !at.behind();
+  const Scores<XB> x(p.target, at.row, p.vocab);
+  Scores<YB> y(drafted ? p.draft : p.target, drafted ? at.first + at.j : at.row, p.vocab);
+  y.aligned = ((y.lead - x.lead) & (y.W - 1)) == 0;
+  // this CTA's part, in groups that start on 16 aligned bytes of the target's row
+  const int groups = int((x.lead + p.vocab + 7) / 8), per = (groups + p.parts - 1) >> p.part_bits;
+  const Piece piece = {min(groups, part * per), min(groups, (part + 1) * per), -x.lead};
+  // half of the warps for each row, where there are two
+  constexpr int kHalf = kRowWarps / 2;
+  Top top, none;
+  Sum z;
+  if (!drafted) z = fast_sum<MODE == kGreedy>(x, piece, threadIdx.x, kRowThreads, p.target.k, top);
+  else if (warp < kHalf) z = fast_sum<false>(x, piece, threadIdx.x, 32 * kHalf, p.target.k, none);
+  else z = fast_sum<false>(y, piece, threadIdx.x - 32 * kHalf, 32 * kHalf, p.draft.k, none);
+  z = warp_join(z);
+  if (MODE == kGreedy) top = largest(top);
+  if (lane == 0) posts[warp] = {__int_as_float(z.c), z.s, MODE == kGreedy ? top.x : 0.0f, MODE == kGreedy ? __int_as_float(top.at) : 0.0f};
+  __syncthreads();
+  if (warp != 0) return;
+  const Post v = posts[lane % kRowWarps];
+  z = {__float_as_int(v.a), v.b};
+  const Sum nothing = {kNone, 0.0f};
+  Sum zx = warp_join(lane < (drafted ? kHalf : kRowWarps) ? z : nothing), zy = nothing;
+  if (drafted) zy = warp_join(lane >= kHalf && lane < kRowWarps ? z : nothing);
+  if (MODE == kGreedy) top = largest({v.c, __float_as_int(v.d)});
+  // (sums of many parts grow by a factor of 32 a level: to [1/2, 1) again)
+  if (zx.s > 0.0f && zx.s < INFINITY && zx.c > kLow) zx = normalized(zx.c, zx.s);
+  if (zy.s > 0.0f && zy.s < INFINITY && zy.c > kLow) zy = normalized(zy.c, zy.s);
+  int last = 0;
+  if (lane == 0) {
+    __stcg(reinterpret_cast<float4*>(p.sums + int64_t(at.row) * p.parts + part),
+           MODE == kGreedy ? make_float4(__int_as_float(zx.c), zx.s, top.x, __int_as_float(top.at))
+                           : make_float4(__int_as_float(zx.c), zx.s, __int_as_float(zy.c), zy.s));
+    if (p.fallen != nullptr) {
+      __threadfence();
+      last = atomicAdd(p.done + at.row, 1) == p.parts - 1;
+    }
+  }
+  if (p.fallen == nullptr || at.behind() || !__shfl_sync(~0u, last, 0)) return;
+  __threadfence();
+  const Verdict r = decide<XB, YB, MODE, false>(p, at, lane);
+  if (lane == 0 && (r.stands == 0 || r.stands == -1)) atomicMin(p.fallen + at.s, at.j);
+}
+
+// ---------------------------------------------------------------- draws
+
+// What every warp of a cluster tells the others in one phase.
+enum Phase : int { kExact = 0, kTotals = 1, kTotalsAgain = 2, kPhases = 3 };
 
 struct Shared {
   Post posts[kPhases][kRowWarps];
-  uint64_t full[kRowWarps];  // a warp's part of the rows is in shared memory
-  int abort;
-  int skip;
-  int odd;    // scores so large that their bias has to be taken off first: 1: the target's, 2: the draft's
-  int stands;
-  float bias_x, bias_y;
-  Sum zx, zy;
+  Verdict verdicts[kRowWarps];
   float rho, rho_low;
   int owner;  // of a draw's border: rank * kRowWarps + warp, -1: no weight
   double before, target;
   Two parts[kRowWarps];
-  Two log2_z;
 };
 
 __device__ __forceinline__ void cluster_barrier() {
@@ -144,20 +514,6 @@ __device__ __forceinline__ Post peer_post(const Post* p, int rank) {
       : "memory");
   return v;
 }
-__device__ __forceinline__ int peer_int(const int* p, int rank) {
-  int v;
-  asm volatile(
-      "{\n"
-      ".reg .b32 remote;\n"
-      "mapa.shared::cluster.u32 remote, %1, %2;\n"
-      "ld.shared::cluster.s32 %0, [remote];\n"
-      "}\n"
-      : "=r"(v)
-      : "r"(uint32_t(__cvta_generic_to_shared(p))), "r"(rank)
-      : "memory");
-  return v;
-}
-
 // A phase's posts are written once, then read by every CTA's first warp, two a lane.
 __device__ __forceinline__ void posted(int ranks) {
   if (ranks > 1) cluster_barrier();
@@ -168,283 +524,75 @@ __device__ __forceinline__ Post post_at(const Shared& sh, int phase, int i, int 
   return ranks > 1 ? peer_post(p, i / kRowWarps) : *p;
 }
 
-// A row of scores as a warp sees it: its part in shared memory, where it has
-// been copied to, or the row itself.
-template <bool BF16, bool HOLD>
-struct Scores {
-  static constexpr int ES = BF16 ? 2 : 4, W = 16 / ES;
-  const char* row;
-  int n;
-  int lead;      // elements between 16 aligned bytes and the first one
-  int shift;     // HOLD: element i is at held + shift + i * ES
-  bool aligned;  // groups of 8 start on 16 aligned bytes
-  float bias;    // taken off every score: 0, or the maximum where scores are so large that x k has no fraction
-  __device__ Scores(const VerifyRows& r, int64_t at, int64_t vocab) {
-    row = r.data + at * r.ld * ES;
-    n = int(vocab);
-    lead = int(reinterpret_cast<uintptr_t>(row) / ES % W);
-    shift = 0;
-    aligned = true;
-    bias = 0.0f;
+// 2^(x k - c) to fp32's last place, two at a time; 0 where it is below 2^-126.
+struct Weights {
+  Pair k, minus_k, minus_k_low, c, minus_c;
+  float least;  // (for scores below it the difference to c would have no value)
+  __device__ __forceinline__ Weights(const VerifyRows& r, int shift) {
+    const float f = float(shift);
+    k = pair_of(r.k, r.k), minus_k = pair_of(-r.k, -r.k), minus_k_low = pair_of(-r.k_low, -r.k_low);
+    c = pair_of(f, f), minus_c = pair_of(-f, -f);
+    least = (f - 199.0f) / r.k;
   }
-  __device__ __forceinline__ void place(int from, int offset) { shift = offset - (from - (from + lead + 8) % W) * ES; }
-  // Copies the elements [from, to) to where place() has put them, -inf for those that the row does not have: whole 16
-  // aligned bytes by one bulk copy (its size is returned), the others by the lanes. (from >= -7)
-  __device__ uint32_t copy(int from, int to, int lane, uint64_t* bar) const {
-    const int head = lead > 0 ? W - lead : 0, tail = max(head, (lead + n) / W * W - lead);
-    const int a = max(from - (from + lead + 8) % W, head), b = min(to + (W - (to + lead) % W) % W, tail);
-    const int few = lane < W ? (lane < head ? lane : -1) : tail + lane - W;  // edges: elements 0 .. head - 1, tail .. n - 1
-    if (lane < 2 * W && few >= max(from, 0) && few < min(to, n)) put(few, one(few));
-    if (lane < 8 && from + lane < 0) put(from + lane, -INFINITY);
-    if (lane < 8 && to - 1 - lane >= n) put(to - 1 - lane, -INFINITY);
-    if (b <= a) return 0;
-    if (lane == 0) bulk_load(held + shift + a * ES, row + int64_t(a) * ES, uint32_t(b - a) * ES, bar);
-    return uint32_t(b - a) * ES;
-  }
-  __device__ __forceinline__ void put(int i, float x) const {
-    if (BF16) *reinterpret_cast<uint16_t*>(held + shift + i * ES) = uint16_t(__float_as_uint(x) >> 16);
-    else *reinterpret_cast<float*>(held + shift + i * ES) = x;
-  }
-  __device__ __forceinline__ const char* at(int i) const { return HOLD ? held + shift + i * ES : row + int64_t(i) * ES; }
-  __device__ __forceinline__ float one(int i) const {  // from the row
-    return BF16 ? bf16_to_f32(reinterpret_cast<const uint16_t*>(row)[i]) : reinterpret_cast<const float*>(row)[i];
-  }
-  // Elements i .. i + 7; -inf for those outside the row.
-  __device__ __forceinline__ void load(int i, float (&x)[8]) const {
-    load_as_is(i, x);
-    if (bias != 0.0f) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] -= bias;
-    }
-  }
-  __device__ __forceinline__ void load_as_is(int i, float (&x)[8]) const {
-    if (aligned && (HOLD || (i >= 0 && i + 8 <= n))) {
-      if (BF16) {
-        const uint4 r = *reinterpret_cast<const uint4*>(at(i));
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[2 * j] = bf16lo(w[j]), x[2 * j + 1] = bf16hi(w[j]);
-      } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 r = reinterpret_cast<const float4*>(at(i))[h];
-          x[4 * h] = r.x, x[4 * h + 1] = r.y, x[4 * h + 2] = r.z, x[4 * h + 3] = r.w;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[j] = -INFINITY;
-        if (HOLD || (i + j >= 0 && i + j < n))
-          x[j] = BF16 ? bf16_to_f32(*reinterpret_cast<const uint16_t*>(at(i + j))) : *reinterpret_cast<const float*>(at(i + j));
-      }
-    }
+  __device__ __forceinline__ Pair of(float x0, float x1) const {
+    const Pair x = pair_of(fmaxf(x0, least), fmaxf(x1, least)), p = mul2(x, k), t = add2(p, minus_c);
+    // what t lacks, with the other sign: of the product, of k, of the difference
+    Pair left = fma2(x, minus_k_low, fma2(x, minus_k, p));
+    left = add2(left, fma2(p, pair_of(-1.0f, -1.0f), add2(t, c)));
+    const Pair e = exp2_pair(t);
+    return fma2(e, mul2(left, pair_of(-0.69314718f, -0.69314718f)), e);
   }
 };
-
-// The groups of 8 elements of a warp: element 8 g + first is group g's first. A
-// warp's groups lie one behind the other, so that indexes order like (rank,
-// warp, round, lane, element).
-struct Piece {
-  int lo, hi, first;
-};
-
-// The largest score of a warp's piece, and its first place.
-template <class S>
-__device__ __forceinline__ float top_of(const S& s, const Piece& p, int lane) {
-  float top = -INFINITY;
-#pragma unroll 2
-  for (int g = p.lo + lane; g < p.hi; g += 32) {
-    float x[8];
-    s.load_as_is(8 * g + p.first, x);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, x[j]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  return top;
-}
-
-// 2^d for d <= 0, exactly (0 below the normal numbers).
-__device__ __forceinline__ float pow2(int d) { return d > -127 ? __int_as_float((d + 127) << 23) : 0.0f; }
-
-// Sums: kNone for a part that is all -inf (s = 0). s is NaN where a score was NaN
-// or +inf, +inf (at kOdd, above all shifts) where a bias has to be taken off first.
-constexpr int kNone = -(1 << 28), kOdd = 1 << 28;
-__device__ __forceinline__ Sum normalized(int c, float s) {  // s a normal number: to [1/2, 1)
-  const int bits = __float_as_int(s);
-  return {c + (bits >> 23) - 126, __int_as_float((bits & 0x007fffff) | 0x3f000000)};
-}
-// The sum over a warp's lanes.
-__device__ __forceinline__ Sum warp_join(Sum v) {
-  const int c = __reduce_max_sync(~0u, v.c);
-  float s = v.s * pow2(v.c - c);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-  return {c, s};
-}
-
-// Sums that the first group's shift does not serve: with the thread's maximum.
-template <class S>
-__device__ __noinline__ Sum careful_sum(const S s, const Piece p, int lane, float k) {
-  float top = -INFINITY, sum = 0.0f, x[8];
-  bool nan = false;
-  for (int g = p.lo + lane; g < p.hi; g += 32) {
-    s.load(8 * g + p.first, x);
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, x[j]), nan |= x[j] != x[j];
-  }
-  if (nan || top == INFINITY) return {0, __int_as_float(0x7fc00000)};
-  if (top == -INFINITY) return {kNone, 0.0f};
-  if (!(fabsf(top * k) < 4194304.0f)) return {kOdd, INFINITY};
-  const float c = ceilf(top * k);
-  for (int g = p.lo + lane; g < p.hi; g += 32) {
-    s.load(8 * g + p.first, x);
-    for (int j = 0; j < 8; ++j) sum += exp2_approx(fmaf(x[j], k, -c));
-  }
-  return normalized(int(c), sum);
-}
-
-// The sum over a thread's groups, in one pass: the shift is the first group's. TOP: and the largest score with
-// its first place.
-struct Top {
-  float x;
-  int at;
-};
-__device__ __forceinline__ Top larger(Top a, Top b) { return b.x > a.x || (b.x == a.x && b.at < a.at) ? b : a; }
-__device__ __forceinline__ Top largest(Top v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = larger(v, {__shfl_xor_sync(~0u, v.x, o), __shfl_xor_sync(~0u, v.at, o)});
-  return v;
-}
-__device__ __forceinline__ Sum joined(Sum a, Sum b) {
-  const int c = max(a.c, b.c);
-  return {c, a.s * pow2(a.c - c) + b.s * pow2(b.c - c)};
-}
-template <bool TOP, class S>
-__device__ __forceinline__ Sum fast_sum(const S& s, const Piece& p, int lane, float k, Top& top) {
-  int g = p.lo + lane;
-  if (TOP) top = {-INFINITY, INT32_MAX};
-  if (g >= p.hi) return {kNone, 0.0f};
-  float x[8];
-  s.load(8 * g + p.first, x);
-  float m = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-  const float c = fabsf(m * k) < 4194304.0f ? ceilf(m * k) : 0.0f;
-  const Pair kk = pair_of(k, k), cc = pair_of(-c, -c);
-  int best = g;
-  if (TOP) top.x = m;
-  Two sum = {0.0f, 0.0f};
-  while (g < p.hi) {
-    Pair a = pair_of(0.0f, 0.0f), b = a;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (g < p.hi) {
-        s.load(8 * g + p.first, x);
-        if (TOP) {
-          m = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-          if (m > top.x) top.x = m, best = g;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; j += 4) {
-          a = add2(a, exp2_pair(fma2(pair_of(x[j], x[j + 1]), kk, cc)));
-          b = add2(b, exp2_pair(fma2(pair_of(x[j + 2], x[j + 3]), kk, cc)));
-        }
-      }
-      g += 32;
-    }
-    const float2 v = floats_of(add2(a, b));
-    sum = add(sum, {v.x + v.y, 0.0f});
-  }
-  if (TOP) {
-    s.load(8 * best + p.first, x);
-#pragma unroll
-    for (int j = 7; j >= 0; --j)
-      if (x[j] == top.x) top.at = 8 * best + p.first + j;
-  }
-  if (sum.hi > 7.9e-31f && sum.hi < 1.2e30f) return normalized(int(c), sum.hi);
-  return careful_sum(s, p, lane, k);
-}
-
-// 2^(x k - c) to fp32's last place; 0 where it is below 2^-126.
-struct Weight {
-  float k, k_low, c;
-  __device__ __forceinline__ float operator()(float x) const {
-    const float p = fmaxf(x * k, c - 200.0f), t = p - c;  // (the limit: -inf has no differences)
-    const float left = fmaf(x, k_low, fmaf(x, k, -p)) + (p - (t + c));
-    const float e = exp2_approx(t);
-    return t > -200.0f ? fmaf(e, left * 0.69314718f, e) : 0.0f;
-  }
-};
-
-template <class S>
-__device__ __forceinline__ Two exact_sum(const S& s, const Piece& p, int lane, const Weight& w) {
-  Two sum = {0.0f, 0.0f};
-#pragma unroll 2
-  for (int g = p.lo + lane; g < p.hi; g += 32) {
-    float x[8];
-    s.load(8 * g + p.first, x);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = w(x[j]);
-    sum = add(sum, {((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7])), 0.0f});
-  }
-  return sum;
-}
-
-// log2 of a sum, in two parts.
-__device__ __forceinline__ Two log2_of(Sum v) { return two_sum(float(v.c), log2f(v.s)); }
-// x k less such a logarithm, in two parts. (k as the sum has it, without what fp32 leaves of it.)
-__device__ __forceinline__ Two log2_p(float x, float k, Two log2_z) {
-  const float p = x * k;
-  return add(two_sum(p, -log2_z.hi), {fmaf(x, k, -p) - log2_z.lo, 0.0f});
-}
-__device__ __forceinline__ float to_e(Two v) {  // times log 2
-  return fmaf(v.hi, 0.693147182f, fmaf(v.hi, -1.90465421e-9f, v.lo * 0.693147182f));
-}
 
 // What a token is drawn from: w_i, less the draft's weight (a row's, or one token's).
 enum Less : int { kNothing = 0, kRow = 1, kToken = 2 };
 template <class X, class Y>
 struct Draw {
-  const X& x;
-  const Y& y;
-  Weight wx, wy;
+  static constexpr int kVecsX = X::kVecs, kVecsY = Y::kVecs;
+  X x;
+  Y y;
+  Weights wx, wy;
   float rho, rho_low;  // Z / Z'
   int token;
   int less;
-  __device__ __forceinline__ float weights(int i, float (&w)[8]) const {
-    x.load(i, w);
+  // A group's weights w; exact: of the target (w) and of the draft (v) instead.
+  __device__ __forceinline__ void weights(const uint4 (&rx)[X::kVecs], const uint4 (&ry)[Y::kVecs], int i, bool exact,
+                                          Pair (&w)[4], Pair (&v)[4]) const {
+    float a[8];
+    x.scores(rx, a);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = wx(w[j]);
+    for (int j = 0; j < 4; ++j) w[j] = wx.of(a[2 * j], a[2 * j + 1]);
     if (less == kRow) {
-      float v[8];
-      y.load(i, v);
+      y.scores(ry, a);
+      const Pair r = pair_of(-rho, -rho), r_low = pair_of(-rho_low, -rho_low);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float a = wy(v[j]);
-        w[j] = fmaxf(fmaf(-a, rho_low, fmaf(-a, rho, w[j])), 0.0f);
+      for (int j = 0; j < 4; ++j) {
+        v[j] = wy.of(a[2 * j], a[2 * j + 1]);
+        if (!exact) {
+          const float2 d = floats_of(fma2(v[j], r_low, fma2(v[j], r, w[j])));
+          w[j] = pair_of(fmaxf(d.x, 0.0f), fmaxf(d.y, 0.0f));
+        }
       }
     } else if (less == kToken) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (i + j == token) w[j] = 0.0f;
+      for (int j = 0; j < 4; ++j) {
+        const float2 d = floats_of(w[j]);
+        w[j] = pair_of(i + 2 * j == token ? 0.0f : d.x, i + 2 * j + 1 == token ? 0.0f : d.y);
+      }
     }
-    return ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
   }
-  __device__ __forceinline__ Two total(const Piece& p, int lane) const {
-    Two sum = {0.0f, 0.0f};
-#pragma unroll 2
-    for (int g = p.lo + lane; g < p.hi; g += 32) {
-      float w[8];
-      sum = add(sum, {weights(8 * g + p.first, w), 0.0f});
-    }
-    return warp_sum(sum);
+  __device__ __forceinline__ void fetch(int i, uint4 (&rx)[X::kVecs], uint4 (&ry)[Y::kVecs]) const {
+    x.fetch(i, rx);
+    if (less == kRow) y.fetch(i, ry);
   }
 };
+__device__ __forceinline__ Pair sum4(const Pair (&w)[4]) { return add2(add2(w[0], w[1]), add2(w[2], w[3])); }
 
 // Of up to 64 parts one behind the other (each lane's two), the one that the border lies in, and the sum before it
 // (one warp). Behind the last border by rounding: the last part with weight; -1: none has any.
-__device__ __forceinline__ int part_of(double v0, double v1, double before_all, double target, int lane, double& before) {
+__device__ __noinline__ int part_of(double v0, double v1, double before_all, double target, int lane, double* before) {
   double run = v0 + v1;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const double v = __shfl_up_sync(~0u, run, o);
     if (lane >= o) run += v;
@@ -456,352 +604,226 @@ __device__ __forceinline__ int part_of(double v0, double v1, double before_all, 
   if (some == 0) return -1;
   const int owner = over != 0 ? __ffs(int(over)) - 1 : 31 - __clz(int(some));
   const bool low = over != 0 ? first : !(v1 > 0.0);
-  before = __shfl_sync(~0u, low ? mine : mine + v0, owner);
+  *before = __shfl_sync(~0u, low ? mine : mine + v0, owner);
   return 2 * owner + (__shfl_sync(~0u, int(low), owner) != 0 ? 0 : 1);
 }
 
 // The border's token, by the warp whose piece it lies in.
 template <class D>
 __device__ __forceinline__ int token_at(const D& d, const Piece& p, int lane, double before, double target) {
-  int last = -1, hit = -1;
-  for (int g0 = p.lo; g0 < p.hi && hit < 0; g0 += 32) {
+  int found = -1;
+#pragma unroll 1
+  for (int g0 = p.lo; g0 < p.hi; g0 += 32) {
     const int i = 8 * (g0 + lane) + p.first;
-    float w[8];
-    double chunk = 0.0;
-    if (g0 + lane < p.hi) chunk = double(d.weights(i, w));
-    double run = chunk;  // of the lanes up to this one
+    Pair w[4], v[4];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double v = __shfl_up_sync(~0u, run, o);
-      if (lane >= o) run += v;
+    for (int j = 0; j < 4; ++j) w[j] = pair_of(0.0f, 0.0f);
+    if (g0 + lane < p.hi) {
+      uint4 rx[D::kVecsX], ry[D::kVecsY];
+      d.fetch(i, rx, ry);
+      d.weights(rx, ry, i, false, w, v);
     }
-    const unsigned over = __ballot_sync(~0u, chunk > 0.0 && before + run > target), some = __ballot_sync(~0u, chunk > 0.0);
-    if (some != 0) {
-      // the lane that holds the border, else the last one with weight
-      const int owner = over != 0 ? __ffs(int(over)) - 1 : 31 - __clz(int(some));
-      if (lane == owner) {
-        double at = before + (run - chunk);
+    const float2 total = floats_of(sum4(w));
+    const double chunk = double(total.x + total.y);
+    double upto = 0.0;
+    const int at = part_of(chunk, 0.0, before, target, lane, &upto);
+    if (at < 0) continue;
+    // the lane that holds the border, else the last one with weight
+    int hit = -1, last = -1;
+    bool over = false;
+    if (lane == at / 2) {
+      double run = upto;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          at += double(w[j]);
-          if (w[j] > 0.0f) {
-            last = i + j;
-            if (at > target && hit < 0) hit = last;
-          }
-        }
-        if (over != 0 && hit < 0) hit = last;
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = floats_of(w[j]);
+        run += double(f.x);
+        if (f.x > 0.0f) last = i + 2 * j, hit = hit < 0 && run > target ? last : hit;
+        run += double(f.y);
+        if (f.y > 0.0f) last = i + 2 * j + 1, hit = hit < 0 && run > target ? last : hit;
       }
-      last = __shfl_sync(~0u, last, owner);
-      hit = __shfl_sync(~0u, hit, owner);
+      over = upto + chunk > target;
     }
-    before += __shfl_sync(~0u, run, 31);
+    found = __shfl_sync(~0u, hit >= 0 ? hit : last, at / 2);
+    if (__shfl_sync(~0u, int(over), at / 2) != 0) break;
+    double all = chunk;
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(~0u, all, o);
+    before += all;
   }
-  return hit >= 0 ? hit : last;
+  return found;
 }
 
-__device__ __forceinline__ int64_t start_of(const VerifyParams& p, int64_t s) {
-  if (p.draft_start == nullptr) return s == 0 ? 0 : p.n_drafts;
-  return min(max(p.draft_start[s], int64_t(0)), p.n_drafts);
-}
-
-template <bool XB, bool YB, int MODE, bool HOLD>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ VerifyParams p) {
-  using X = Scores<XB, HOLD>;
-  using Y = Scores<YB, HOLD>;
+template <bool XB, bool YB, int MODE>
+__global__ void __launch_bounds__(kRowThreads, kDrawCtas) draw_kernel(const __grid_constant__ VerifyParams p) {
+  using X = Scores<XB>;
+  using Y = Scores<YB>;
   grid_dependency_wait();
   grid_dependents_launch();
   __shared__ Shared sh;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int ranks = p.ranks, rank = int(blockIdx.x) % ranks;
-  // rows are visited `pitch` apart, so that those of a sequence come one after the other
-  const int64_t item = int64_t(blockIdx.x) / ranks, across = (p.n_drafts + p.n_seq + p.pitch - 1) / p.pitch;
-  const int64_t row = item % across * p.pitch + item / across;
-  if (row >= p.n_drafts + p.n_seq) return;
-  if (HOLD && threadIdx.x < kRowWarps) mbar_init(&sh.full[threadIdx.x], 1);
-  if (threadIdx.x == 0) sh.abort = 0;
-  if (HOLD) mbar_init_fence();
-  // the sequence: the last one whose first row is not behind this one
-  int64_t s = -1;
-  for (int64_t base = 0; base < p.n_seq; base += kRowThreads) {
-    const int64_t i = base + threadIdx.x;
-    const int n = __syncthreads_count(i < p.n_seq && start_of(p, i) + i <= row);
-    s += n;
-    if (n < kRowThreads) break;
-  }
-  if (s < 0) return;
-  const int64_t first = start_of(p, s), count = max(start_of(p, s + 1) - first, int64_t(0)), place = row - s - first;
-  if (place < 0 || place > count) return;
-  if (p.fallen != nullptr) {
-    // all CTAs of the cluster go by what the first one sees
-    if (threadIdx.x == 0) sh.skip = *const_cast<volatile int*>(p.fallen + s) < place;
-    int skip;
-    if (ranks > 1) {
-      cluster_barrier();
-      skip = peer_int(&sh.skip, 0);
-      if (skip) cluster_barrier();  // (read by all before the first one goes)
-    } else {
-      __syncthreads();
-      skip = sh.skip;
+  const int ranks = 1 << p.rank_bits, rank = int(blockIdx.x) & (ranks - 1), s = int(blockIdx.x >> p.rank_bits);
+  const int first = start_of(p, s), count = max(start_of(p, s + 1) - first, 0), row0 = first + s;
+  // a warp a draft, eight at a time, until one falls (there is none in the last row); where rows may have been skipped
+  // it is the one that they were skipped for
+  const int stop = p.fallen != nullptr ? __ldcg(p.fallen + s) : -1;
+  int a;
+  for (int j0 = 0;; j0 += kRowWarps) {
+    const int j = j0 + warp;
+    Verdict v = {0};
+    if (j <= count) {
+      v = decide<XB, YB, MODE, true>(p, {row0 + j, s, first, count, j}, lane);
+      if (j == stop) v.stands = min(v.stands, 0);
+      if (lane == 0) sh.verdicts[warp] = v;
     }
-    if (skip) return;
+    __syncthreads();
+    a = j0;
+    while (a < j0 + kRowWarps && a < count && sh.verdicts[a - j0].stands == 1) ++a;
+    if (rank == 0 && lane == 0 && j < a) {
+      p.tokens[row0 + j] = p.drafts[first + j];
+      p.logp[row0 + j] = v.logp;
+    }
+    if (a < j0 + kRowWarps) break;
+    __syncthreads();
   }
-  const bool behind = place == count;  // the row behind all drafts
-  const bool drafted = MODE == kDrafted && !behind;
+  const Verdict at = sh.verdicts[a % kRowWarps];
+  if (rank == 0) {
+    if (threadIdx.x == 0) p.accepted[s] = a;
+    for (int j = a + 1 + int(threadIdx.x); j <= count; j += kRowThreads) {
+      p.tokens[row0 + j] = -1;
+      p.logp[row0 + j] = 0.0f;
+    }
+  }
+  const int row = row0 + a;
+  if (MODE == kGreedy || at.stands < 0) {
+    if (rank == 0 && threadIdx.x == 0) {
+      p.tokens[row] = at.stands < 0 ? -1 : at.best;
+      p.logp[row] = at.stands < 0 ? __int_as_float(0x7fc00000) : at.logp;
+    }
+    return;
+  }
+
+  const bool behind = a == count, drafted = MODE == kDrafted && !behind;
   X x(p.target, row, p.vocab);
-  Y y(drafted ? p.draft : p.target, drafted ? first + place : row, p.vocab);
-  if (drafted) y.aligned = ((y.lead - x.lead) & (Y::W - 1)) == 0;
-  // this CTA's part, in groups that start on 16 aligned bytes of the target's row, and its warps' (whole rounds)
-  const int groups = int((x.lead + p.vocab + 7) / 8), per = (groups + ranks - 1) / ranks;
+  Y y(drafted ? p.draft : p.target, drafted ? first + a : row, p.vocab);
+  y.aligned = ((y.lead - x.lead) & (Y::W - 1)) == 0;
+  // this CTA's part, in groups that start on 16 aligned bytes of the target's row, and its warps' (whole rounds):
+  // indexes order like (rank, warp, round, lane, element)
+  const int groups = int((x.lead + p.vocab + 7) / 8), per = (groups + ranks - 1) >> p.rank_bits;
   const int g0 = min(groups, rank * per), g1 = min(groups, g0 + per);
   const int per_warp = (g1 - g0 + 32 * kRowWarps - 1) / (32 * kRowWarps) * 32;
   const auto piece_of = [&](int w) { return Piece{min(g1, g0 + w * per_warp), min(g1, g0 + (w + 1) * per_warp), -x.lead}; };
-  const Piece piece = piece_of(warp);
-  // shared memory: the target's part, then the draft's, each warp's with up to 16 bytes on both sides
-  const auto place_rows = [&](int w) {
-    const Piece q = piece_of(w);
-    x.place(8 * q.lo + q.first, (q.lo - g0) * 8 * X::ES);
-    if (drafted) y.place(8 * q.lo + q.first, (g1 - g0) * 8 * X::ES + (q.lo - g0) * 8 * Y::ES + w * 32);
-  };
-  if (HOLD) place_rows(warp);
-  if (HOLD && piece.lo < piece.hi) {
-    const int from = 8 * piece.lo + piece.first, to = 8 * piece.hi + piece.first;
-    uint32_t bytes = x.copy(from, to, lane, &sh.full[warp]);
-    if (drafted) bytes += y.copy(from, to, lane, &sh.full[warp]);
-    if (lane == 0) mbar_arrive_expect_tx(&sh.full[warp], bytes);
-  }
-  // what thread 0 needs for the decision
-  int64_t token = -1;
-  float xt = -INFINITY, yt = -INFINITY, u_draft = 0.0f, u_draw = 0.0f;
-  if (!behind && (threadIdx.x == 0 || MODE == kLookup)) token = p.drafts[first + place];
-  const bool inside = token >= 0 && token < p.vocab;
-  if (MODE != kGreedy) {
-    u_draw = p.uniforms[s + first + count];
-    if (threadIdx.x == 0 && inside) {
-      xt = x.one(int(token));
-      if (drafted) yt = y.one(int(token));
-      u_draft = p.uniforms[row];
+  Piece piece = piece_of(warp);
+  const int64_t token = behind || drafted ? -1 : p.drafts[first + a];
+  const float last = p.uniforms[row0 + count];
+  const float u = fminf(fmaxf(last == last ? last : 0.0f, 0.0f), 0.99999994f);
+  Draw<X, Y> d = {x, y, Weights(p.target, at.zx.c), Weights(drafted ? p.draft : p.target, at.zy.c), 0.0f, 0.0f,
+                  token >= 0 && token < p.vocab ? int(token) : -1, behind ? kNothing : drafted ? kRow : kToken};
+  d.x.bias = at.bias_x;
+  d.y.bias = at.bias_y;
+  // exact sums of both rows; the totals of what is drawn from (of p itself where there is no residue); those of the
+  // owner's piece, once more over all its warps; then the round of the warp that has the border
+  enum Stage : int { kBoth, kWhole, kWholeAgain, kOwner };
+#pragma unroll 1
+  for (int stage = drafted ? kBoth : kWhole;;) {
+    Two sx = {0.0f, 0.0f}, sy = {0.0f, 0.0f};
+#pragma unroll 1
+    for (int g = piece.lo + lane; g < piece.hi; g += kRounds * 32) {
+      uint4 rx[kRounds][X::kVecs], ry[kRounds][Y::kVecs];
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        X::nothing(rx[r]);
+        Y::nothing(ry[r]);
+        if (g + 32 * r < piece.hi) d.fetch(8 * (g + 32 * r) + piece.first, rx[r], ry[r]);
+      }
+      Pair a = pair_of(0.0f, 0.0f), b = a;
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        Pair w[4], v[4];
+        d.weights(rx[r], ry[r], 8 * (g + 32 * r) + piece.first, stage == kBoth, w, v);
+        a = add2(a, sum4(w));
+        if (stage == kBoth) b = add2(b, sum4(v));
+      }
+      const float2 f = floats_of(a), h = floats_of(b);
+      sx = add(sx, {f.x + f.y, 0.0f});
+      if (stage == kBoth) sy = add(sy, {h.x + h.y, 0.0f});
     }
-  }
-  bool copied = true;
-  if (HOLD && piece.lo < piece.hi) {
-    const StatusRef status = {p.status_word, p.status_host};
-    copied = mbar_wait(&sh.full[warp], 0, kPolls, &sh.abort, status);
-    __syncwarp();
-  }
-
-  // the sums, once more where the scores turn out to be too large as they are
-  const float kx = p.target.k, ky = p.draft.k;
-  for (int again = 0; again < 2; ++again) {
-    Top top, none;
-    Sum zx = warp_join(fast_sum<MODE == kGreedy>(x, piece, lane, kx, top)), zy = {0, 0.5f};
-    if (drafted) zy = warp_join(fast_sum<false>(y, piece, lane, ky, none));
-    if (MODE == kGreedy) top = largest(top);
-    if (lane == 0)
-      sh.posts[2 * again][warp] = MODE == kGreedy ? Post{__int_as_float(zx.c), zx.s, top.x, __int_as_float(top.at)}
-                                                  : Post{__int_as_float(zx.c), zx.s, __int_as_float(zy.c), zy.s};
+    sx = warp_sum(sx);
+    if (stage == kOwner) {
+      if (lane == 0) sh.parts[warp] = sx;
+      break;
+    }
+    if (stage == kBoth) sy = warp_sum(sy);
+    if (lane == 0) sh.posts[stage][warp] = {sx.hi, sx.lo, sy.hi, sy.lo};
     posted(ranks);
     if (warp == 0) {
-      Sum ax[2], ay[2];
-      Top at[2];
+      Post v[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int i = lane + 32 * h;
-        ax[h] = ay[h] = {kNone, 0.0f};
-        at[h] = {-INFINITY, INT32_MAX};
-        if (i < ranks * kRowWarps) {
-          const Post v = post_at(sh, 2 * again, i, ranks);
-          ax[h] = {__float_as_int(v.a), v.b};
-          if (MODE == kGreedy) at[h] = {v.c, __float_as_int(v.d)};
-          else ay[h] = {__float_as_int(v.c), v.d};
-        }
+        v[h] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (2 * lane + h < ranks * kRowWarps) v[h] = post_at(sh, stage, 2 * lane + h, ranks);
       }
-      zx = warp_join(joined(ax[0], ax[1]));
-      if (MODE == kDrafted) zy = warp_join(joined(ay[0], ay[1]));
-      if (MODE == kGreedy) top = largest(larger(at[0], at[1]));
-      const int odd = again > 0 ? 0 : (zx.s == INFINITY ? 1 : 0) | (drafted && zy.s == INFINITY ? 2 : 0);
-      // neither NaN nor nothing
-      const bool ok = zx.s > 0.0f && zx.s < INFINITY && (!drafted || (zy.s > 0.0f && zy.s < INFINITY));
-      if (lane == 0) sh.odd = odd;
-      if (lane == 0 && odd == 0) {
-        RowResult* result = p.results + row;
-        bool fell = true;
-        sh.stands = 1;  // 1: no draw follows
-        if (!ok) {
-          if (rank == 0) *result = {-1, __int_as_float(0x7fc00000), 0.0f, 0, 0};
-        } else {
-          sh.zx = zx = normalized(zx.c, zx.s);
-          const Two log2_zx = log2_of(zx);
-          sh.log2_z = log2_zx;
-          if (MODE == kGreedy) {
-            const float lp = to_e(log2_p(top.x, kx, log2_zx));
-            fell = token != top.at;
-            if (rank == 0) *result = {top.at, lp, lp, int32_t(!behind && !fell), 0};
-          } else {
-            sh.stands = 0;
-            if (drafted) sh.zy = zy = normalized(zy.c, zy.s);
-            if (xt > -INFINITY) {
-              const Two lp = log2_p(xt - x.bias, kx, log2_zx);
-              Two gap = lp;
-              if (drafted) {
-                const Two lq = log2_p(yt - y.bias, ky, log2_of(zy));
-                gap = add(lp, {-lq.hi, -lq.lo});
-              }
-              // (a draft that its own distribution gives nothing stands)
-              const bool stands = u_draft <= 0.0f || (drafted && yt == -INFINITY) ||
-                                  fminf(u_draft, 0.99999994f) < exp2f(gap.hi) * fmaf(gap.lo, 0.69314718f, 1.0f);
-              if (stands && u_draft == u_draft) {
-                sh.stands = 1;
-                fell = false;
-                if (rank == 0) *result = {-1, 0.0f, to_e(lp), 1, 0};
-              }
-            }
-          }
-        }
-        if (p.fallen != nullptr && rank == 0 && !behind && fell) atomicMin(p.fallen + s, int(place));
-      }
-    }
-    __syncthreads();
-    if (sh.odd == 0) break;
-    const float mx = top_of(x, piece, lane), my = drafted ? top_of(y, piece, lane) : 0.0f;
-    if (lane == 0) sh.posts[kTops][warp] = {mx, my, 0.0f, 0.0f};
-    posted(ranks);
-    if (threadIdx.x == 0) {
-      float bx = mx, by = my;
-      for (int i = 0; i < ranks * kRowWarps; ++i) {
-        const Post v = post_at(sh, kTops, i, ranks);
-        bx = fmaxf(bx, v.a), by = fmaxf(by, v.b);
-      }
-      sh.bias_x = sh.odd & 1 ? bx : 0.0f;
-      sh.bias_y = sh.odd & 2 ? by : 0.0f;
-    }
-    __syncthreads();
-    x.bias = sh.bias_x;
-    y.bias = sh.bias_y;
-  }
-  if (MODE != kGreedy && !sh.stands) {
-    Draw<X, Y> d = {x, y, {kx, p.target.k_low, float(sh.zx.c)}, {ky, p.draft.k_low, drafted ? float(sh.zy.c) : 0.0f}, 0.0f, 0.0f,
-                    inside ? int(token) : -1, behind ? kNothing : drafted ? kRow : kToken};
-    if (drafted) {
-      const Two a = warp_sum(exact_sum(x, piece, lane, d.wx)), b = warp_sum(exact_sum(y, piece, lane, d.wy));
-      if (lane == 0) sh.posts[kExact][warp] = {a.hi, a.lo, b.hi, b.lo};
-      posted(ranks);
-      if (warp == 0) {
-        Two c = {0.0f, 0.0f}, e = {0.0f, 0.0f};
-        for (int i = lane; i < ranks * kRowWarps; i += 32) {
-          const Post v = post_at(sh, kExact, i, ranks);
-          c = add(c, {v.a, v.b});
-          e = add(e, {v.c, v.d});
-        }
-        c = warp_sum(c);
-        e = warp_sum(e);
+      const Two c = warp_sum(add({v[0].a, v[0].b}, {v[1].a, v[1].b}));
+      if (stage == kBoth) {
+        const Two e = warp_sum(add({v[0].c, v[0].d}, {v[1].c, v[1].d}));
         // the quotient of both pairs: a rounded one, and what it leaves
         const float rho = c.hi / e.hi;
         if (lane == 0) sh.rho = rho, sh.rho_low = ((fmaf(-rho, e.hi, c.hi) + c.lo) - rho * e.lo) / e.hi;
-      }
-      __syncthreads();
-      d.rho = sh.rho;
-      d.rho_low = sh.rho_low;
-    }
-    const float u = fminf(fmaxf(u_draw == u_draw ? u_draw : 0.0f, 0.0f), 0.99999994f);
-    for (int again = 0; again < 2; ++again) {
-      const Two total = d.total(piece, lane);
-      if (lane == 0) sh.posts[kTotals + again][warp] = {total.hi, total.lo, 0.0f, 0.0f};
-      posted(ranks);
-      if (warp == 0) {
-        double v[2] = {0.0, 0.0}, before = 0.0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (2 * lane + h < ranks * kRowWarps) {
-            const Post t = post_at(sh, kTotals + again, 2 * lane + h, ranks);
-            v[h] = wide({t.a, t.b});
-          }
-        double all = v[0] + v[1];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(~0u, all, o);
-        const double target = double(u) * all;
-        const int owner = part_of(v[0], v[1], 0.0, target, lane, before);
+      } else {
+        const double target = double(u) * wide(c);
+        double before = 0.0;
+        const int owner = part_of(wide({v[0].a, v[0].b}), wide({v[1].a, v[1].b}), 0.0, target, lane, &before);
         if (lane == 0) sh.owner = owner, sh.before = before, sh.target = target;
       }
-      __syncthreads();
-      if (sh.owner >= 0) break;
-      d.less = kNothing;  // no residue: from p itself
     }
-    if (sh.owner >= 0 && sh.owner / kRowWarps == rank) {
-      // the owner's piece, once more over all warps, then the round of the warp that has the border
+    __syncthreads();
+    if (stage == kBoth) {
+      d.rho = sh.rho;
+      d.rho_low = sh.rho_low;
+      stage = kWhole;
+    } else if (sh.owner < 0 && stage == kWhole) {
+      d.less = kNothing;
+      stage = kWholeAgain;
+    } else {
+      if (sh.owner < 0 || sh.owner / kRowWarps != rank) break;
       const Piece q = piece_of(sh.owner % kRowWarps);
-      if (HOLD) place_rows(sh.owner % kRowWarps);
       const int per_part = ((q.hi - q.lo + kRowWarps - 1) / kRowWarps + 31) / 32 * 32;
-      const Piece part = {min(q.hi, q.lo + warp * per_part), min(q.hi, q.lo + (warp + 1) * per_part), q.first};
-      const Two total = d.total(part, lane);
-      if (lane == 0) sh.parts[warp] = total;
-      __syncthreads();
-      const double v = lane < kRowWarps ? wide(sh.parts[lane]) : 0.0;
-      double before = 0.0;
-      const int owner = part_of(v, 0.0, sh.before, sh.target, lane, before) / 2;
-      if (owner == warp) {
-        const int found = token_at(d, part, lane, before, sh.target);
-        if (lane == 0 && found >= 0)
-          p.results[row] = {found, to_e(log2_p(x.one(found) - x.bias, kx, sh.log2_z)), 0.0f, 0, 0};
-      }
+      piece = {min(q.hi, q.lo + warp * per_part), min(q.hi, q.lo + (warp + 1) * per_part), q.first};
+      stage = kOwner;
     }
   }
-  if (!copied) {  // (recorded; the copy may still be under way, and shared memory has to stay until it is not)
-    for (uint32_t i = 0; i < kPolls && !mbar_try_wait(&sh.full[warp], 0); ++i) {
+  if (sh.owner >= 0 && sh.owner / kRowWarps == rank) {
+    __syncthreads();
+    const double v = lane < kRowWarps ? wide(sh.parts[lane]) : 0.0;
+    double before = 0.0;
+    const int owner = part_of(v, 0.0, sh.before, sh.target, lane, &before) / 2;
+    if (owner == warp) {
+      const int found = token_at(d, piece, lane, before, sh.target);
+      if (lane == 0) {
+        p.tokens[row] = found;
+        p.logp[row] = found >= 0 ? to_e(log2_p(x.one(found) - at.bias_x, p.target.k, log2_of(at.zx))) : 0.0f;
+      }
     }
   }
   if (ranks > 1) cluster_barrier();  // no CTA goes while another may still read from it
 }
 
-// No draft of any sequence has fallen yet.
+// No row is done, and no draft of any sequence has fallen yet.
 __global__ void __launch_bounds__(256) clear_kernel(const __grid_constant__ VerifyParams p) {
   grid_dependency_wait();
   grid_dependents_launch();
-  const int64_t s = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (s < p.n_seq) p.fallen[s] = INT32_MAX;
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i < p.n_seq) p.fallen[i] = INT32_MAX;
+  if (i < p.n_drafts + p.n_seq) p.done[i] = 0;
 }
 
-// A warp a sequence: the first draft that falls, and the tokens up to it.
-__global__ void __launch_bounds__(256) tokens_kernel(const __grid_constant__ VerifyParams p) {
-  grid_dependency_wait();
-  grid_dependents_launch();
-  const int64_t s = int64_t(blockIdx.x) * 8 + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  if (s >= p.n_seq) return;
-  const int64_t first = start_of(p, s), count = max(start_of(p, s + 1) - first, int64_t(0)), row = first + s;
-  int64_t a = count;
-  for (int64_t j = 0; j < count; j += 32) {
-    const unsigned falls = __ballot_sync(~0u, j + lane < count && p.results[row + j + lane].stands == 0);
-    if (falls != 0) {
-      a = j + __ffs(int(falls)) - 1;
-      break;
-    }
-  }
-  for (int64_t j = lane; j <= count; j += 32) {
-    const RowResult& r = p.results[row + j];
-    int64_t token = -1;
-    float logp = 0.0f;
-    if (j < a) {
-      token = p.drafts[first + j];
-      logp = r.draft_logp;
-    } else if (j == a) {
-      token = r.token >= 0 && r.token < p.vocab ? r.token : -1;
-      logp = r.token_logp;
-    }
-    p.tokens[row + j] = token;
-    p.logp[row + j] = logp;
-  }
-  if (lane == 0) p.accepted[s] = a;
-}
+// ---------------------------------------------------------------- launches
 
 // Launched so that it may be scheduled while the kernel before it drains; every
 // kernel here waits for that one before it touches memory.
-cudaError_t launch_after(void (*kernel)(VerifyParams), const VerifyParams& p, int64_t grid, int threads, int cluster,
-                         size_t smem, cudaStream_t stream) {
-  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+cudaError_t launch_after(void (*kernel)(VerifyParams), const VerifyParams& p, dim3 grid, int cluster, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(grid));
-  cfg.blockDim = dim3(unsigned(threads));
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kRowThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -814,56 +836,53 @@ cudaError_t launch_after(void (*kernel)(VerifyParams), const VerifyParams& p, in
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <bool HOLD>
-void (*rows_kernel_of(const VerifyParams& p))(VerifyParams) {
+using Kernel = void (*)(VerifyParams);
+
+Kernel sums_of(const VerifyParams& p) {
   const bool x = p.target.bf16 != 0, y = p.draft.bf16 != 0;
-  if (p.greedy) return x ? rows_kernel<true, true, kGreedy, HOLD> : rows_kernel<false, false, kGreedy, HOLD>;
-  if (p.draft.data == nullptr) return x ? rows_kernel<true, true, kLookup, HOLD> : rows_kernel<false, false, kLookup, HOLD>;
-  if (x) return y ? rows_kernel<true, true, kDrafted, HOLD> : rows_kernel<true, false, kDrafted, HOLD>;
-  return y ? rows_kernel<false, true, kDrafted, HOLD> : rows_kernel<false, false, kDrafted, HOLD>;
+  if (p.greedy) return x ? sums_kernel<true, true, kGreedy> : sums_kernel<false, false, kGreedy>;
+  if (p.draft.data == nullptr) return x ? sums_kernel<true, true, kLookup> : sums_kernel<false, false, kLookup>;
+  if (x) return y ? sums_kernel<true, true, kDrafted> : sums_kernel<true, false, kDrafted>;
+  return y ? sums_kernel<false, true, kDrafted> : sums_kernel<false, false, kDrafted>;
+}
+Kernel draw_of(const VerifyParams& p) {
+  const bool x = p.target.bf16 != 0, y = p.draft.bf16 != 0;
+  if (p.greedy) return x ? draw_kernel<true, true, kGreedy> : draw_kernel<false, false, kGreedy>;
+  if (p.draft.data == nullptr) return x ? draw_kernel<true, true, kLookup> : draw_kernel<false, false, kLookup>;
+  if (x) return y ? draw_kernel<true, true, kDrafted> : draw_kernel<true, false, kDrafted>;
+  return y ? draw_kernel<false, true, kDrafted> : draw_kernel<false, false, kDrafted>;
 }
 
-// Shared memory of a CTA: its part of the target's row in whole groups, and
-// the draft's elements of the same places, each warp's with up to 16 bytes on both sides.
-int64_t part_bytes(const VerifyParams& p, int ranks) {
-  const int64_t groups = (p.vocab + 14) / 8, per = (groups + ranks - 1) / ranks;
-  const int64_t x = per * 8 * (p.target.bf16 ? 2 : 4);
-  return p.draft.data == nullptr ? x : x + per * 8 * (p.draft.bf16 ? 2 : 4) + 32 * kRowWarps;
-}
-
-constexpr int64_t kMostHeld = 220 << 10;   // what a CTA can have, less its static part
-constexpr int64_t kGoodPart = 72 << 10;    // three CTAs an SM: one copies while others compute
-constexpr int64_t kLeastPart = 8 << 10;
+constexpr int64_t kPart = 32768, kLeastPart = 4096;  // elements of a row that a CTA of sums_kernel takes
+constexpr int64_t kLeastDraw = 2048;                 // ... of draw_kernel: a round of all its warps
 
 }  // namespace
 
 cudaError_t launch_verify(const VerifyParams& q, cudaStream_t stream) {
   VerifyParams p = q;
   const int64_t rows = p.n_drafts + p.n_seq, sms = device_sms();
-  p.ranks = 1;
-  while (p.ranks < kMaxRanks && part_bytes(p, p.ranks) > kGoodPart) p.ranks *= 2;
-  // few rows: spread over all SMs
-  while (p.ranks < kMaxRanks && rows * p.ranks * 2 <= 2 * sms && part_bytes(p, 2 * p.ranks) >= kLeastPart) p.ranks *= 2;
-  while (p.ranks > 1 && rows * p.ranks > 0x7fffffff) p.ranks /= 2;
-  const int64_t part = part_bytes(p, p.ranks);
-  const bool hold = part <= kMostHeld;
-  void (*kernel)(VerifyParams) = hold ? rows_kernel_of<true>(p) : rows_kernel_of<false>(p);
-  const size_t smem = hold ? size_t(part) : 0;
-  if (smem > (40 << 10)) {
-    const cudaError_t err = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostHeld));
-    if (err != cudaSuccess) return err;
-  }
+  // parts of a row: of a good size, or smaller where that keeps SMs without work
+  p.part_bits = 0;
+  while (p.part_bits < kVerifyPartBits && (p.vocab >> p.part_bits) > kPart) ++p.part_bits;
+  while (p.part_bits < kVerifyPartBits && (rows << p.part_bits) < 2 * sms && (p.vocab >> p.part_bits) >= 2 * kLeastPart) ++p.part_bits;
+  while (p.part_bits > 0 && (rows << p.part_bits) > 0x7fffffff) --p.part_bits;
+  p.parts = 1 << p.part_bits;
   // more rows than run at once: by their place in their sequence, and not behind a draft that fell
-  const bool waves = rows * p.ranks > 3 * sms && p.n_drafts > 0;
-  p.pitch = waves ? (rows + p.n_seq - 1) / p.n_seq : 1;
-  if ((rows + p.pitch) * p.ranks > 0x7fffffff) p.pitch = 1;
+  const bool waves = rows * p.parts > 4 * sms && p.n_drafts > 0 && rows / p.n_seq < 60000;
+  p.pitch = waves ? int((rows + p.n_seq - 1) / p.n_seq) : 1;
   if (!waves) p.fallen = nullptr;
-  cudaError_t err = status_ref(&p.status_word, &p.status_host);
-  if (err == cudaSuccess && waves) err = launch_after(clear_kernel, p, (p.n_seq + 255) / 256, 256, 1, 0, stream);
-  const int64_t items = (rows + p.pitch - 1) / p.pitch * p.pitch;
-  if (err == cudaSuccess) err = launch_after(kernel, p, items * p.ranks, kRowThreads, p.ranks, smem, stream);
-  if (err == cudaSuccess) err = launch_after(tokens_kernel, p, (p.n_seq + 7) / 8, 256, 1, 0, stream);
+  // a cluster a sequence, all at once where they fit
+  p.rank_bits = 0;
+  if (!p.greedy)
+    while ((1 << p.rank_bits) < kMaxRanks && (p.n_seq << p.rank_bits) * 2 <= kDrawCtas * sms && (p.vocab >> p.rank_bits) >= 2 * kLeastDraw)
+      ++p.rank_bits;
+  cudaError_t err = cudaSuccess;
+  if (err == cudaSuccess && waves) err = launch_after(clear_kernel, p, dim3(unsigned((rows + 255) / 256)), 1, stream);
+  const int64_t across = (rows + p.pitch - 1) / p.pitch;
+  if (err == cudaSuccess)
+    err = launch_after(sums_of(p), p, dim3(unsigned(across << p.part_bits), unsigned(p.pitch)), 1, stream);
+  if (err == cudaSuccess)
+    err = launch_after(draw_of(p), p, dim3(unsigned(p.n_seq << p.rank_bits)), 1 << p.rank_bits, stream);
   return err;
 }
 

@@ -10,14 +10,12 @@
 
 namespace ar {
 
-// What a row's CTA leaves for the sequence: whether its draft stands, the
-// token drawn in its place, and the log-probabilities of both.
-struct RowResult {
-  int64_t token;
-  float token_logp, draft_logp;
-  int32_t stands;
-  int32_t unused;
+// A part of a row's sums: shift and sum of the target's and of the draft's, or, greedy,
+// of the target's, its largest score and that one's place.
+struct RowSums {
+  float v[4];
 };
+constexpr int kVerifyPartBits = 5;  // at most 32 parts of a row
 
 struct VerifyRows {
   const char* data;
@@ -38,20 +36,25 @@ struct VerifyParams {
   int64_t* accepted;
   int64_t* tokens;
   float* logp;
-  RowResult* results;  // workspace, [n_drafts + n_seq]
-  int32_t* fallen;     // workspace, [n_seq]: a draft that fell, by its place; null: not kept
-  int ranks;           // CTAs a row
-  int64_t pitch;       // rows are visited this far apart
-  unsigned int* status_word;  // where waits that ran out are recorded
-  unsigned int* const* status_host;
+  RowSums* sums;    // workspace, [n_drafts + n_seq][parts]
+  int32_t* done;    // workspace, [n_drafts + n_seq]: parts of a row that are
+  int32_t* fallen;  // workspace, [n_seq]: a draft that fell, by its place; null: not kept
+  int parts, part_bits;  // of a row in sums_kernel: a power of two
+  int pitch;             // rows that are visited one after the other
+  int rank_bits;         // CTAs a sequence in draw_kernel: a power of two
 };
 
-// Byte offset of `fallen` in the workspace, and its size.
-inline int64_t verify_fallen(int64_t n_drafts, int64_t n_seq) {
-  return (int64_t(sizeof(RowResult)) * (n_drafts + n_seq) + 255) / 256 * 256;
-}
-inline int64_t verify_bytes(int64_t n_drafts, int64_t n_seq) {
-  return verify_fallen(n_drafts, n_seq) + (4 * n_seq + 255) / 256 * 256;
+// Byte offsets of the workspace's parts, and its size.
+struct VerifyLayout {
+  int64_t done, fallen, bytes;
+};
+inline VerifyLayout verify_layout(int64_t n_drafts, int64_t n_seq) {
+  const auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
+  VerifyLayout l;
+  l.done = (int64_t(sizeof(RowSums)) << kVerifyPartBits) * (n_drafts + n_seq);
+  l.fallen = l.done + up(4 * (n_drafts + n_seq));
+  l.bytes = l.fallen + up(4 * n_seq);
+  return l;
 }
 
 cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream);

@@ -34,9 +34,7 @@ ar_status score_rows(const ar_score_rows& r, int64_t rows, int64_t vocab, Verify
   out.data = static_cast<const char*>(r.data);
   out.ld = r.ld;
   out.bf16 = r.dtype == AR_BF16;
-  out.inv_temp = 1.0 / double(r.temperature);
   out.k = float(k);
-  out.k_low = float(k - double(float(k)));
   memory = range(r.data, rows > 0 ? ((rows - 1) * r.ld + vocab) * es : 0);
   return AR_OK;
 }

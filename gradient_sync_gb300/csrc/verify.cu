@@ -19,11 +19,10 @@
 // Results do not depend on which rows were skipped: none before the first fall is.
 //
 // A draw has to put u on the right side of borders that may lie anywhere, also
-// between tokens of 1e-6 and less. So its weights are to fp32's last place (the
-// fast ones of the sums that only decide about drafts are not): the exponent is
-// carried with what fp32 leaves of it, the draft's weight is subtracted in one
-// fused operation with a two-part factor, sums beyond 32 terms are pairs of fp32
-// numbers (fp64 adds are slow here), borders 64 bits.
+// between tokens of 1e-6 and less. Its terms are fp32 exponentials, as in the
+// sums: each is off by some 2^-22 of itself, and by half a last place of its
+// exponent x k - c. Sums beyond 64 terms, and borders, are pairs of fp32 numbers (one fp64 operation
+// takes a warp some 200 cycles here); the draft's weight is subtracted in one fused operation.
 #include "verify.h"
 
 #include <algorithm>
@@ -70,11 +69,6 @@ __device__ __forceinline__ Pair add2(Pair a, Pair b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-  Pair r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
 __device__ __forceinline__ Pair exp2_pair(Pair a) {
   const float2 y = floats_of(a);
   return pair_of(exp2_approx(y.x), exp2_approx(y.y));
@@ -94,7 +88,15 @@ __device__ __forceinline__ Two add(Two a, Two b) {
   const float hi = s.hi + lo;
   return {hi, lo - (hi - s.hi)};
 }
-__device__ __forceinline__ double wide(Two a) { return double(a.hi) + double(a.lo); }
+__device__ __forceinline__ bool above(Two a, Two b) {
+  const Two d = add(a, {-b.hi, -b.lo});
+  return d.hi > 0.0f || (d.hi == 0.0f && d.lo > 0.0f);
+}
+__device__ __forceinline__ Two times(Two a, float u) {
+  const float p = a.hi * u;
+  return two_sum(p, fmaf(a.hi, u, -p) + a.lo * u);
+}
+__device__ __forceinline__ Two shuffled(Two v, int from) { return {__shfl_sync(~0u, v.hi, from), __shfl_sync(~0u, v.lo, from)}; }
 __device__ __forceinline__ Two warp_sum(Two v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = add(v, {__shfl_xor_sync(~0u, v.hi, o), __shfl_xor_sync(~0u, v.lo, o)});
@@ -485,79 +487,46 @@ __global__ void __launch_bounds__(kRowThreads, 4) sums_kernel(const __grid_const
 
 // ---------------------------------------------------------------- draws
 
-// What every warp of a cluster tells the others in one phase.
-enum Phase : int { kExact = 0, kTotals = 1, kTotalsAgain = 2, kPhases = 3 };
-
-struct Shared {
-  Post posts[kPhases][kRowWarps];
-  Verdict verdicts[kRowWarps];
-  float rho, rho_low;
-  int owner;  // of a draw's border: rank * kRowWarps + warp, -1: no weight
-  double before, target;
-  Two parts[kRowWarps];
-};
-
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ Post peer_post(const Post* p, int rank) {
-  Post v;
+__device__ __forceinline__ Two peer_post(const Two* p, int rank) {
+  Two v;
   asm volatile(
       "{\n"
       ".reg .b32 remote;\n"
-      "mapa.shared::cluster.u32 remote, %4, %5;\n"
-      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [remote];\n"
+      "mapa.shared::cluster.u32 remote, %2, %3;\n"
+      "ld.shared::cluster.v2.f32 {%0, %1}, [remote];\n"
       "}\n"
-      : "=f"(v.a), "=f"(v.b), "=f"(v.c), "=f"(v.d)
+      : "=f"(v.hi), "=f"(v.lo)
       : "r"(uint32_t(__cvta_generic_to_shared(p))), "r"(rank)
       : "memory");
   return v;
 }
-// A phase's posts are written once, then read by every CTA's first warp, two a lane.
-__device__ __forceinline__ void posted(int ranks) {
-  if (ranks > 1) cluster_barrier();
-  else __syncthreads();
-}
-__device__ __forceinline__ Post post_at(const Shared& sh, int phase, int i, int ranks) {
-  const Post* p = &sh.posts[phase][i % kRowWarps];
-  return ranks > 1 ? peer_post(p, i / kRowWarps) : *p;
-}
 
-// 2^(x k - c) to fp32's last place, two at a time; 0 where it is below 2^-126.
+// 2^(x k - c), two at a time.
 struct Weights {
-  Pair k, minus_k, minus_k_low, c, minus_c;
-  float least;  // (for scores below it the difference to c would have no value)
-  __device__ __forceinline__ Weights(const VerifyRows& r, int shift) {
-    const float f = float(shift);
-    k = pair_of(r.k, r.k), minus_k = pair_of(-r.k, -r.k), minus_k_low = pair_of(-r.k_low, -r.k_low);
-    c = pair_of(f, f), minus_c = pair_of(-f, -f);
-    least = (f - 199.0f) / r.k;
-  }
-  __device__ __forceinline__ Pair of(float x0, float x1) const {
-    const Pair x = pair_of(fmaxf(x0, least), fmaxf(x1, least)), p = mul2(x, k), t = add2(p, minus_c);
-    // what t lacks, with the other sign: of the product, of k, of the difference
-    Pair left = fma2(x, minus_k_low, fma2(x, minus_k, p));
-    left = add2(left, fma2(p, pair_of(-1.0f, -1.0f), add2(t, c)));
-    const Pair e = exp2_pair(t);
-    return fma2(e, mul2(left, pair_of(-0.69314718f, -0.69314718f)), e);
-  }
+  Pair k, minus_c;
+  __device__ __forceinline__ Weights(const VerifyRows& r, int shift)
+      : k(pair_of(r.k, r.k)), minus_c(pair_of(-float(shift), -float(shift))) {}
+  __device__ __forceinline__ Pair of(float x0, float x1) const { return exp2_pair(fma2(pair_of(x0, x1), k, minus_c)); }
 };
+
+__device__ __forceinline__ Pair sum4(const Pair (&w)[4]) { return add2(add2(w[0], w[1]), add2(w[2], w[3])); }
 
 // What a token is drawn from: w_i, less the draft's weight (a row's, or one token's).
 enum Less : int { kNothing = 0, kRow = 1, kToken = 2 };
 template <class X, class Y>
 struct Draw {
-  static constexpr int kVecsX = X::kVecs, kVecsY = Y::kVecs;
   X x;
   Y y;
   Weights wx, wy;
   float rho, rho_low;  // Z / Z'
   int token;
   int less;
-  // A group's weights w; exact: of the target (w) and of the draft (v) instead.
-  __device__ __forceinline__ void weights(const uint4 (&rx)[X::kVecs], const uint4 (&ry)[Y::kVecs], int i, bool exact,
-                                          Pair (&w)[4], Pair (&v)[4]) const {
+  // A group's weights.
+  __device__ __forceinline__ void weights(const uint4 (&rx)[X::kVecs], const uint4 (&ry)[Y::kVecs], int i, Pair (&w)[4]) const {
     float a[8];
     x.scores(rx, a);
 #pragma unroll
@@ -567,11 +536,9 @@ struct Draw {
       const Pair r = pair_of(-rho, -rho), r_low = pair_of(-rho_low, -rho_low);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        v[j] = wy.of(a[2 * j], a[2 * j + 1]);
-        if (!exact) {
-          const float2 d = floats_of(fma2(v[j], r_low, fma2(v[j], r, w[j])));
-          w[j] = pair_of(fmaxf(d.x, 0.0f), fmaxf(d.y, 0.0f));
-        }
+        const Pair v = wy.of(a[2 * j], a[2 * j + 1]);
+        const float2 d = floats_of(fma2(v, r_low, fma2(v, r, w[j])));
+        w[j] = pair_of(fmaxf(d.x, 0.0f), fmaxf(d.y, 0.0f));
       }
     } else if (less == kToken) {
 #pragma unroll
@@ -585,73 +552,64 @@ struct Draw {
     x.fetch(i, rx);
     if (less == kRow) y.fetch(i, ry);
   }
-};
-__device__ __forceinline__ Pair sum4(const Pair (&w)[4]) { return add2(add2(w[0], w[1]), add2(w[2], w[3])); }
-
-// Of up to 64 parts one behind the other (each lane's two), the one that the border lies in, and the sum before it
-// (one warp). Behind the last border by rounding: the last part with weight; -1: none has any.
-__device__ __noinline__ int part_of(double v0, double v1, double before_all, double target, int lane, double* before) {
-  double run = v0 + v1;
+  // The weight of a lane's groups.
+  __device__ __forceinline__ Two total(const Piece& p, int lane) const {
+    Two sum = {0.0f, 0.0f};
 #pragma unroll 1
-  for (int o = 1; o < 32; o <<= 1) {
-    const double v = __shfl_up_sync(~0u, run, o);
-    if (lane >= o) run += v;
-  }
-  run += before_all;
-  const double mine = run - (v0 + v1);
-  const bool first = v0 > 0.0 && mine + v0 > target, second = v1 > 0.0 && run > target;
-  const unsigned over = __ballot_sync(~0u, first || second), some = __ballot_sync(~0u, v0 > 0.0 || v1 > 0.0);
-  if (some == 0) return -1;
-  const int owner = over != 0 ? __ffs(int(over)) - 1 : 31 - __clz(int(some));
-  const bool low = over != 0 ? first : !(v1 > 0.0);
-  *before = __shfl_sync(~0u, low ? mine : mine + v0, owner);
-  return 2 * owner + (__shfl_sync(~0u, int(low), owner) != 0 ? 0 : 1);
-}
-
-// The border's token, by the warp whose piece it lies in.
-template <class D>
-__device__ __forceinline__ int token_at(const D& d, const Piece& p, int lane, double before, double target) {
-  int found = -1;
-#pragma unroll 1
-  for (int g0 = p.lo; g0 < p.hi; g0 += 32) {
-    const int i = 8 * (g0 + lane) + p.first;
-    Pair w[4], v[4];
+    for (int g = p.lo + lane; g < p.hi; g += kRounds * 32) {
+      uint4 rx[kRounds][X::kVecs], ry[kRounds][Y::kVecs];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = pair_of(0.0f, 0.0f);
-    if (g0 + lane < p.hi) {
-      uint4 rx[D::kVecsX], ry[D::kVecsY];
-      d.fetch(i, rx, ry);
-      d.weights(rx, ry, i, false, w, v);
-    }
-    const float2 total = floats_of(sum4(w));
-    const double chunk = double(total.x + total.y);
-    double upto = 0.0;
-    const int at = part_of(chunk, 0.0, before, target, lane, &upto);
-    if (at < 0) continue;
-    // the lane that holds the border, else the last one with weight
-    int hit = -1, last = -1;
-    bool over = false;
-    if (lane == at / 2) {
-      double run = upto;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = floats_of(w[j]);
-        run += double(f.x);
-        if (f.x > 0.0f) last = i + 2 * j, hit = hit < 0 && run > target ? last : hit;
-        run += double(f.y);
-        if (f.y > 0.0f) last = i + 2 * j + 1, hit = hit < 0 && run > target ? last : hit;
+      for (int r = 0; r < kRounds; ++r) {
+        X::nothing(rx[r]);
+        Y::nothing(ry[r]);
+        if (g + 32 * r < p.hi) fetch(8 * (g + 32 * r) + p.first, rx[r], ry[r]);
       }
-      over = upto + chunk > target;
+      Pair a = pair_of(0.0f, 0.0f);
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        Pair w[4];
+        weights(rx[r], ry[r], 8 * (g + 32 * r) + p.first, w);
+        a = add2(a, sum4(w));
+      }
+      const float2 f = floats_of(a);
+      sum = add(sum, {f.x + f.y, 0.0f});
     }
-    found = __shfl_sync(~0u, hit >= 0 ? hit : last, at / 2);
-    if (__shfl_sync(~0u, int(over), at / 2) != 0) break;
-    double all = chunk;
-#pragma unroll 1
-    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(~0u, all, o);
-    before += all;
+    return sum;
   }
-  return found;
+};
+
+// Of parts one behind the other, two a lane, behind a sum of `before`: the part that the border lies in, and the sum
+// before it. Behind the last border by rounding: the last part with weight; -1: none has any.
+struct Border {
+  int part;
+  Two before;
+};
+__device__ __forceinline__ Border border_of(Two v0, Two v1, Two before, Two target, int lane) {
+  Two run = add(v0, v1);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Two v = {__shfl_up_sync(~0u, run.hi, o), __shfl_up_sync(~0u, run.lo, o)};
+    if (lane >= o) run = add(run, v);
+  }
+  // (a lane's sum before its parts is the one of the lanes before, rounded alike for both)
+  Two mine = {__shfl_up_sync(~0u, run.hi, 1), __shfl_up_sync(~0u, run.lo, 1)};
+  mine = lane > 0 ? add(before, mine) : before;
+  const Two middle = add(mine, v0);
+  const bool first = v0.hi > 0.0f && above(middle, target), second = v1.hi > 0.0f && above(add(before, run), target);
+  const unsigned over = __ballot_sync(~0u, first || second), some = __ballot_sync(~0u, v0.hi > 0.0f || v1.hi > 0.0f);
+  if (some == 0) return {-1, before};
+  const int owner = over != 0 ? __ffs(int(over)) - 1 : 31 - __clz(int(some));
+  const bool low = over != 0 ? first : !(v1.hi > 0.0f);
+  return {2 * owner + (__shfl_sync(~0u, int(low), owner) != 0 ? 0 : 1), shuffled(low ? mine : middle, owner)};
 }
+
+struct Shared {
+  Two posts[2][kRowWarps];
+  Verdict verdicts[kRowWarps];
+  Border border;  // of a draw: its part is rank * kRowWarps + warp
+  Two target;
+  Two parts[kRowWarps];
+};
 
 template <bool XB, bool YB, int MODE>
 __global__ void __launch_bounds__(kRowThreads, kDrawCtas) draw_kernel(const __grid_constant__ VerifyParams p) {
@@ -712,7 +670,7 @@ __global__ void __launch_bounds__(kRowThreads, kDrawCtas) draw_kernel(const __gr
   const int g0 = min(groups, rank * per), g1 = min(groups, g0 + per);
   const int per_warp = (g1 - g0 + 32 * kRowWarps - 1) / (32 * kRowWarps) * 32;
   const auto piece_of = [&](int w) { return Piece{min(g1, g0 + w * per_warp), min(g1, g0 + (w + 1) * per_warp), -x.lead}; };
-  Piece piece = piece_of(warp);
+  const Piece piece = piece_of(warp);
   const int64_t token = behind || drafted ? -1 : p.drafts[first + a];
   const float last = p.uniforms[row0 + count];
   const float u = fminf(fmaxf(last == last ? last : 0.0f, 0.0f), 0.99999994f);
@@ -720,91 +678,100 @@ __global__ void __launch_bounds__(kRowThreads, kDrawCtas) draw_kernel(const __gr
                   token >= 0 && token < p.vocab ? int(token) : -1, behind ? kNothing : drafted ? kRow : kToken};
   d.x.bias = at.bias_x;
   d.y.bias = at.bias_y;
-  // exact sums of both rows; the totals of what is drawn from (of p itself where there is no residue); those of the
-  // owner's piece, once more over all its warps; then the round of the warp that has the border
-  enum Stage : int { kBoth, kWhole, kWholeAgain, kOwner };
+  const float v_bias = at.bias_x;
+  const Sum v_zx = at.zx;
+  if (drafted) {  // the quotient of the sums: rounded, and what that leaves
+    d.rho = at.zx.s / at.zy.s;
+    d.rho_low = fmaf(-d.rho, at.zy.s, at.zx.s) / at.zy.s;
+  }
+
+  // the total of what is drawn from (once more of p itself, where there is no residue), and the piece that the border
+  // lies in
+  Border border;
+  Two target;
 #pragma unroll 1
-  for (int stage = drafted ? kBoth : kWhole;;) {
-    Two sx = {0.0f, 0.0f}, sy = {0.0f, 0.0f};
-#pragma unroll 1
-    for (int g = piece.lo + lane; g < piece.hi; g += kRounds * 32) {
-      uint4 rx[kRounds][X::kVecs], ry[kRounds][Y::kVecs];
-#pragma unroll
-      for (int r = 0; r < kRounds; ++r) {
-        X::nothing(rx[r]);
-        Y::nothing(ry[r]);
-        if (g + 32 * r < piece.hi) d.fetch(8 * (g + 32 * r) + piece.first, rx[r], ry[r]);
-      }
-      Pair a = pair_of(0.0f, 0.0f), b = a;
-#pragma unroll
-      for (int r = 0; r < kRounds; ++r) {
-        Pair w[4], v[4];
-        d.weights(rx[r], ry[r], 8 * (g + 32 * r) + piece.first, stage == kBoth, w, v);
-        a = add2(a, sum4(w));
-        if (stage == kBoth) b = add2(b, sum4(v));
-      }
-      const float2 f = floats_of(a), h = floats_of(b);
-      sx = add(sx, {f.x + f.y, 0.0f});
-      if (stage == kBoth) sy = add(sy, {h.x + h.y, 0.0f});
-    }
-    sx = warp_sum(sx);
-    if (stage == kOwner) {
-      if (lane == 0) sh.parts[warp] = sx;
-      break;
-    }
-    if (stage == kBoth) sy = warp_sum(sy);
-    if (lane == 0) sh.posts[stage][warp] = {sx.hi, sx.lo, sy.hi, sy.lo};
-    posted(ranks);
+  for (int again = 0;; ++again) {
+    const Two sum = warp_sum(d.total(piece, lane));
+    if (lane == 0) sh.posts[again][warp] = sum;
+    // posts are written once, then read by every CTA's first warp, two a lane
+    if (ranks > 1) cluster_barrier();
+    else __syncthreads();
     if (warp == 0) {
-      Post v[2];
+      Two v[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        v[h] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (2 * lane + h < ranks * kRowWarps) v[h] = post_at(sh, stage, 2 * lane + h, ranks);
+        const int i = 2 * lane + h;
+        v[h] = {0.0f, 0.0f};
+        if (i < ranks * kRowWarps)
+          v[h] = ranks > 1 ? peer_post(&sh.posts[again][i % kRowWarps], i / kRowWarps) : sh.posts[again][i];
       }
-      const Two c = warp_sum(add({v[0].a, v[0].b}, {v[1].a, v[1].b}));
-      if (stage == kBoth) {
-        const Two e = warp_sum(add({v[0].c, v[0].d}, {v[1].c, v[1].d}));
-        // the quotient of both pairs: a rounded one, and what it leaves
-        const float rho = c.hi / e.hi;
-        if (lane == 0) sh.rho = rho, sh.rho_low = ((fmaf(-rho, e.hi, c.hi) + c.lo) - rho * e.lo) / e.hi;
-      } else {
-        const double target = double(u) * wide(c);
-        double before = 0.0;
-        const int owner = part_of(wide({v[0].a, v[0].b}), wide({v[1].a, v[1].b}), 0.0, target, lane, &before);
-        if (lane == 0) sh.owner = owner, sh.before = before, sh.target = target;
-      }
+      target = times(warp_sum(add(v[0], v[1])), u);
+      border = border_of(v[0], v[1], {0.0f, 0.0f}, target, lane);
+      if (lane == 0) sh.border = border, sh.target = target;
     }
     __syncthreads();
-    if (stage == kBoth) {
-      d.rho = sh.rho;
-      d.rho_low = sh.rho_low;
-      stage = kWhole;
-    } else if (sh.owner < 0 && stage == kWhole) {
-      d.less = kNothing;
-      stage = kWholeAgain;
-    } else {
-      if (sh.owner < 0 || sh.owner / kRowWarps != rank) break;
-      const Piece q = piece_of(sh.owner % kRowWarps);
+    border = sh.border;
+    target = sh.target;
+    if (border.part >= 0 || again > 0) break;
+    d.less = kNothing;
+  }
+  if (ranks > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");  // (this CTA reads no other's posts any more)
+
+  if (border.part >= 0 && border.part / kRowWarps == rank) {
+    // the piece, split over all warps again and again, until a lane has one group
+    Piece q = piece_of(border.part % kRowWarps);
+#pragma unroll 1
+    for (;;) {
       const int per_part = ((q.hi - q.lo + kRowWarps - 1) / kRowWarps + 31) / 32 * 32;
-      piece = {min(q.hi, q.lo + warp * per_part), min(q.hi, q.lo + (warp + 1) * per_part), q.first};
-      stage = kOwner;
-    }
-  }
-  if (sh.owner >= 0 && sh.owner / kRowWarps == rank) {
-    __syncthreads();
-    const double v = lane < kRowWarps ? wide(sh.parts[lane]) : 0.0;
-    double before = 0.0;
-    const int owner = part_of(v, 0.0, sh.before, sh.target, lane, &before) / 2;
-    if (owner == warp) {
-      const int found = token_at(d, piece, lane, before, sh.target);
-      if (lane == 0) {
-        p.tokens[row] = found;
-        p.logp[row] = found >= 0 ? to_e(log2_p(x.one(found) - at.bias_x, p.target.k, log2_of(at.zx))) : 0.0f;
+      const Piece part = {min(q.hi, q.lo + warp * per_part), min(q.hi, q.lo + (warp + 1) * per_part), q.first};
+      Pair w[4];
+      Two mine;
+      if (per_part == 32) {
+        uint4 rx[X::kVecs], ry[Y::kVecs];
+        X::nothing(rx);
+        Y::nothing(ry);
+        if (part.lo + lane < part.hi) d.fetch(8 * (part.lo + lane) + q.first, rx, ry);
+        d.weights(rx, ry, 8 * (part.lo + lane) + q.first, w);
+        const float2 f = floats_of(sum4(w));
+        mine = {f.x + f.y, 0.0f};
+      } else {
+        mine = d.total(part, lane);
       }
+      const Two sum = warp_sum(mine);
+      if (lane == 0) sh.parts[warp] = sum;
+      __syncthreads();
+      const Border at = border_of(lane < kRowWarps ? sh.parts[lane % kRowWarps] : Two{0.0f, 0.0f}, {0.0f, 0.0f}, border.before, target, lane);
+      if (per_part > 32) {
+        border.before = at.before;
+        q = {min(q.hi, q.lo + at.part / 2 * per_part), min(q.hi, q.lo + (at.part / 2 + 1) * per_part), q.first};
+        __syncthreads();
+        continue;
+      }
+      if (at.part / 2 == warp) {
+        const Border in = border_of(mine, {0.0f, 0.0f}, at.before, target, lane);
+        if (lane == in.part / 2) {  // (never -1: the warp's sum is not 0)
+          const int i = 8 * (part.lo + lane) + q.first;
+          Two run = in.before;
+          int hit = -1, last = -1;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 f = floats_of(w[j / 2]);
+            const float v = j % 2 ? f.y : f.x;
+            run = add(run, {v, 0.0f});
+            if (v > 0.0f) {
+              last = i + j;
+              if (hit < 0 && above(run, target)) hit = last;
+            }
+          }
+          const int found = hit >= 0 ? hit : last;
+          p.tokens[row] = found;
+          p.logp[row] = found >= 0 ? to_e(log2_p(x.one(found) - v_bias, p.target.k, log2_of(v_zx))) : 0.0f;
+        }
+      }
+      break;
     }
   }
-  if (ranks > 1) cluster_barrier();  // no CTA goes while another may still read from it
+  if (ranks > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");  // no CTA goes while another may still read from it
 }
 
 // No row is done, and no draft of any sequence has fallen yet.
@@ -853,7 +820,7 @@ Kernel draw_of(const VerifyParams& p) {
   return y ? draw_kernel<false, true, kDrafted> : draw_kernel<false, false, kDrafted>;
 }
 
-constexpr int64_t kPart = 32768, kLeastPart = 4096;  // elements of a row that a CTA of sums_kernel takes
+constexpr int64_t kPart = 32768, kLeastPart = 4096;  // elements that a CTA of sums_kernel takes (of one row or two)
 constexpr int64_t kLeastDraw = 2048;                 // ... of draw_kernel: a round of all its warps
 
 }  // namespace
@@ -863,7 +830,8 @@ cudaError_t launch_verify(const VerifyParams& q, cudaStream_t stream) {
   const int64_t rows = p.n_drafts + p.n_seq, sms = device_sms();
   // parts of a row: of a good size, or smaller where that keeps SMs without work
   p.part_bits = 0;
-  while (p.part_bits < kVerifyPartBits && (p.vocab >> p.part_bits) > kPart) ++p.part_bits;
+  const int64_t part = p.draft.data != nullptr ? kPart / 2 : kPart;
+  while (p.part_bits < kVerifyPartBits && (p.vocab >> p.part_bits) > part) ++p.part_bits;
   while (p.part_bits < kVerifyPartBits && (rows << p.part_bits) < 2 * sms && (p.vocab >> p.part_bits) >= 2 * kLeastPart) ++p.part_bits;
   while (p.part_bits > 0 && (rows << p.part_bits) > 0x7fffffff) --p.part_bits;
   p.parts = 1 << p.part_bits;

@@ -21,8 +21,7 @@ struct VerifyRows {
   const char* data;
   int64_t ld;
   int bf16;
-  double inv_temp;
-  float k, k_low;  // log2(e) / temperature, and what fp32 leaves of it
+  float k;  // log2(e) / temperature
 };
 
 struct VerifyParams {

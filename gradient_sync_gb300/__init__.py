@@ -646,6 +646,7 @@ class TensorList:
             raise ValueError("a list of at least one tensor wanted")
         self.c = (_lib.ArTensor * n)()
         self.counts, self.layouts, self.device = [], [], None
+        self._alike = set()  # lists known to be laid out like this one, by their numbers
         for i, t in enumerate(self.tensors):
             if t is None:
                 self.c[i].data, self.c[i].count, self.c[i].dtype = None, 0, AR_F32
@@ -663,6 +664,10 @@ class TensorList:
             self.counts.append(t.numel())
             # what an element's place depends on, where it is not simply its index
             self.layouts.append(None if t.is_contiguous() else (tuple(t.shape), t.stride()))
+        TensorList._made += 1
+        self._number = TensorList._made
+
+    _made = 0
 
     def __len__(self):
         return len(self.tensors)
@@ -672,6 +677,7 @@ def _tensors(x, what: str, like: TensorList | None = None):
     """A TensorList of `x` (None stays None), laid out like another one."""
     if x is None:
         return None
+    given = x
     if not isinstance(x, TensorList):
         try:
             x = TensorList(x)
@@ -680,6 +686,8 @@ def _tensors(x, what: str, like: TensorList | None = None):
     if like is None:
         if any(v is None for v in x.counts):
             raise ValueError(f"{what}: None in place of a tensor")
+        return x
+    if x._number in like._alike:
         return x
     if x.device is not None and x.device != like.device:
         raise ValueError(f"{what}: tensors on {like.device} wanted, got {x.device}")
@@ -690,6 +698,8 @@ def _tensors(x, what: str, like: TensorList | None = None):
             for a, b, c, d in zip(x.counts, like.counts, x.layouts, like.layouts))
         if not same:
             raise ValueError(f"{what}: as many tensors wanted, with the same numbers of elements in the same order")
+    elif given is x:
+        like._alike.add(x._number)
     return x
 
 

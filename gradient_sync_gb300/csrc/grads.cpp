@@ -36,20 +36,47 @@ Range range(const void* p, int64_t bytes, bool write) {
 }
 Range range(const ar_tensor& t, bool write) { return range(t.data, t.count * esize(t.dtype), write); }
 
-// No written range overlaps another one. (Lists are mostly in the order of
-// their addresses already; those that are not are sorted.)
-bool apart(std::vector<Range>& v) {
-  v.erase(std::remove_if(v.begin(), v.end(), [](const Range& r) { return r.lo >= r.hi; }), v.end());
-  const auto by_lo = [](const Range& a, const Range& b) { return a.lo < b.lo; };
-  if (!std::is_sorted(v.begin(), v.end(), by_lo)) std::sort(v.begin(), v.end(), by_lo);
-  uintptr_t written = 0, any = 0;  // the ends so far
-  for (const Range& r : v) {
-    if (r.lo < written || (r.write && r.lo < any)) return false;
-    any = std::max(any, r.hi);
-    if (r.write) written = std::max(written, r.hi);
+// The ranges of a call, list by list. Lists are mostly in the order of their
+// addresses, so that merging them is quicker than sorting all ranges.
+struct Ranges {
+  std::vector<Range> v;
+  std::vector<size_t> ends;  // of ascending runs
+  explicit Ranges(size_t most) { v.reserve(most); }
+  void add(const Range& r) {
+    if (r.lo >= r.hi) return;
+    if (!v.empty() && r.lo < v.back().lo) ends.push_back(v.size());
+    v.push_back(r);
   }
-  return true;
-}
+  // Whether no written range overlaps another one.
+  bool apart() {
+    const auto by_lo = [](const Range& a, const Range& b) { return a.lo < b.lo; };
+    ends.push_back(v.size());
+    if (ends.size() > 64) {
+      std::sort(v.begin(), v.end(), by_lo);
+    } else {
+      while (ends.size() > 1) {
+        size_t from = 0, kept = 0;
+        for (size_t i = 0; i < ends.size(); i += 2) {
+          if (i + 1 < ends.size()) {
+            std::inplace_merge(v.begin() + from, v.begin() + ends[i], v.begin() + ends[i + 1], by_lo);
+            from = ends[i + 1];
+          } else {
+            from = ends[i];
+          }
+          ends[kept++] = from;
+        }
+        ends.resize(kept);
+      }
+    }
+    uintptr_t written = 0, any = 0;  // the ends so far
+    for (const Range& r : v) {
+      if (r.lo < written || (r.write && r.lo < any)) return false;
+      any = std::max(any, r.hi);
+      if (r.write) written = std::max(written, r.hi);
+    }
+    return true;
+  }
+};
 
 ar_status device_ready() {
   int dev = -1;
@@ -74,30 +101,33 @@ ar_status grad_norm(const ar_tensor* grads, int n, const ar_tensor* outs, bool c
   if (!aligned(stats, 4) || !aligned(workspace, 16) || (norms != nullptr && !aligned(norms, 4))) return AR_EINVAL;
   if (!valid(grads, n) || (outs != nullptr && !valid(outs, n))) return AR_EINVAL;
   std::vector<GradTensor> t(n);
-  std::vector<Range> ranges;
-  ranges.reserve(size_t(2 * n + 3));
+  Ranges ranges(size_t(2 * n + 3));
   for (int i = 0; i < n; ++i) {
     const ar_tensor& in = grads[i];
     const ar_tensor& out = outs != nullptr ? outs[i] : in;
     if (out.count != in.count || out.dtype != in.dtype) return AR_EINVAL;
     t[i] = {static_cast<const char*>(in.data), static_cast<char*>(out.data), in.count, in.dtype == AR_BF16};
-    if (!clip || out.data != in.data) ranges.push_back(range(in, false));
-    if (clip) ranges.push_back(range(out, true));
+    if (!clip || out.data != in.data) ranges.add(range(in, false));
   }
-  ranges.push_back(range(stats, 16, true));
-  ranges.push_back(range(norms, norms != nullptr ? 4 * int64_t(n) : 0, true));
-  ranges.push_back(range(workspace, kGradWorkspace, true));
-  if (!apart(ranges)) return AR_EINVAL;
+  for (int i = 0; clip && i < n; ++i) ranges.add(range(outs != nullptr ? outs[i] : grads[i], true));
+  ranges.add(range(stats, 16, true));
+  ranges.add(range(norms, norms != nullptr ? 4 * int64_t(n) : 0, true));
+  ranges.add(range(workspace, kGradWorkspace, true));
+  if (!ranges.apart()) return AR_EINVAL;
   if ((s = device_ready()) != AR_OK) return s;
   GradJob job = {};
   job.kind = desc->kind;
-  job.max_norm = desc->max_norm;
-  job.eps = desc->eps;
+  const auto halves = [](double v, float& hi, float& low) {
+    hi = float(v);
+    low = std::isfinite(hi) ? float(v - double(hi)) : 0.0f;
+  };
+  halves(desc->max_norm, job.max_norm, job.max_norm_low);
+  halves(desc->eps, job.eps, job.eps_low);
   job.grad_scale = desc->grad_scale;
   job.stats = stats;
   job.norms = norms;
-  job.groups = static_cast<double*>(workspace);
-  job.partials = reinterpret_cast<double*>(static_cast<char*>(workspace) + kGradPartials);
+  job.groups = workspace;
+  job.partials = static_cast<char*>(workspace) + kGradPartials;
   return from_cuda(launch_grad_norm(t.data(), n, clip, job, static_cast<cudaStream_t>(stream)));
 }
 
@@ -165,16 +195,7 @@ ar_status ar_adamw_step(const ar_adamw_desc* desc, int n_tensors, const ar_tenso
   for (const ar_tensor* list : {params, grads, exp_avgs, exp_avg_sqs, params_out, exp_avgs_out, exp_avg_sqs_out})
     if (!valid(list, n)) return AR_EINVAL;
   std::vector<AdamEntry> e(n);
-  std::vector<Range> ranges;
-  ranges.reserve(size_t(9 * n + 2));
   bool in_place = true;
-  const auto pair = [&](const ar_tensor& in, const ar_tensor& out) {
-    if (in.data != out.data) {
-      ranges.push_back(range(in, false));
-      in_place = false;
-    }
-    ranges.push_back(range(out, true));
-  };
   for (int i = 0; i < n; ++i) {
     const ar_tensor &p = params[i], &g = grads[i], &m = exp_avgs[i], &v = exp_avg_sqs[i], &po = params_out[i],
                     &mo = exp_avgs_out[i], &vo = exp_avg_sqs_out[i];
@@ -201,15 +222,25 @@ ar_status ar_adamw_step(const ar_adamw_desc* desc, int n_tensors, const ar_tenso
     ph.add(wo.data, w.dtype == AR_BF16);
     if (has_master) ph.add(po.data, p.dtype == AR_BF16);
     e[i].phase = ph.value();
-    ranges.push_back(range(g, false));
-    pair(m, mo);
-    pair(v, vo);
-    pair(w, wo);
-    if (has_master) ranges.push_back(range(po, true));
+    if (m.data != mo.data || v.data != vo.data || w.data != wo.data) in_place = false;
   }
-  if (clip != nullptr) ranges.push_back(range(clip, 16, false));
-  if (desc->device_step != nullptr) ranges.push_back(range(desc->device_step, 8, false));
-  if (!apart(ranges)) return AR_EINVAL;
+  Ranges ranges(size_t(9 * n + 2));
+  for (int i = 0; i < n; ++i) ranges.add(range(grads[i], false));
+  const auto list = [&](auto in, auto out, int64_t size) {  // of the entries' arrays
+    for (int i = 0; i < n; ++i)
+      if (in(i) != out(i)) ranges.add(range(in(i), e[i].count * size, false));
+    for (int i = 0; i < n; ++i) ranges.add(range(out(i), e[i].count * size, true));
+  };
+  list([&](int i) { return e[i].m; }, [&](int i) { return e[i].m_out; }, 4);
+  list([&](int i) { return e[i].v; }, [&](int i) { return e[i].v_out; }, 4);
+  for (int i = 0; i < n; ++i)
+    if (e[i].w != e[i].w_out) ranges.add(range(e[i].w, e[i].count * (e[i].w_bf16 ? 2 : 4), false));
+  for (int i = 0; i < n; ++i) ranges.add(range(e[i].w_out, e[i].count * (e[i].w_bf16 ? 2 : 4), true));
+  for (int i = 0; i < n; ++i)
+    if (e[i].p_out != nullptr) ranges.add(range(e[i].p_out, e[i].count * (e[i].p_bf16 ? 2 : 4), true));
+  if (clip != nullptr) ranges.add(range(clip, 16, false));
+  if (desc->device_step != nullptr) ranges.add(range(desc->device_step, 8, false));
+  if (!ranges.apart()) return AR_EINVAL;
   if ((s = device_ready()) != AR_OK) return s;
   AdamJob job = {};
   job.rates = {float(desc->beta1), float(desc->beta2), float(1.0 - desc->beta1), float(1.0 - desc->beta2), 0.0f, 0.0f,

@@ -14,6 +14,11 @@
 // work, and a tensor's sum is that of the stretches it lies in. A stretch and a
 // tensor meet at most once, so that the sum of warp w over tensor i has a place
 // of its own, w + i, and nothing is added in an order that timing could change.
+//
+// Sums of squares are pairs of fp32 numbers, about 46 bits (one fp64 operation takes
+// a warp some 200 cycles here: joins in fp64 cost more than the reading), in
+// three bands of magnitude, each at its own power of two, so that finite elements of
+// any size have their norm.
 #include "grads.h"
 
 #include <algorithm>
@@ -34,29 +39,92 @@ __device__ __forceinline__ uint4 load16(const char* p) {
   return r;
 }
 
-// Sum of squares of a batch in 64 bits, from memory again: squares of fp32
-// numbers are exact there and within range.
+// A sum as two fp32 numbers.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = a + b, z = s - a;
+  return {s, (a - (s - z)) + (b - z)};
+}
+__device__ __forceinline__ Two add(Two a, Two b) {
+  Two s = two_sum(a.hi, b.hi);
+  const float lo = s.lo + (a.lo + b.lo), hi = s.hi + lo;
+  return {hi, lo - (hi - s.hi)};
+}
+
+// A sum of squares v * 2^(176 band), or, of maxima, a magnitude (band 0). An
+// infinity among the elements is the band kInf, a NaN kNan: the higher band is
+// what a join keeps (the lower one's share is below 2^-46 of it, but
+// for the bottom of a band, where it is added).
+enum Band : int { kSmall = -1, kMid = 0, kBig = 1, kInf = 2, kNan = 3 };
+struct Value {
+  int band;
+  Two v;
+};
+constexpr float kScale = 3.0948500982134507e26f;      // 2^88
+constexpr float kUnscale = 3.2311742677852644e-27f;   // 2^-88
+constexpr float kMidLow = 8.0779356694631609e-28f;    // 2^-90: where a batch's fp32 squares have lost nothing
+constexpr float kMidHigh = 1.2379400392853803e27f;    // 2^90: where 2^34 batches still fit
+__device__ __forceinline__ Two lowered(Two v) { return {v.hi * kUnscale * kUnscale, v.lo * kUnscale * kUnscale}; }
+__device__ __forceinline__ Value sum_of(Value a, Value b) {
+  if (a.band == b.band) return {a.band, add(a.v, b.v)};
+  const Value& top = a.band > b.band ? a : b;
+  const Value& low = a.band > b.band ? b : a;
+  return {top.band, top.band - low.band == 1 && top.band <= kBig ? add(top.v, lowered(low.v)) : top.v};
+}
+__device__ __forceinline__ Value larger(Value a, Value b) { return a.band > b.band || (a.band == b.band && a.v.hi >= b.v.hi) ? a : b; }
+template <bool MAX>
+__device__ __forceinline__ Value join(Value a, Value b) {
+  return MAX ? larger(a, b) : sum_of(a, b);
+}
+__device__ __forceinline__ Value nothing() { return {kSmall, {0.0f, 0.0f}}; }
+
+template <bool MAX>
+__device__ __forceinline__ Value warp_join(Value a) {
+  // (the bands mostly agree)
+  const int top = __reduce_max_sync(~0u, a.band);
+  if (!MAX && __reduce_min_sync(~0u, a.band) == top) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a.v = add(a.v, {__shfl_xor_sync(~0u, a.v.hi, o), __shfl_xor_sync(~0u, a.v.lo, o)});
+    return a;
+  }
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1)
+    a = join<MAX>(a, {__shfl_xor_sync(~0u, a.band, o), {__shfl_xor_sync(~0u, a.v.hi, o), __shfl_xor_sync(~0u, a.v.lo, o)}});
+  return a;
+}
+
+// One square, in its band.
+__device__ __forceinline__ Value square(float x) {
+  const float a = fabsf(x);
+  if (!(a < INFINITY)) return {a == INFINITY ? kInf : kNan, {0.0f, 0.0f}};
+  const float f = a < 1e-13f ? kScale : a > 1e13f ? kUnscale : 1.0f, b = a * f;
+  return {a < 1e-13f ? kSmall : a > 1e13f ? kBig : kMid, {b * b, fmaf(b, b, -(b * b))}};
+}
+
+// The sum of squares of a batch whose fp32 squares could have overflowed, or have
+// been lost below fp32's range, from memory again.
 template <bool BF16>
-__device__ __noinline__ double squares_wide(const char* base, int64_t g, int64_t hi) {
-  double s = 0.0;
+__device__ __noinline__ Value squares_in_bands(const char* base, int64_t g, int64_t hi) {
+  Value s = nothing();
 #pragma unroll 1
   for (int i = 0; i < kLoads && g < hi; ++i, g += 32) {
     const uint4 r = load16(base + 16 * g);
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
+#pragma unroll 1
     for (int j = 0; j < 4; ++j) {
-      const double a = BF16 ? double(bf16lo(w[j])) : double(__uint_as_float(w[j])), b = BF16 ? double(bf16hi(w[j])) : 0.0;
-      s += a * a + b * b;
+      s = sum_of(s, square(BF16 ? bf16lo(w[j]) : __uint_as_float(w[j])));
+      if (BF16) s = sum_of(s, square(bf16hi(w[j])));
     }
   }
   return s;
 }
 
-// The sum of squares of a batch, the granules g, g + 32, ... below hi: fp32
-// within it (at most 64 terms), 64 bits beyond. Where fp32 squares could have
-// overflowed, or have been lost below its range, the batch is summed in 64 bits.
+// Adds the sum of squares of a batch, the granules g, g + 32, ... below hi, to a
+// sum: fp32 within it (at most 64 terms). `odd`: of batches outside the middle band.
 template <bool BF16>
-__device__ __forceinline__ double squares(const uint4 (&r)[kLoads], const char* base, int64_t g, int64_t hi) {
+__device__ __forceinline__ void add_squares(const uint4 (&r)[kLoads], const char* base, int64_t g, int64_t hi, Two& mid, Value& odd) {
   float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   uint32_t any = 0;
 #pragma unroll
@@ -71,9 +139,8 @@ __device__ __forceinline__ double squares(const uint4 (&r)[kLoads], const char* 
     }
   }
   const float sum = (s[0] + s[1]) + (s[2] + s[3]);
-  if (sum > 1e-25f && sum < 1e37f) return double(sum);
-  if ((any & (BF16 ? 0x7fff7fffu : 0x7fffffffu)) == 0) return 0.0;
-  return squares_wide<BF16>(base, g, hi);
+  if (sum >= kMidLow && sum < kMidHigh) mid = add(mid, {sum, 0.0f});
+  else if ((any & (BF16 ? 0x7fff7fffu : 0x7fffffffu)) != 0) odd = sum_of(odd, squares_in_bands<BF16>(base, g, hi));
 }
 
 // Magnitudes as integers order like the numbers, NaN above infinity.
@@ -93,6 +160,22 @@ __device__ __forceinline__ uint32_t largest(const uint4 (&r)[kLoads], uint32_t t
     }
   }
   return top;
+}
+__device__ __forceinline__ Value magnitude(uint32_t bits) {
+  if (bits >= 0x7f800000u) return {bits > 0x7f800000u ? kNan : kInf, {0.0f, 0.0f}};
+  return {kMid, {__uint_as_float(bits), 0.0f}};
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// The same place in another CTA of the cluster.
+template <class T>
+__device__ __forceinline__ T* peer(T* p, int rank) {
+  uint64_t a;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(p), "r"(rank));
+  return reinterpret_cast<T*>(a);
 }
 
 // A tensor as granules: `lead` elements of the first one lie before it.
@@ -137,129 +220,151 @@ __device__ __forceinline__ int entry_of(const Table& t, int64_t g) {
 }
 
 // Granules a warp: a multiple of 32, so that its loads are whole lines.
-__host__ __device__ inline int64_t stretch(int64_t granules, int64_t warps) {
-  return (granules + warps * 32 - 1) / (warps * 32) * 32;
-}
+inline int64_t stretch(int64_t granules, int64_t warps) { return (granules + warps * 32 - 1) / (warps * 32) * 32; }
+// The warp that a granule belongs to. (2^37 granules, 2 TB, are more than any device has.)
+__device__ __forceinline__ int warp_of(int64_t granule, int64_t per) { return int(uint32_t(granule >> 5) / uint32_t(per >> 5)); }
 
-template <bool BF16>
-__device__ __forceinline__ double squares_of(const char* base, int64_t lo, int64_t hi, int lane) {
-  double sum = 0.0;
-  int64_t g = lo + lane;
+template <bool BF16, bool MAX>
+__device__ __forceinline__ Value value_of(const char* base, int64_t lo, int64_t hi, int lane) {
+  Two mid = {0.0f, 0.0f};
+  Value odd = nothing();
+  uint32_t top = 0;
   uint4 r[kLoads];
+  int64_t g = lo + lane;
+  const auto take = [&] {
+    if (MAX) top = largest<BF16>(r, top);
+    else add_squares<BF16>(r, base, g, hi, mid, odd);
+  };
+#pragma unroll 1
   for (; g + 32 * (kLoads - 1) < hi; g += 32 * kLoads) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) r[i] = load16(base + 16 * (g + 32 * i));
-    sum += squares<BF16>(r, base, g, hi);
+    take();
   }
   if (g < hi) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) r[i] = g + 32 * i < hi ? load16(base + 16 * (g + 32 * i)) : make_uint4(0, 0, 0, 0);
-    sum += squares<BF16>(r, base, g, hi);
+    take();
   }
-  return sum;
+  if (MAX) return magnitude(top);
+  return mid.hi > 0.0f ? sum_of(odd, {kMid, mid}) : odd;
 }
 
-template <bool BF16>
-__device__ __forceinline__ double largest_of(const char* base, int64_t lo, int64_t hi, int lane) {
-  uint32_t top = 0;
-  uint4 r[kLoads];
-  for (int64_t g = lo + lane; g < hi; g += 32 * kLoads) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) r[i] = g + 32 * i < hi ? load16(base + 16 * (g + 32 * i)) : make_uint4(0, 0, 0, 0);
-    top = largest<BF16>(r, top);
-  }
-  return double(__uint_as_float(top));
-}
-
-// The larger one; a NaN where either is.
-__device__ __forceinline__ double larger(double a, double b) { return a >= b || a != a ? a : b; }
-
-template <bool MAX>
-__device__ __forceinline__ double warp_join(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const double u = __shfl_xor_sync(~0u, v, o);
-    v = MAX ? larger(v, u) : v + u;
-  }
-  return v;
-}
-
-// Every warp's sum over each tensor that its stretch meets.
-template <int CAP, bool MAX>
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(const __grid_constant__ GradTable<CAP> t, GradJob job) {
-  grid_dependency_wait();
-  grid_dependents_launch();
-  const int lane = threadIdx.x % 32;
-  const int64_t warps = int64_t(gridDim.x) * (kNormThreads / 32);
-  const int64_t w = int64_t(blockIdx.x) * (kNormThreads / 32) + threadIdx.x / 32;
-  const int64_t per = stretch(t.granules, warps);
-  const int64_t lo = w * per, hi = min(t.granules, lo + per);
+// Every warp's sum over each tensor that its stretch [lo, hi) meets: place(i) for tensor i.
+template <bool MAX, class Table, class Place>
+__device__ __forceinline__ void stretch_values(const Table& t, int64_t lo, int64_t hi, int lane, Place place) {
   if (lo >= hi) return;
+#pragma unroll 1
   for (int i = entry_of(t, lo); i < t.n && t.e[i].first < hi; ++i) {
     const Span s(t.e[i].in, t.e[i].count);
     const int64_t g0 = max(lo - t.e[i].first, int64_t(0)), g1 = min(hi - t.e[i].first, s.granules);
     if (g0 >= g1) continue;
     const int64_t a = max(g0, int64_t(s.lead > 0)), b = min(g1, s.full);
-    double v;
-    if (MAX) v = s.es == 2 ? largest_of<true>(s.base, a, b, lane) : largest_of<false>(s.base, a, b, lane);
-    else v = s.es == 2 ? squares_of<true>(s.base, a, b, lane) : squares_of<false>(s.base, a, b, lane);
+    Value v = s.es == 2 ? value_of<true, MAX>(s.base, a, b, lane) : value_of<false, MAX>(s.base, a, b, lane);
     const int64_t e = s.edge(g0, g1, lane);
     if (e >= 0) {
-      const double x = double(element(t.e[i].in, e, s.es));
-      v = MAX ? larger(v, fabs(x)) : v + x * x;
+      const float x = element(t.e[i].in, e, s.es);
+      v = MAX ? larger(v, magnitude(__float_as_uint(x) & 0x7fffffffu)) : x != 0.0f ? sum_of(v, square(x)) : v;
     }
     v = warp_join<MAX>(v);
-    if (lane == 0) job.partials[w + i] = v;
+    if (lane == 0) *place(i) = v;
   }
 }
 
-__device__ __forceinline__ void write_stats(const GradJob& job, double total) {
-  const double scale = fabs(double(job.grad_scale));
-  const double norm = (job.kind == AR_NORM_MAX ? total : sqrt(total)) * scale;
-  const bool finite = isfinite(total);
-  const double ratio = job.max_norm / (norm + job.eps);
-  const float c = !finite ? 0.0f : ratio < 1.0 ? float(ratio) : 1.0f;
-  job.stats[0] = float(norm);
+template <int CAP, bool MAX>
+__global__ void __launch_bounds__(kNormThreads) norm_kernel(const __grid_constant__ GradTable<CAP> t, GradJob job) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int64_t w = int64_t(blockIdx.x) * (kNormThreads / 32) + threadIdx.x / 32;
+  const int64_t lo = w * t.per, hi = min(t.granules, lo + t.per);
+  Value* partials = reinterpret_cast<Value*>(job.partials) + w;
+  stretch_values<MAX>(t, lo, hi, threadIdx.x % 32, [&](int i) { return partials + i; });
+}
+
+// The root of a sum of squares as two numbers (times 2^(88 band)).
+__device__ __forceinline__ Two root_of(Two v) {
+  if (!(v.hi > 0.0f)) return {0.0f, 0.0f};
+  const float r = sqrtf(v.hi);
+  return {r, (fmaf(-r, r, v.hi) + v.lo) / (2.0f * r)};
+}
+__device__ __forceinline__ float power(int band) { return band == kBig ? kScale : band == kSmall ? kUnscale : 1.0f; }
+
+// A sum's norm, in fp32.
+template <bool MAX>
+__device__ __forceinline__ float norm_of(Value v, float scale) {
+  if (v.band >= kInf) return v.band == kInf ? INFINITY : __int_as_float(0x7fc00000);
+  const Two r = MAX ? v.v : root_of(v.v);
+  // (one of the two factors may leave fp32's range where the norm does not)
+  const float f = MAX ? 1.0f : power(v.band);
+  return fabsf(scale) >= 1.0f == f >= 1.0f ? (r.hi + r.lo) * f * scale : (r.hi + r.lo) * (f * scale);
+}
+
+template <bool MAX>
+__device__ __forceinline__ void write_stats(const GradJob& job, Value total) {
+  const bool finite = total.band < kInf;
+  const float scale = fabsf(job.grad_scale);
+  float c = 0.0f;
+  if (finite) {
+    // max_norm / (r scale + eps), all in pairs and times f
+    Two r = MAX ? total.v : root_of(total.v);
+    float f = MAX ? 1.0f : 1.0f / power(total.band);
+    if (MAX && r.hi > 1e18f) f = kUnscale, r = {r.hi * f, 0.0f};
+    const float p = r.hi * scale;
+    r = two_sum(p, fmaf(r.hi, scale, -p) + r.lo * scale);
+    const Two n = add(r, {job.eps * f, job.eps_low * f}), m = {job.max_norm * f, job.max_norm_low * f};
+    c = m.hi / n.hi;
+    if (c < INFINITY) c += ((fmaf(-c, n.hi, m.hi) + m.lo) - c * n.lo) / n.hi;
+    if (!(c < 1.0f)) c = p < INFINITY ? 1.0f : 0.0f;  // (1 also for 0 / 0: a norm of 0 and no eps)
+  }
+  job.stats[0] = norm_of<MAX>(total, scale);
   job.stats[1] = c;
   job.stats[2] = c < 1.0f ? 1.0f : 0.0f;
   job.stats[3] = finite ? 1.0f : 0.0f;
 }
 
-// One CTA: the tensors' norms from the warps' sums; behind the last launch of a
-// call, the statistics.
-template <int CAP, bool MAX>
-__global__ void __launch_bounds__(1024) finish_kernel(const __grid_constant__ GradTable<CAP> t, GradJob job, int64_t warps,
-                                                      int group, int groups) {
-  grid_dependency_wait();
-  grid_dependents_launch();
-  extern __shared__ double part[];
-  __shared__ double sums[32];
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int64_t per = stretch(t.granules, warps);
-  const int used = int(t.granules > 0 ? (t.granules - 1) / per + t.n : 0);
-  for (int i = threadIdx.x; i < used; i += 1024) part[i] = job.partials[i];
-  __syncthreads();
+// The tensors' norms from the warps' sums in `part`, by one CTA; returns the sum over all tensors (thread 0).
+template <bool MAX, class Table>
+__device__ __forceinline__ Value finish_tensors(const Table& t, const GradJob& job, const Value* part, Value* sums) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = int(blockDim.x) / 32;
   const float scale = fabsf(job.grad_scale);
-  double mine = 0.0;
-  for (int i = warp; i < t.n; i += 32) {
+  Value mine = nothing();
+#pragma unroll 1
+  for (int i = warp; i < t.n; i += warps) {
     const int64_t first = t.e[i].first, end = i + 1 < t.n ? t.e[i + 1].first : t.granules;
-    double v = 0.0;
-    if (end > first)
-      for (int j = int(first / per) + i + lane; j <= int((end - 1) / per) + i; j += 32) v = MAX ? larger(v, part[j]) : v + part[j];
-    v = warp_join<MAX>(v);
-    if (lane == 0 && job.norms != nullptr) job.norms[i] = float((MAX ? v : sqrt(v)) * scale);
-    mine = MAX ? larger(mine, v) : mine + v;
+    Value v = nothing();
+    if (end > first) {
+      const int last = warp_of(end - 1, t.per) + i;
+      for (int j = warp_of(first, t.per) + i + lane; j <= last; j += 32) v = join<MAX>(v, part[j]);
+      v = warp_join<MAX>(v);
+    }
+    if (lane == 0 && job.norms != nullptr) job.norms[i] = norm_of<MAX>(v, scale);
+    mine = join<MAX>(mine, v);
   }
   if (lane == 0) sums[warp] = mine;
   __syncthreads();
+  if (warp == 0) mine = warp_join<MAX>(lane < warps ? sums[lane] : nothing());
+  return mine;
+}
+
+// One CTA; behind the last launch of a call, the statistics.
+template <int CAP, bool MAX>
+__global__ void __launch_bounds__(1024) finish_kernel(const __grid_constant__ GradTable<CAP> t, GradJob job, int group, int groups) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  extern __shared__ __align__(16) char shared[];
+  Value* part = reinterpret_cast<Value*>(shared);
+  __shared__ Value sums[32];
+  const int used = t.granules > 0 ? warp_of(t.granules - 1, t.per) + t.n : 0;
+  for (int i = threadIdx.x; i < used; i += 1024) part[i] = reinterpret_cast<const Value*>(job.partials)[i];
+  __syncthreads();
+  Value total = finish_tensors<MAX>(t, job, part, sums);
   if (threadIdx.x == 0) {
-    double total = 0.0;
-    for (int i = 0; i < 32; ++i) total = MAX ? larger(total, sums[i]) : total + sums[i];
+    Value* all = reinterpret_cast<Value*>(job.groups);
     if (group + 1 < groups) {
-      job.groups[group] = total;
+      all[group] = total;
     } else {
-      for (int i = 0; i < group; ++i) total = MAX ? larger(total, job.groups[i]) : total + job.groups[i];
-      write_stats(job, total);
+      for (int i = 0; i < group; ++i) total = join<MAX>(total, all[i]);
+      write_stats<MAX>(job, total);
     }
   }
 }
@@ -297,18 +402,11 @@ __device__ __forceinline__ void scale_granules(const char* base, char* out, int6
 }
 
 // The scaled gradients, stretch by stretch as the norm read them.
-template <int CAP>
-__global__ void __launch_bounds__(kNormThreads) scale_kernel(const __grid_constant__ GradTable<CAP> t, GradJob job) {
-  grid_dependency_wait();
-  grid_dependents_launch();
-  const int lane = threadIdx.x % 32;
-  const int64_t warps = int64_t(gridDim.x) * (kNormThreads / 32);
-  const int64_t w = int64_t(blockIdx.x) * (kNormThreads / 32) + threadIdx.x / 32;
-  const int64_t per = stretch(t.granules, warps);
-  const int64_t lo = w * per, hi = min(t.granules, lo + per);
+// The stretch [lo, hi), scaled, from its end: what the norm read last may still be in the L2.
+template <class Table>
+__device__ __forceinline__ void scale_stretch(const Table& t, int64_t lo, int64_t hi, int lane, float f, bool zero) {
   if (lo >= hi) return;
-  const bool zero = job.stats[3] == 0.0f;
-  const float f = zero ? 0.0f : job.stats[1] * job.grad_scale;
+#pragma unroll 1
   for (int i = entry_of(t, hi - 1); i >= 0; --i) {
     const GradEntry& e = t.e[i];
     const Span s(e.in, e.count);
@@ -333,9 +431,53 @@ __global__ void __launch_bounds__(kNormThreads) scale_kernel(const __grid_consta
   }
 }
 
+// The scaled gradients, stretch by stretch as the norm read them.
+template <int CAP>
+__global__ void __launch_bounds__(kNormThreads) scale_kernel(const __grid_constant__ GradTable<CAP> t, GradJob job) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int64_t w = int64_t(blockIdx.x) * (kNormThreads / 32) + threadIdx.x / 32;
+  const bool zero = job.stats[3] == 0.0f;
+  scale_stretch(t, w * t.per, min(t.granules, (w + 1) * t.per), threadIdx.x % 32, zero ? 0.0f : job.stats[1] * job.grad_scale, zero);
+}
+
+// A short list, by one cluster in one launch: the warps' sums, the statistics, and, CLIP, the scaled gradients.
+constexpr int kMaxRanks = 8;
+template <bool MAX, bool CLIP>
+__global__ void __launch_bounds__(kNormThreads) short_kernel(const __grid_constant__ GradTable<kGradCapSmall> t, GradJob job) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  __shared__ Value part[kMaxRanks * (kNormThreads / 32) + kGradCapSmall], sums[32];
+  __shared__ float factor;
+  const int lane = threadIdx.x % 32, ranks = int(gridDim.x), rank = int(blockIdx.x);
+  const int w = rank * (kNormThreads / 32) + threadIdx.x / 32;
+  const int64_t lo = w * t.per, hi = min(t.granules, lo + t.per);
+  if (ranks > 1) cluster_barrier();  // (the first CTA runs)
+  // the first CTA's shared memory has all sums
+  Value* to = ranks > 1 ? peer(part, 0) : part;
+  stretch_values<MAX>(t, lo, hi, lane, [&](int i) { return to + (w + i); });
+  if (ranks > 1) cluster_barrier();
+  else __syncthreads();
+  if (rank == 0) {
+    const Value total = finish_tensors<MAX>(t, job, part, sums);
+    if (threadIdx.x == 0) {
+      write_stats<MAX>(job, total);
+      factor = total.band >= kInf ? 0.0f : job.stats[1] * job.grad_scale;
+      sums[0].band = total.band;
+    }
+  }
+  if (!CLIP) return;
+  if (ranks > 1) cluster_barrier();
+  else __syncthreads();
+  const float f = ranks > 1 ? *peer(&factor, 0) : factor;
+  const bool zero = (ranks > 1 ? peer(sums, 0) : sums)->band >= kInf;
+  scale_stretch(t, lo, hi, lane, f, zero);
+  if (ranks > 1) cluster_barrier();  // (the first CTA stays until it has been read)
+}
+
 // ---------------------------------------------------------------- AdamW
 
-constexpr int kAdamThreads = 256;
+constexpr int kAdamThreads = 256, kAdamCtas = 3;  // CTAs an SM
 
 __device__ __forceinline__ void load8(const void* p, int64_t e, bool bf16, float (&x)[8]) {
   if (bf16) {
@@ -392,7 +534,7 @@ __device__ __forceinline__ void adam_one(const AdamEntry& e, int64_t x, const Ad
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamTable<CAP> t, AdamJob job) {
+__global__ void __launch_bounds__(kAdamThreads, kAdamCtas) adamw_kernel(const __grid_constant__ AdamTable<CAP> t, AdamJob job) {
   grid_dependency_wait();
   grid_dependents_launch();
   AdamStep step = {job.rates, job.grad_scale, false};
@@ -420,9 +562,33 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
       continue;
     }
     // groups of 8 elements at multiples of 8 in memory
+    constexpr int kGroups = kAdamTile / (8 * kAdamThreads);
+    const int64_t x0 = from + 8 * int(threadIdx.x) - e.phase;
+    if (x0 >= 0 && x0 + 8 * kAdamThreads * (kGroups - 1) + 8 <= e.count) {
+      float g[kGroups][8], w[kGroups][8], m[kGroups][8], v[kGroups][8];
 #pragma unroll
-    for (int i = 0; i < kAdamTile / (8 * kAdamThreads); ++i) {
-      const int64_t x = from + 8 * (i * kAdamThreads + int(threadIdx.x)) - e.phase;
+      for (int i = 0; i < kGroups; ++i) {
+        const int64_t x = x0 + 8 * kAdamThreads * i;
+        load8(e.g, x, e.g_bf16, g[i]);
+        load8(e.w, x, e.w_bf16, w[i]);
+        load8(e.m, x, false, m[i]);
+        load8(e.v, x, false, v[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) {
+        const int64_t x = x0 + 8 * kAdamThreads * i;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) step(g[i][j], w[i][j], m[i][j], v[i][j]);
+        store8(e.m_out, x, false, m[i]);
+        store8(e.v_out, x, false, v[i]);
+        store8(e.w_out, x, e.w_bf16, w[i]);
+        if (e.p_out != nullptr) store8(e.p_out, x, e.p_bf16, w[i]);
+      }
+      continue;
+    }
+#pragma unroll 1
+    for (int i = 0; i < kGroups; ++i) {
+      const int64_t x = x0 + 8 * kAdamThreads * i;
       if (x >= 0 && x + 8 <= e.count) {
         float g[8], w[8], m[8], v[8];
         load8(e.g, x, e.g_bf16, g);
@@ -447,17 +613,21 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
 // Launched so that it may be scheduled while the kernel before it drains; every
 // kernel here waits for that one before it touches memory.
 template <class... Params, class... Args>
-cudaError_t launch(void (*kernel)(Params...), int64_t grid, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
+cudaError_t launch(void (*kernel)(Params...), int64_t grid, int threads, int cluster, size_t smem, cudaStream_t stream,
+                   const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
   cfg.blockDim = dim3(unsigned(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -487,13 +657,19 @@ cudaError_t launch_norm_group(const GradTensor* g, int n, const GradJob& job, in
   GradTable<CAP> t;
   fill(t, g, n);
   const int64_t ctas = norm_ctas(t.granules), warps = ctas * (kNormThreads / 32);
+  t.per = stretch(t.granules, warps);
   const bool max = job.kind == AR_NORM_MAX;
   cudaError_t err = cudaSuccess;
   if (t.granules > 0)
-    err = launch(max ? norm_kernel<CAP, true> : norm_kernel<CAP, false>, ctas, kNormThreads, 0, stream, t, job);
+    err = launch(max ? norm_kernel<CAP, true> : norm_kernel<CAP, false>, ctas, kNormThreads, 1, 0, stream, t, job);
   if (err != cudaSuccess) return err;
-  return launch(max ? finish_kernel<CAP, true> : finish_kernel<CAP, false>, 1, 1024, size_t(8 * (warps + n)), stream, t, job,
-                warps, group, groups);
+  const size_t smem = sizeof(Value) * size_t(warps + n);
+  const auto finish = max ? finish_kernel<CAP, true> : finish_kernel<CAP, false>;
+  if (smem > (40 << 10))
+    err = cudaFuncSetAttribute(reinterpret_cast<const void*>(finish), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               int(sizeof(Value) * (kMaxGradWarps + CAP)));
+  if (err != cudaSuccess) return err;
+  return launch(finish, 1, 1024, 1, smem, stream, t, job, group, groups);
 }
 
 template <int CAP>
@@ -501,7 +677,22 @@ cudaError_t launch_scale_group(const GradTensor* g, int n, const GradJob& job, c
   GradTable<CAP> t;
   fill(t, g, n);
   if (t.granules == 0) return cudaSuccess;
-  return launch(scale_kernel<CAP>, norm_ctas(t.granules), kNormThreads, 0, stream, t, job);
+  const int64_t ctas = norm_ctas(t.granules);
+  t.per = stretch(t.granules, ctas * (kNormThreads / 32));
+  return launch(scale_kernel<CAP>, ctas, kNormThreads, 1, 0, stream, t, job);
+}
+
+// Lists of at most this many granules take one launch.
+constexpr int64_t kShort = 2 << 16;
+
+cudaError_t launch_short(GradTable<kGradCapSmall>& t, bool clip, const GradJob& job, cudaStream_t stream) {
+  int ranks = 1;  // 4 granules a lane, where there are as many
+  while (ranks < kMaxRanks && t.granules > int64_t(ranks) * kNormThreads * 4) ranks *= 2;
+  t.per = std::max<int64_t>(32, stretch(t.granules, ranks * (kNormThreads / 32)));
+  const bool max = job.kind == AR_NORM_MAX;
+  return launch(clip ? (max ? short_kernel<true, true> : short_kernel<false, true>)
+                     : (max ? short_kernel<true, false> : short_kernel<false, false>),
+                ranks, kNormThreads, ranks, 0, stream, t, job);
 }
 
 template <int CAP>
@@ -517,13 +708,18 @@ cudaError_t launch_adam_group(const AdamEntry* e, int n, const AdamJob& job, cud
   if (tiles == 0) return cudaSuccess;
   if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
   t.tiles = int(tiles);
-  const int64_t ctas = std::min<int64_t>(tiles, 4 * device_sms());
-  return launch(adamw_kernel<CAP>, ctas, kAdamThreads, 0, stream, t, job);
+  const int64_t ctas = std::min<int64_t>(tiles, kAdamCtas * device_sms());
+  return launch(adamw_kernel<CAP>, ctas, kAdamThreads, 1, 0, stream, t, job);
 }
 
 }  // namespace
 
 cudaError_t launch_grad_norm(const GradTensor* g, int n, bool clip, const GradJob& job, cudaStream_t stream) {
+  if (n <= kGradCapSmall) {
+    GradTable<kGradCapSmall> t;
+    fill(t, g, n);
+    if (t.granules <= kShort) return launch_short(t, clip, job, stream);
+  }
   const int groups = (n + kGradCap - 1) / kGradCap;
   cudaError_t err = cudaSuccess;
   for (int k = 0; k < groups && err == cudaSuccess; ++k) {

@@ -28,24 +28,25 @@ template <int CAP>
 struct GradTable {
   int n;
   int64_t granules;  // of all entries
+  int64_t per;       // of them a warp
   GradEntry e[CAP];
 };
 
 // What the launches of one call have in common.
 struct GradJob {
   int kind;  // ar_norm_kind
-  double max_norm, eps;
+  float max_norm, max_norm_low, eps, eps_low;  // each as two numbers
   float grad_scale;
   float* stats;
-  float* norms;      // may be null
-  double* groups;    // workspace: the sum (or maximum) of every launch's tensors
-  double* partials;  // workspace: [warps + tensors] of one launch
+  float* norms;    // may be null
+  void* groups;    // workspace: the sum (or maximum) of every launch's tensors, 12 bytes each
+  void* partials;  // workspace: those of one launch's warps, [warps + tensors]
 };
 
 // Byte offsets of the workspace's parts, and its size.
 constexpr int kGradGroups = (AR_MAX_TENSORS + kGradCap - 1) / kGradCap;
-constexpr int64_t kGradPartials = (8 * kGradGroups + 255) / 256 * 256;
-constexpr int64_t kGradWorkspace = kGradPartials + 8 * (kMaxGradWarps + kGradCap);
+constexpr int64_t kGradPartials = (12 * kGradGroups + 255) / 256 * 256;
+constexpr int64_t kGradWorkspace = kGradPartials + (12 * (kMaxGradWarps + kGradCap) + 255) / 256 * 256;
 
 // A tensor of a call, as checked.
 struct GradTensor {

@@ -15,12 +15,12 @@ namespace ar {
 // a captured launch is complete in itself. Short lists take a short table.
 constexpr int kGradCap = 768, kGradCapSmall = 48;
 constexpr int kAdamCap = 360, kAdamCapSmall = 40;
-constexpr int kMaxGradWarps = 4864;  // warps of a norm launch: 32 an SM
+constexpr int kMaxGradCtas = 512;  // CTAs of a norm launch
 
 struct GradEntry {
   const char* in;
   char* out;      // clipping only
-  int64_t first;  // granules (16 aligned bytes) of the tensors before this one
+  int64_t first;  // granules (16 aligned bytes, and some a tensor) of the tensors before this one
   int64_t count;  // elements * 2 + (1: bf16)
 };
 
@@ -40,13 +40,13 @@ struct GradJob {
   float* stats;
   float* norms;    // may be null
   void* groups;    // workspace: the sum (or maximum) of every launch's tensors, 12 bytes each
-  void* partials;  // workspace: those of one launch's warps, [warps + tensors]
+  void* partials;  // workspace: those of one launch's CTAs, [CTAs + tensors]
 };
 
 // Byte offsets of the workspace's parts, and its size.
 constexpr int kGradGroups = (AR_MAX_TENSORS + kGradCap - 1) / kGradCap;
 constexpr int64_t kGradPartials = (12 * kGradGroups + 255) / 256 * 256;
-constexpr int64_t kGradWorkspace = kGradPartials + (12 * (kMaxGradWarps + kGradCap) + 255) / 256 * 256;
+constexpr int64_t kGradWorkspace = kGradPartials + (12 * (kMaxGradCtas + kGradCap) + 255) / 256 * 256;
 
 // A tensor of a call, as checked.
 struct GradTensor {

@@ -703,12 +703,12 @@ def _tensors(x, what: str, like: TensorList | None = None):
     return x
 
 
-def _here(tensors: TensorList):
+def _here(device):
     """Refuses tensors of another device than the one that the call would run on."""
     import torch
 
-    if torch.cuda.is_initialized() and tensors.device.index != torch._C._cuda_getDevice():
-        raise ValueError(f"tensors on {tensors.device}, but the current device is cuda:{torch._C._cuda_getDevice()}")
+    if torch.cuda.is_initialized() and device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on {device}, but the current device is cuda:{torch._C._cuda_getDevice()}")
 
 
 @functools.lru_cache(maxsize=1024)
@@ -725,7 +725,7 @@ def ar_grad_workspace(grads) -> int:
 
 def _norm_call(grads, max_norm, kind, eps, grad_scale, stats, norms, workspace, stream):
     grads = _tensors(grads, "grads")
-    _here(grads)
+    _here(grads.device)
     n, like = len(grads), grads.like
     stats, stats_at = _output(stats, 4, like, "stats", stream)
     norms, norms_at = _output(norms, n, like, "norms", stream)
@@ -770,7 +770,7 @@ def ar_adamw_step(params, grads, exp_avgs, exp_avg_sqs, lr: float, step, betas=(
     import torch
 
     p = _tensors(params, "params")
-    _here(p)
+    _here(p.device)
     g = _tensors(grads, "grads", p)
     m, v = _tensors(exp_avgs, "exp_avgs", p), _tensors(exp_avg_sqs, "exp_avg_sqs", p)
     w, wo = _tensors(masters, "masters", p), _tensors(masters_out, "masters_out", p)
@@ -811,6 +811,7 @@ def ar_verify_drafts(target, drafts, uniforms=None, draft_start=None, draft_logi
     import torch
 
     ld = _row_major(target, "target")
+    _here(target.device)
     rows, vocab = target.shape
     n_drafts = drafts.shape[0] if drafts.dim() == 1 else -1
     n_seq = rows - n_drafts
@@ -823,15 +824,13 @@ def ar_verify_drafts(target, drafts, uniforms=None, draft_start=None, draft_logi
         raise ValueError("uniforms: wanted, but in greedy mode")
     u = 0 if uniforms is None else _vector(uniforms, torch.float32, rows, "uniforms")
     start = 0 if draft_start is None else _vector(draft_start, torch.int64, n_seq + 1, "draft_start")
-    d = _lib.ArVerifyDesc(vocab=vocab, drafts=drafts_at, uniforms=u, draft_start=start, n_drafts=n_drafts, n_seq=n_seq,
-                          mode=mode)
-    d.target = _lib.ArScoreRows(target.data_ptr(), rows, ld, _dtype_of(target), temperature)
+    x, y = (target.data_ptr(), rows, ld, _dtype_of(target), temperature), ()
     if draft_logits is not None:
-        if tuple(draft_logits.shape) != (n_drafts, vocab):
+        if draft_logits.shape != (n_drafts, vocab):
             raise ValueError(f"draft_logits: {(n_drafts, vocab)} wanted, got {tuple(draft_logits.shape)}")
-        d.draft = _lib.ArScoreRows(draft_logits.data_ptr(), n_drafts, _row_major(draft_logits, "draft_logits"),
-                                   _dtype_of(draft_logits),
-                                   temperature if draft_temperature is None else draft_temperature)
+        y = (draft_logits.data_ptr(), n_drafts, _row_major(draft_logits, "draft_logits"), _dtype_of(draft_logits),
+             temperature if draft_temperature is None else draft_temperature)
+    d = _lib.ArVerifyDesc(x, y, vocab, drafts_at, u, start, n_drafts, n_seq, mode)
     accepted, accepted_at = _output(accepted, n_seq, target, "accepted", stream, torch.int64)
     tokens, tokens_at = _output(tokens, rows, target, "tokens", stream, torch.int64)
     logp, logp_at = _output(logp, rows, target, "logp", stream)

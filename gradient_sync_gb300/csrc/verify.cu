@@ -417,30 +417,28 @@ template <bool XB, bool YB, int MODE>
 __global__ void __launch_bounds__(kRowThreads, 4) sums_kernel(const __grid_constant__ VerifyParams p) {
   grid_dependency_wait();
   grid_dependents_launch();
-  __shared__ Place found;
-  __shared__ int skip;
   __shared__ Post posts[kRowWarps];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int part = int(blockIdx.x) & (p.parts - 1);
   const int64_t row = int64_t(blockIdx.x >> p.part_bits) * p.pitch + blockIdx.y;
   if (row >= p.n_drafts + p.n_seq) return;
-  // the row's sequence, by the thread that has it
-  int any = 0;
-  for (int64_t base = 0; base < p.n_seq && !any; base += kRowThreads) {
-    const int64_t i = base + threadIdx.x;
-    bool here = false;
-    if (i < p.n_seq) {
-      const int first = start_of(p, i), count = max(start_of(p, i + 1) - first, 0);
-      here = first + i <= row && row <= first + i + count;
-      if (here) {
-        found = {int(row), int(i), first, count, int(row - first - i)};
-        skip = p.fallen != nullptr && *const_cast<volatile int*>(p.fallen + i) < row - first - i;
-      }
-    }
-    any = __syncthreads_or(here);
+  // the row's sequence: the last one whose first row is not behind this one, found among as many as there are threads
+  // at a time
+  int seq = 0;
+  for (int64_t end = p.n_seq;;) {
+    const int64_t step = (end - seq + kRowThreads - 1) / kRowThreads, i = seq + threadIdx.x * step;
+    const int n = __syncthreads_count(i < end && start_of(p, i) + i <= row);
+    if (n == 0) return;
+    seq += int((n - 1) * step);
+    if (step == 1) break;
+    end = min(end, seq + step);
   }
-  if (!any || skip) return;
-  const Place at = found;
+  const int first = start_of(p, seq), count = max(start_of(p, seq + 1) - first, 0);
+  const Place at = {int(row), seq, first, count, int(row) - first - seq};
+  if (at.j < 0 || at.j > count) return;
+  if (p.fallen != nullptr && at.j > 0 &&
+      __syncthreads_or(threadIdx.x == 0 && *const_cast<volatile int*>(p.fallen + seq) < at.j))
+    return;
   const bool drafted = MODE == kDrafted && !at.behind();
   const Scores<XB> x(p.target, at.row, p.vocab);
   Scores<YB> y(drafted ? p.draft : p.target, drafted ? at.first + at.j : at.row, p.vocab);
@@ -654,7 +652,7 @@ __global__ void __launch_bounds__(kRowThreads, kDrawCtas) draw_kernel(const __gr
   const int row = row0 + a;
   if (MODE == kGreedy || at.stands < 0) {
     if (rank == 0 && threadIdx.x == 0) {
-      p.tokens[row] = at.stands < 0 ? -1 : at.best;
+      p.tokens[row] = at.stands < 0 || at.best < 0 || at.best >= p.vocab ? -1 : at.best;
       p.logp[row] = at.stands < 0 ? __int_as_float(0x7fc00000) : at.logp;
     }
     return;

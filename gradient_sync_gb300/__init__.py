@@ -663,7 +663,7 @@ class TensorList:
             self.c[i].data, self.c[i].count, self.c[i].dtype = t.data_ptr(), t.numel(), _dtype_of(t)
             self.counts.append(t.numel())
             # what an element's place depends on, where it is not simply its index
-            self.layouts.append(None if t.is_contiguous() else (tuple(t.shape), t.stride()))
+            self.layouts.append(None if t.is_contiguous() else tuple((a, b) for a, b in zip(t.shape, t.stride()) if a != 1))
         TensorList._made += 1
         self._number = TensorList._made
 
@@ -779,7 +779,7 @@ def ar_adamw_step(params, grads, exp_avgs, exp_avg_sqs, lr: float, step, betas=(
     at = 0
     if isinstance(step, torch.Tensor):
         at, step = _vector(step.reshape(-1), torch.int64, 1, "step"), 0
-    desc = _lib.ArAdamwDesc(lr, betas[0], betas[1], eps, weight_decay, grad_scale, step, at)
+    desc = _lib.ArAdamwDesc(lr, betas[0], betas[1], eps, weight_decay, grad_scale, int(step), at)
     scale = None if clip is None else _vector(clip, torch.float32, 4, "clip")
     c = [None if x is None else x.c for x in (p, g, m, v, w, po, mo, vo, wo)]
     _check(_lib.load().ar_adamw_step(desc, len(p), *c, scale, _stream(stream)), "ar_adamw_step")

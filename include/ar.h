@@ -771,9 +771,9 @@ ar_status ar_grad_workspace(int n_tensors, size_t* bytes);
  *   c = min(1, max_norm / (N + eps)), [2] 1 where c < 1, else 0,
  *   [3] 1 where every element is finite, else 0: c is 0 then.
  * norms [n_tensors] (device, fp32; NULL: not wanted): each tensor's norm.
- * Sums of squares are kept in 64 bits and cover all of fp32's range, whatever
- * the elements' size; c is worked out in 64 bits. A NaN makes N NaN, else an
- * infinity makes it infinite. The order of the sums depends on the list alone:
+ * Sums of squares are kept as pairs of fp32 numbers (about 46 bits) beyond 64
+ * elements and cover all of fp32's range, whatever the elements' size; c is
+ * rounded once. A NaN makes N NaN, else an infinity makes it infinite. The order of the sums depends on the list alone:
  * equal calls give equal bits. */
 ar_status ar_grad_norm(const ar_tensor* grads, int n_tensors, const ar_norm_desc* desc, float* stats, float* norms,
                        void* workspace, void* stream);
@@ -783,7 +783,8 @@ ar_status ar_grad_norm(const ar_tensor* grads, int n_tensors, const ar_norm_desc
  * not finite, so that a step with such gradients adds nothing to moments and
  * weights but their decay. outs: the same counts and types; NULL, or an out
  * at its gradient's own address: in place (where the factor is 1, nothing is
- * written then). Otherwise no out overlaps another one or any gradient. */
+ * written then). Otherwise no out overlaps another one or any gradient. (A
+ * tensor named twice counts twice in ar_grad_norm, and is refused here.) */
 ar_status ar_grad_clip(const ar_tensor* grads, int n_tensors, const ar_tensor* outs, const ar_norm_desc* desc,
                        float* stats, float* norms, void* workspace, void* stream);
 
@@ -828,8 +829,10 @@ ar_status ar_adamw_step(const ar_adamw_desc* desc, int n_tensors, const ar_tenso
  *   one token is drawn behind the standing ones, from w = max(p_a - q_a, 0), or
  *   w = p_a where a = K_s: the first i whose w_0 + .. + w_i passes u * sum(w)
  * (the speculative sampling of Leviathan et al. 2023 and Chen et al. 2023). p and
- * q are softmaxes of logits / temperature. Weights below 2^-125 of the largest
- * count as 0. Sums that decide a draw are kept to 64 bits, their terms to fp32.  */
+ * q are softmaxes of logits / temperature. Their terms are fp32 exponentials, each
+ * off by up to about 2^-20 of itself, and 0 below 2^-126 of the sum; sums beyond 64 terms are pairs
+ * of fp32 numbers, so that a draw's borders are where those terms put them. Results
+ * do not depend on timing. */
 typedef enum {
   AR_VERIFY_SAMPLE = 0, /* as above; without draft logits q_j is 1 at x_j */
   AR_VERIFY_GREEDY = 1  /* draft j stands while it is the first largest logit of its
@@ -864,8 +867,8 @@ ar_status ar_verify_workspace(int64_t n_drafts, int64_t n_seq, int64_t vocab, si
  * the target's rows: the standing drafts, the drawn token, then -1. logp
  * [n_drafts + n_seq] (fp32): the tokens' log-probabilities under the target,
  * 0 where the token is -1: with the tokens as labels, the old_logp of
- * ar_policy_loss. Rows outside every sequence are neither read nor written;
- * offsets outside [0, n_drafts], or descending, are clamped.
+ * ar_policy_loss. Rows outside every sequence are neither read nor written.
+ * Offsets outside [0, n_drafts] are clamped; descending ones give tokens of no meaning, not a fault.
  * A draft outside the vocabulary never stands. A row with a NaN, a +infinity
  * or nothing but -infinity is no distribution: no draft stands there, and the
  * token drawn from it is -1 with log-probability NaN. A residue w without

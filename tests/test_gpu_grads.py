@@ -358,3 +358,30 @@ def test_gradients_of_more_than_2_to_the_31_elements(g):
     assert stats[0].item() == 5.0 and abs(t[-1].item() - 0.6) < 0.6 * 2.0 ** -8 and t[-2].item() == 0.0
     del t
     torch.cuda.empty_cache()
+
+
+def test_coefficients(g):
+    """max_norm / (norm + eps), rounded once: against the quotient in 64 bits, over magnitudes and scales."""
+    for size in (1e-35, 1e-12, 1.0, 3e15, 1e36):
+        for scale in (1.0, 1e-3, -3.0):
+            for kind in ("l2", "max"):
+                t = torch.tensor([3.0, 4.0], device="cuda") * size
+                for max_norm, eps in ((size, 0.0), (0.3 * size, size), (1e3 * size * abs(scale), 0.0), (float("inf"), 0.0)):
+                    got = g.ar_grad_norm([t], max_norm, kind=kind, eps=eps, grad_scale=scale)[0].tolist()
+                    want = G.norm([t.double().cpu().numpy()], max_norm, kind, eps, float(np.float32(scale)))[0]
+                    # the quotient of pairs is off by some 2^-44, its rounding by 2^-24; the norm by its scale's too
+                    assert abs(got[1] - want[1]) <= want[1] * 2.0 ** -23 and abs(got[0] - want[0]) <= want[0] * 2.0 ** -22
+                    assert got[2:] == want[2:].tolist()
+    zero = torch.zeros(5, device="cuda")
+    assert g.ar_grad_norm([zero], 1.0, eps=0.0)[0].tolist() == [0.0, 1.0, 0.0, 1.0]
+    big = torch.full((4,), 3e38, device="cuda")  # the scaled norm leaves fp32's range: finite elements all the same
+    for kind in ("l2", "max"):
+        stats = g.ar_grad_norm([big], 1.0, kind=kind, grad_scale=100.0)[0].tolist()
+        assert stats[0] == float("inf") and stats[1] < 1e-38 and stats[2:] == [1.0, 1.0]
+
+
+def test_a_tensor_named_twice_counts_twice(g):
+    t = torch.tensor([3.0, 4.0], device="cuda")
+    assert g.ar_grad_norm([t, t[:1]], 1.0)[0][0].item() == pytest.approx(34 ** 0.5, rel=2.0 ** -22)
+    with pytest.raises(g.ArError):
+        g.ar_grad_clip([t, t[:1]], 1.0)

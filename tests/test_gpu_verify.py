@@ -263,3 +263,61 @@ def test_logp_is_what_token_logp_gives(g):
     again = g.ar_token_logp(c["target"].cuda(), tokens, temperature=0.8)
     assert (again - logp).abs().max() < 2.0 ** -18  # two fp32 sums of the same row
     assert torch.equal(tokens < 0, logp == 0)
+
+
+@pytest.mark.parametrize("temperature", [1e-6, 1e-3, 0.1, 30.0])
+@pytest.mark.parametrize("shift", [0.0, 1e4, -3e30])
+def test_temperatures_and_far_scores(g, temperature, shift):
+    """Scores over the temperature so large that their product with log2 e has no fraction: the maximum is taken off first.
+    (A shift that fp32 can hold beside the scores' differences; one that cannot leaves equal scores.)"""
+    c = C.make([3, 0, 2], 2011, "f32", seed=17, drafted=False, temperature=max(temperature, 0.1), spread=2.0)
+    c["target"] = (c["target"] + shift).contiguous()
+    C.settle(c, temperature)
+    C.check(C.call(g, c, temperature), C.want(c, temperature))
+    C.check(C.call(g, c, temperature, mode="greedy"), C.want(c, temperature, greedy=True))
+
+
+def test_far_scores_of_both_policies(g):
+    """Distances beyond fp32's range, scores masked with the lowest value, another temperature for the draft."""
+    c = C.make([4, 1], 1500, "f32", seed=23)
+    c["target"] *= 1e30
+    c["draft_logits"][:, 100:] = torch.finfo(torch.float32).min
+    c["target"][:, 700:] = torch.finfo(torch.float32).min
+    c["drafts"][:] = torch.tensor([3, 99, 0, 7, 50])
+    for t, q in ((1.0, 1.0), (1e30, 0.5), (3e29, 1e31)):
+        C.settle(c, t, q)
+        C.check(C.call(g, c, t, draft_temperature=q), C.want(c, t, draft_temperature=q))
+
+
+def test_a_sequence_of_many_drafts(g):
+    """Hundreds of drafts that stand, and one that falls between them."""
+    n, vocab = 700, 64
+    x = torch.zeros(n + 1, vocab)
+    drafts = torch.arange(n) % vocab
+    x[torch.arange(n), drafts] = 12.0
+    u = torch.full((n + 1,), 0.5)
+    for fall in (n, 0, 7, 8, 333, n - 1):
+        v = u.clone()
+        if fall < n:
+            v[fall] = 0.9999  # p = 1 / (1 + 63 e^-12) = 0.99961
+        accepted, tokens, _ = g.ar_verify_drafts(x.cuda(), drafts.cuda(), v.cuda())
+        assert accepted.tolist() == [fall]
+        assert torch.equal(tokens[:fall].cpu(), drafts[:fall]) and (tokens[fall + 1:] == -1).all()
+        # half of the 63 others, or of all 64 equal scores behind the last draft
+        rest = [t for t in range(vocab) if fall == n or t != int(drafts[fall])]
+        assert tokens[fall].item() == rest[len(rest) // 2]
+
+
+def test_many_sequences_of_many_rows_are_skipped_alike(g):
+    """More rows than run at once: whichever are skipped, the result is that of each sequence alone."""
+    rng = np.random.default_rng(5)
+    c = C.make(rng.integers(0, 9, 300).tolist(), 3000, "f32", seed=30, blur=0.7)
+    C.settle(c)
+    expected = C.want(c)
+    for _ in range(5):
+        C.check(C.call(g, c), expected)
+    d = C.make([6] * 260, 2500, "bf16", seed=31, drafted=False, spread=4.0)
+    C.settle(d)
+    C.check(C.call(g, d), C.want(d))
+    d["drafts"][::2] = d["target"].double().argmax(1)[torch.arange(260 * 6) + torch.arange(260).repeat_interleave(6)][::2]
+    C.check(C.call(g, d, mode="greedy"), C.want(d, greedy=True))

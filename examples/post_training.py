@@ -4,12 +4,16 @@ Each rank samples answers from a small policy, scores them, and differentiates
 a loss on its own answers; the gradients of all ranks are summed bucket by
 bucket, and the orthogonalised step updates the weights:
 
+    ar_verify_drafts                  with --drafts: tokens drafted by the reference policy, kept or redrawn
     ar_token_logp                     log-probabilities under the old and the reference policy
     ar_policy_loss / ar_preference_loss  the loss and the gradient of the logits, in one call
     BucketedReducer                   the sum over the ranks' gradients
+    ar_grad_clip                      with --max-norm: the global norm, and the clipped gradients
     ar_muon_step                      momentum, orthogonalisation, weight update
+    ar_adamw_step                     with --adamw: the step of embedding and head
 
     python examples/post_training.py [--objective policy|preference] [--steps 12] [--ranks 4]
+                                     [--drafts 0] [--max-norm X] [--adamw]
 
 The policy is a one-hidden-layer model of the next token given the last one;
 an answer's reward is the share of its tokens below vocab / 2.
@@ -62,24 +66,72 @@ def rollouts(policy, answers, length, vocab, gen):
     return torch.stack(before, 1)[keep], torch.stack(after, 1)[keep], start
 
 
+def drafted_rollouts(policy, draft, answers, length, vocab, gen, drafts):
+    """The same, `drafts` tokens at a time: drafted by the policy `draft`, verified by one pass of `policy`. Also the
+    tokens' log-probabilities under it."""
+    rows = torch.arange(answers, device="cuda")
+    last = torch.randint(0, vocab, (answers,), generator=gen, device="cuda")
+    have = torch.zeros_like(last)
+    room = length + drafts + 1
+    before, after = torch.zeros(2, answers, room, dtype=torch.long, device="cuda")
+    logps = torch.zeros(answers, room, device="cuda")
+    starts = torch.arange(answers + 1, device="cuda") * drafts
+    place = torch.arange(drafts + 1, device="cuda")
+    while int(have.min()) < length:
+        chain, scores = [last], []
+        for _ in range(drafts):
+            scores.append(draft.logits(chain[-1]))
+            chain.append(torch.multinomial(torch.softmax(scores[-1], 1), 1, generator=gen)[:, 0])
+        chain = torch.stack(chain, 1)
+        u = torch.rand(answers * (drafts + 1), generator=gen, device="cuda")
+        kept, tokens, logp = g.ar_verify_drafts(
+            policy.logits(chain.reshape(-1)), chain[:, 1:].contiguous().reshape(-1), u, starts,
+            draft_logits=torch.stack(scores, 1).reshape(answers * drafts, vocab))
+        tokens, logp = tokens.reshape(answers, -1), logp.reshape(answers, -1)
+        at = (have[:, None] + place).clamp(max=room - 1)
+        fits = (place <= kept[:, None]) & (at < length)
+        at = torch.where(fits, at, torch.full_like(at, room - 1))  # (the last place is nobody's)
+        before.scatter_(1, at, torch.where(place == 0, last[:, None], tokens.roll(1, 1)))
+        after.scatter_(1, at, tokens)
+        logps.scatter_(1, at, logp)
+        have = (have + kept + 1).clamp(max=length)
+        last = tokens[rows, kept]
+    lengths = torch.randint(1, length + 1, (answers,), generator=gen, device="cuda")
+    keep = torch.arange(room, device="cuda")[None, :] < lengths[:, None]
+    start = torch.cat([lengths.new_zeros(1), lengths.cumsum(0)])
+    return before[keep], after[keep], start, logps[keep]
+
+
 def sequence_means(values, start):
     total = torch.cat([values.new_zeros(1), values.cumsum(0)])
     return (total[start[1:]] - total[start[:-1]]) / (start[1:] - start[:-1])
 
 
-def train(objective="policy", steps=12, ranks=4, answers=64, length=24, vocab=512, hidden=128, lr=0.2, seed=0):
+def train(objective="policy", steps=12, ranks=4, answers=64, length=24, vocab=512, hidden=128, lr=0.2, seed=0,
+          drafts=0, max_norm=None, adamw=False):
     """Runs `steps` steps; returns the mean reward of the ranks' answers at each."""
-    policy = Policy(vocab, hidden, seed)
-    reference = [w.clone() for w in policy.weights]
-    momenta = [torch.zeros_like(w) for w in policy.weights]
-    plan = g.ar_ortho_plan([tuple(w.shape) for w in policy.weights])
+    policy, frozen = Policy(vocab, hidden, seed), Policy(vocab, hidden, seed)
+    reference = frozen.weights
+    matrices, others = ([1], [0, 2]) if adamw else ([0, 1, 2], [])
+
+    def of(which, tensors):
+        return [tensors[i] for i in which]
+
+    momenta = [torch.zeros_like(w) for w in of(matrices, policy.weights)]
+    moments = [[torch.zeros_like(w) for w in of(others, policy.weights)] for _ in range(2)]
+    updates = 0
+    plan = g.ar_ortho_plan([tuple(w.shape) for w in of(matrices, policy.weights)])
     workspace = torch.empty(g.ar_ortho_workspace(plan), dtype=torch.uint8, device="cuda")
     gen = torch.Generator(device="cuda").manual_seed(seed + 1)
     rewards = []
     for _ in range(steps):
         batches = []
         for _ in range(ranks):
-            before, after, start = rollouts(policy, answers, length, vocab, gen)
+            old = None
+            if drafts:
+                before, after, start, old = drafted_rollouts(policy, frozen, answers, length, vocab, gen, drafts)
+            else:
+                before, after, start = rollouts(policy, answers, length, vocab, gen)
             score = sequence_means((after < vocab // 2).float(), start)
             if objective == "preference":  # the better of two answers first
                 first = (score[0::2] < score[1::2]).long() + torch.arange(0, answers, 2, device="cuda")
@@ -88,8 +140,9 @@ def train(objective="policy", steps=12, ranks=4, answers=64, length=24, vocab=51
                 rows = torch.cat(spans)
                 start = torch.tensor([0] + [len(s) for s in spans], device="cuda").cumsum(0)
                 before, after, score = before[rows], after[rows], score[order]
+                old = None
             with torch.no_grad():
-                old = g.ar_token_logp(policy.logits(before), after)
+                old = g.ar_token_logp(policy.logits(before), after) if old is None else old
                 ref = g.ar_token_logp(policy.logits(before, reference), after)
             which = torch.repeat_interleave(torch.arange(answers, device="cuda"), start[1:] - start[:-1])
             advantage = (score - score.mean()) / (score.std() + 1e-6)
@@ -114,7 +167,13 @@ def train(objective="policy", steps=12, ranks=4, answers=64, length=24, vocab=51
             for t in reversed(range(len(policy.weights))):
                 reducer.ready(t)
             reducer.finish()
-            g.ar_muon_step(plan, policy.weights, grads[0], momenta, lr=lr, workspace=workspace)
+            if max_norm is not None:
+                g.ar_grad_clip(grads[0], max_norm)
+            g.ar_muon_step(plan, of(matrices, policy.weights), of(matrices, grads[0]), momenta, lr=lr,
+                           workspace=workspace)
+            updates += 1
+            if others:
+                g.ar_adamw_step(of(others, policy.weights), of(others, grads[0]), *moments, lr=0.1 * lr, step=updates)
     return rewards
 
 
@@ -123,8 +182,11 @@ def main(argv=None):
     ap.add_argument("--objective", choices=("policy", "preference"), default="policy")
     ap.add_argument("--steps", type=int, default=12)
     ap.add_argument("--ranks", type=int, default=4)
+    ap.add_argument("--drafts", type=int, default=0, help="tokens that the reference policy drafts at a time")
+    ap.add_argument("--max-norm", type=float, help="clip the gradients' global norm")
+    ap.add_argument("--adamw", action="store_true", help="embedding and head take AdamW steps")
     a = ap.parse_args(argv)
-    for i, r in enumerate(train(a.objective, a.steps, a.ranks)):
+    for i, r in enumerate(train(a.objective, a.steps, a.ranks, drafts=a.drafts, max_norm=a.max_norm, adamw=a.adamw)):
         print(f"step {i}: mean reward {r:.3f}")
 
 

@@ -80,18 +80,29 @@ __device__ __forceinline__ Value join(Value a, Value b) {
 }
 __device__ __forceinline__ Value nothing() { return {kSmall, {0.0f, 0.0f}}; }
 
+// A magnitude by its bits.
+__device__ __forceinline__ Value magnitude(uint32_t bits) {
+  if (bits >= 0x7f800000u) return {bits > 0x7f800000u ? kNan : kInf, {0.0f, 0.0f}};
+  return {kMid, {__uint_as_float(bits), 0.0f}};
+}
+
 template <bool MAX>
 __device__ __forceinline__ Value warp_join(Value a) {
-  // (the bands mostly agree)
+  if (MAX) {
+    const uint32_t top = __reduce_max_sync(~0u, a.band == kMid ? __float_as_uint(a.v.hi) : a.band < kMid ? 0u : a.band == kInf ? 0x7f800000u : 0x7fc00000u);
+    return magnitude(top);
+  }
+  // (the bands mostly agree, but for lanes that have nothing)
   const int top = __reduce_max_sync(~0u, a.band);
-  if (!MAX && __reduce_min_sync(~0u, a.band) == top) {
+  if (a.v.hi == 0.0f && a.band < kInf) a.band = top;
+  if (__reduce_min_sync(~0u, a.band) == top) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a.v = add(a.v, {__shfl_xor_sync(~0u, a.v.hi, o), __shfl_xor_sync(~0u, a.v.lo, o)});
     return a;
   }
 #pragma unroll 1
   for (int o = 16; o > 0; o >>= 1)
-    a = join<MAX>(a, {__shfl_xor_sync(~0u, a.band, o), {__shfl_xor_sync(~0u, a.v.hi, o), __shfl_xor_sync(~0u, a.v.lo, o)}});
+    a = sum_of(a, {__shfl_xor_sync(~0u, a.band, o), {__shfl_xor_sync(~0u, a.v.hi, o), __shfl_xor_sync(~0u, a.v.lo, o)}});
   return a;
 }
 
@@ -160,10 +171,6 @@ __device__ __forceinline__ uint32_t largest(const uint4 (&r)[kLoads], uint32_t t
     }
   }
   return top;
-}
-__device__ __forceinline__ Value magnitude(uint32_t bits) {
-  if (bits >= 0x7f800000u) return {bits > 0x7f800000u ? kNan : kInf, {0.0f, 0.0f}};
-  return {kMid, {__uint_as_float(bits), 0.0f}};
 }
 
 __device__ __forceinline__ void cluster_barrier() {
@@ -345,24 +352,42 @@ __device__ __forceinline__ void write_stats(const GradJob& job, Value total) {
   job.stats[3] = finite ? 1.0f : 0.0f;
 }
 
-// The tensors' norms from the sums in `part`, each of `per` granules, by one CTA; returns the sum over all tensors (thread 0).
+// The tensors' norms from the sums in `part`, each of `per` granules, by one CTA; returns the sum over all tensors
+// (thread 0). A lane a tensor, but for tensors of many sums.
 template <bool MAX, class Table>
-__device__ __forceinline__ Value finish_tensors(const Table& t, int64_t per, const GradJob& job, const Value* part, Value* sums) {
+__device__ __forceinline__ Value finish_tensors(const Table& table, int64_t per, const GradJob& job, const Value* part, Value* sums) {
+  constexpr int kFew = 4;
+  const Table* t = &table;
+  asm("" : "+l"(t));  // (ordinary loads: lanes read entries of their own)
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = int(blockDim.x) / 32;
   const float scale = fabsf(job.grad_scale);
   Value mine = nothing();
 #pragma unroll 1
-  for (int i = warp; i < t.n; i += warps) {
-    const int64_t first = t.e[i].first, end = first + (t.e[i].count > 1 ? Span(t.e[i].in, t.e[i].count).granules : 0);
-    Value v = nothing();
-    if (end > first) {
-      const int last = warp_of(end - 1, per) + i;
-      for (int j = warp_of(first, per) + i + lane; j <= last; j += 32) v = join<MAX>(v, part[j]);
-      v = warp_join<MAX>(v);
+  for (int i0 = 0; i0 < t->n; i0 += 32 * warps) {
+    const int i = i0 + lane * warps + warp;  // (tensors beside one another are often alike: to different warps)
+    int from = 0, to = 0;  // of the tensor's sums
+    if (i < t->n && t->e[i].count > 1) {
+      const int64_t first = t->e[i].first;
+      from = warp_of(first, per) + i;
+      to = warp_of(first + Span(t->e[i].in, t->e[i].count).granules - 1, per) + i + 1;
     }
-    if (lane == 0 && job.norms != nullptr) job.norms[i] = norm_of<MAX>(v, scale);
+    Value v = nothing();
+    if (to - from <= kFew)
+      for (int j = from; j < to; ++j) v = join<MAX>(v, part[j]);
+    unsigned many = __ballot_sync(~0u, to - from > kFew);
+    while (many != 0) {
+      const int owner = __ffs(int(many)) - 1;
+      many &= many - 1;
+      const int last = __shfl_sync(~0u, to, owner);
+      Value w = nothing();
+      for (int j = __shfl_sync(~0u, from, owner) + lane; j < last; j += 32) w = join<MAX>(w, part[j]);
+      w = warp_join<MAX>(w);
+      if (lane == owner) v = w;
+    }
+    if (i < t->n && job.norms != nullptr) job.norms[i] = norm_of<MAX>(v, scale);
     mine = join<MAX>(mine, v);
   }
+  mine = warp_join<MAX>(mine);
   if (lane == 0) sums[warp] = mine;
   __syncthreads();
   if (warp == 0) mine = warp_join<MAX>(lane < warps ? sums[lane] : nothing());

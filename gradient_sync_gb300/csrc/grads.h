@@ -29,6 +29,7 @@ struct GradTable {
   int n;
   int64_t granules;  // of all entries
   int64_t per;       // of them a warp
+  int64_t keep;      // of those, the last ones that stay in the L2
   GradEntry e[CAP];
 };
 

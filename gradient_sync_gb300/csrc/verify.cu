@@ -35,7 +35,6 @@ namespace {
 constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 constexpr int kMaxRanks = 8;  // CTAs of a cluster of draw_kernel
 constexpr int kDrawCtas = 3;  // CTAs of draw_kernel an SM
-constexpr int kRounds = 2;    // of a warp, loaded together
 
 enum Mode : int { kLookup = 0, kDrafted = 1, kGreedy = 2 };  // drafts without distributions, with them, greedy
 
@@ -552,6 +551,7 @@ struct Draw {
   }
   // The weight of a lane's groups.
   __device__ __forceinline__ Two total(const Piece& p, int lane) const {
+    constexpr int kRounds = 4 / (X::kVecs > Y::kVecs ? X::kVecs : Y::kVecs);  // loaded together
     Two sum = {0.0f, 0.0f};
 #pragma unroll 1
     for (int g = p.lo + lane; g < p.hi; g += kRounds * 32) {

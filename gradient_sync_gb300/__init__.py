@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import itertools
 
 from . import _lib
 
@@ -664,10 +665,9 @@ class TensorList:
             self.counts.append(t.numel())
             # what an element's place depends on, where it is not simply its index
             self.layouts.append(None if t.is_contiguous() else tuple((a, b) for a, b in zip(t.shape, t.stride()) if a != 1))
-        TensorList._made += 1
-        self._number = TensorList._made
+        self._number = next(TensorList._numbers)
 
-    _made = 0
+    _numbers = itertools.count()
 
     def __len__(self):
         return len(self.tensors)
@@ -699,6 +699,8 @@ def _tensors(x, what: str, like: TensorList | None = None):
         if not same:
             raise ValueError(f"{what}: as many tensors wanted, with the same numbers of elements in the same order")
     elif given is x:
+        if len(like._alike) >= 64:
+            like._alike.clear()
         like._alike.add(x._number)
     return x
 

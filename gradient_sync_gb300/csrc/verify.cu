@@ -1,4 +1,5 @@
-// Verification of drafted tokens against the target's probabilities.
+// Verification of drafted tokens against the target's probabilities (speculative
+// sampling: Leviathan et al. 2023, Chen et al. 2023).
 //
 // For a row of target logits x, p_i = w_i / Z with
 //   w_i = 2^(x_i k - c), k = log2(e) / temperature, Z = sum w_i,
@@ -8,21 +9,28 @@
 // where positive (v, Z' the draft's): the first index whose running sum passes u
 // times the total.
 //
-//  sums_kernel  Z and Z' of every row, in parts of a row, a CTA each: one pass, no CTA
-//               waits for another. Where a call has more rows than run at once, they are visited
-//               by their place in their sequence; the last CTA of a row to finish
-//               decides about its draft, and rows behind one that fell are not
-//               read any more. Bound by HBM for many rows.
+//  sums_kernel  Z and Z' of every row, in parts of a row, a CTA each: one pass, no CTA waits
+//               for another. Where a call has more rows than run at once, they are visited by
+//               their place in their sequence; the last CTA of a row to finish decides about
+//               its draft, and rows behind one that fell are not read any more.
 //  draw_kernel  a cluster of up to 8 CTAs a sequence: joins the parts, finds the first draft
-//               that falls, draws from that row alone (read two or three times, from
-//               the L2 where it is still there), writes the tokens.
-// Results do not depend on which rows were skipped: none before the first fall is.
+//               that falls, draws from that row alone (read two or three times, from the L2
+//               where it is still there), writes the tokens.
+// Results do not depend on which rows were skipped: none up to the first fall is.
 //
-// A draw has to put u on the right side of borders that may lie anywhere, also
-// between tokens of 1e-6 and less. Its terms are fp32 exponentials, as in the
-// sums: each is off by some 2^-22 of itself, and by half a last place of its
-// exponent x k - c. Sums beyond 64 terms, and borders, are pairs of fp32 numbers (one fp64 operation
-// takes a warp some 200 cycles here); the draft's weight is subtracted in one fused operation.
+// A draw has to put u on the right side of borders that may lie anywhere, also between
+// tokens of 1e-6 and less. Its terms are fp32 exponentials, as in the sums: each is off by some
+// 2^-22 of itself, and by half a last place of its exponent x k - c. Sums beyond 64 terms, and
+// borders, are pairs of fp32 numbers; the draft's weight is subtracted in one fused operation.
+//
+// What bounds it, one GB300: 64 sequences of 8 drafts x 131072 bf16, a third of the drafts
+// standing: sums 37 us for the 155 MB of 285 that are not skipped, 51 us (5.5 TB/s, 0.81 of the
+// copy bandwidth) where all are read; the draw 13 us, latency. One sequence of 4 drafts x 32000
+// fp32: 10 us in a graph of calls, two kernels of 3 and 6 us, latency.
+// Taken apart and left: rows held in shared memory by clusters that decide and draw
+// themselves (99 us for the batch: barriers of a cluster take 0.6 us each, five a row, and
+// rows that fall in vain are drawn from); fp64 for borders (an operation takes a warp some 200
+// cycles: 16 us for the one sequence); weights to fp32's last place (draws 46 us for 27).
 #include "verify.h"
 
 #include <algorithm>
@@ -95,7 +103,9 @@ __device__ __forceinline__ Two times(Two a, float u) {
   const float p = a.hi * u;
   return two_sum(p, fmaf(a.hi, u, -p) + a.lo * u);
 }
-__device__ __forceinline__ Two shuffled(Two v, int from) { return {__shfl_sync(~0u, v.hi, from), __shfl_sync(~0u, v.lo, from)}; }
+__device__ __forceinline__ Two shuffled(Two v, int from) {
+  return {__shfl_sync(~0u, v.hi, from), __shfl_sync(~0u, v.lo, from)};
+}
 __device__ __forceinline__ Two warp_sum(Two v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = add(v, {__shfl_xor_sync(~0u, v.hi, o), __shfl_xor_sync(~0u, v.lo, o)});
@@ -620,13 +630,13 @@ __global__ void __launch_bounds__(kRowThreads, kDrawCtas) draw_kernel(const __gr
   const int ranks = 1 << p.rank_bits, rank = int(blockIdx.x) & (ranks - 1), s = int(blockIdx.x >> p.rank_bits);
   const int first = start_of(p, s), count = max(start_of(p, s + 1) - first, 0), row0 = first + s;
   // a warp a draft, eight at a time, until one falls (there is none in the last row); where rows may have been skipped
-  // it is the one that they were skipped for
-  const int stop = p.fallen != nullptr ? __ldcg(p.fallen + s) : -1;
+  // it is the one that they were skipped for, and those behind it have no sums
+  const int stop = p.fallen != nullptr ? __ldcg(p.fallen + s) : INT32_MAX;
   int a;
   for (int j0 = 0;; j0 += kRowWarps) {
     const int j = j0 + warp;
     Verdict v = {0};
-    if (j <= count) {
+    if (j <= min(count, stop)) {
       v = decide<XB, YB, MODE, true>(p, {row0 + j, s, first, count, j}, lane);
       if (j == stop) v.stands = min(v.stands, 0);
       if (lane == 0) sh.verdicts[warp] = v;

@@ -773,8 +773,9 @@ ar_status ar_grad_workspace(int n_tensors, size_t* bytes);
  * norms [n_tensors] (device, fp32; NULL: not wanted): each tensor's norm.
  * Sums of squares are kept as pairs of fp32 numbers (about 46 bits) beyond 64
  * elements and cover all of fp32's range, whatever the elements' size; c is
- * rounded once. A NaN makes N NaN, else an infinity makes it infinite. The order of the sums depends on the list alone:
- * equal calls give equal bits. */
+ * rounded once. A NaN makes N NaN, else an infinity makes it infinite. The
+ * order of the sums depends on the list (its sizes and alignments) and the
+ * device alone: equal calls give equal bits. */
 ar_status ar_grad_norm(const ar_tensor* grads, int n_tensors, const ar_norm_desc* desc, float* stats, float* norms,
                        void* workspace, void* stream);
 
@@ -803,13 +804,14 @@ typedef struct {
  * clip (device): the stats of ar_grad_norm or ar_grad_clip with the same
  * grad_scale (after ar_grad_clip the outs are scaled already: NULL then);
  * where it says that an element was not finite, the step is skipped: every
- * output is its input.
+ * output is its input (in place nothing is written; elsewhere, a parameter
+ * beside a master is that one, rounded).
  * params fp32 or bf16, each as it is; moments fp32. masters (NULL, or a list in
  * which a tensor without a master has data NULL): fp32 weights W that are
  * updated in the parameters' place; the parameter itself is not read then, and
- * written with W' rounded once. The four *_out lists may be NULL, or name the inputs
- * themselves: in place. Otherwise no two arrays of the call overlap, but for
- * gradients with one another. masters_out needs masters. */
+ * written with W' rounded once. The four *_out lists may be NULL, or name the
+ * inputs themselves: in place. Otherwise no two arrays of the call overlap, but
+ * for gradients with one another. masters_out needs masters. */
 ar_status ar_adamw_step(const ar_adamw_desc* desc, int n_tensors, const ar_tensor* params, const ar_tensor* grads,
                         const ar_tensor* exp_avgs, const ar_tensor* exp_avg_sqs, const ar_tensor* masters,
                         const ar_tensor* params_out, const ar_tensor* exp_avgs_out,
@@ -829,10 +831,10 @@ ar_status ar_adamw_step(const ar_adamw_desc* desc, int n_tensors, const ar_tenso
  *   one token is drawn behind the standing ones, from w = max(p_a - q_a, 0), or
  *   w = p_a where a = K_s: the first i whose w_0 + .. + w_i passes u * sum(w)
  * (the speculative sampling of Leviathan et al. 2023 and Chen et al. 2023). p and
- * q are softmaxes of logits / temperature. Their terms are fp32 exponentials, each
- * off by up to about 2^-20 of itself, and 0 below 2^-126 of the sum; sums beyond 64 terms are pairs
- * of fp32 numbers, so that a draw's borders are where those terms put them. Results
- * do not depend on timing. */
+ * q are softmaxes of logits / temperature. Their terms are fp32 exponentials,
+ * each off by up to about 2^-20 of itself, and 0 below 2^-126 of the sum; sums
+ * beyond 64 terms are pairs of fp32 numbers, so that a draw's borders are where
+ * those terms put them. Results do not depend on timing.                       */
 typedef enum {
   AR_VERIFY_SAMPLE = 0, /* as above; without draft logits q_j is 1 at x_j */
   AR_VERIFY_GREEDY = 1  /* draft j stands while it is the first largest logit of its
@@ -868,7 +870,8 @@ ar_status ar_verify_workspace(int64_t n_drafts, int64_t n_seq, int64_t vocab, si
  * [n_drafts + n_seq] (fp32): the tokens' log-probabilities under the target,
  * 0 where the token is -1: with the tokens as labels, the old_logp of
  * ar_policy_loss. Rows outside every sequence are neither read nor written.
- * Offsets outside [0, n_drafts] are clamped; descending ones give tokens of no meaning, not a fault.
+ * Offsets outside [0, n_drafts] are clamped; descending ones give tokens of no
+ * meaning, not a fault.
  * A draft outside the vocabulary never stands. A row with a NaN, a +infinity
  * or nothing but -infinity is no distribution: no draft stands there, and the
  * token drawn from it is -1 with log-probability NaN. A residue w without

@@ -665,6 +665,7 @@ class TensorList:
             self.counts.append(t.numel())
             # what an element's place depends on, where it is not simply its index
             self.layouts.append(None if t.is_contiguous() else tuple((a, b) for a, b in zip(t.shape, t.stride()) if a != 1))
+        self.whole = None not in self.counts
         self._number = next(TensorList._numbers)
 
     _numbers = itertools.count()
@@ -684,7 +685,7 @@ def _tensors(x, what: str, like: TensorList | None = None):
         except ValueError as e:
             raise ValueError(f"{what}{e}") from None
     if like is None:
-        if any(v is None for v in x.counts):
+        if not x.whole:
             raise ValueError(f"{what}: None in place of a tensor")
         return x
     if x._number in like._alike:
@@ -707,10 +708,11 @@ def _tensors(x, what: str, like: TensorList | None = None):
 
 def _here(device):
     """Refuses tensors of another device than the one that the call would run on."""
-    import torch
+    if device.type == "cuda":
+        import torch
 
-    if torch.cuda.is_initialized() and device.index != torch._C._cuda_getDevice():
-        raise ValueError(f"tensors on {device}, but the current device is cuda:{torch._C._cuda_getDevice()}")
+        if device.index != torch._C._cuda_getDevice():
+            raise ValueError(f"tensors on {device}, but the current device is cuda:{torch._C._cuda_getDevice()}")
 
 
 @functools.lru_cache(maxsize=1024)

@@ -509,7 +509,7 @@ __device__ __forceinline__ void scale_stretch(const Table& t, int64_t lo, int64_
 // The scaled gradients, stretch by stretch as the norm read them. (A batch of loads a warp, CTAs from the end of the
 // list on, took 136 us in place of 129 for the clipping of 67 M fp32 elements.)
 template <int CAP>
-__global__ void __launch_bounds__(kNormThreads) scale_kernel(const __grid_constant__ GradTable<CAP> t, GradJob job) {
+__global__ void __launch_bounds__(kNormThreads, 2) scale_kernel(const __grid_constant__ GradTable<CAP> t, GradJob job) {
   grid_dependency_wait();
   grid_dependents_launch();
   const int64_t w = int64_t(blockIdx.x) * (kNormThreads / 32) + threadIdx.x / 32;

@@ -385,3 +385,45 @@ def test_a_tensor_named_twice_counts_twice(g):
     assert g.ar_grad_norm([t, t[:1]], 1.0)[0][0].item() == pytest.approx(34 ** 0.5, rel=2.0 ** -22)
     with pytest.raises(g.ArError):
         g.ar_grad_clip([t, t[:1]], 1.0)
+
+
+def test_workspaces_that_hold_anything(g):
+    lists = {name: tensors(LISTS[name], "mixed", shift=1) for name in LISTS}
+    want = {name: [x.clone() for x in g.ar_grad_norm(ts, 1.0)] for name, ts in lists.items()}
+    ws = torch.empty(g.ar_grad_workspace(1) // 4, device="cuda")
+    for fill in (float("nan"), float("inf"), 0.0, None):
+        for name, ts in lists.items():
+            if fill is not None:
+                ws.fill_(fill)
+            for a, b in zip(g.ar_grad_norm(ts, 1.0, workspace=ws), want[name]):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n", [40, 41, 48, 49, 360, 361, 768, 769])
+def test_lists_as_long_as_the_tables(g, n):
+    """Lists at the lengths where launches change, with empty tensors among them: every tensor is seen once."""
+    ts = tensors([(0,) if i % 5 == 3 else (100 + 7 * (i % 11),) for i in range(n)], "bf16", seed=n)
+    stats, norms, outs = g.ar_grad_clip(ts, 0.5, outs=[torch.zeros_like(t) for t in ts])
+    want, each = G.norm(wide(ts), 0.5)
+    assert np.allclose(norms.cpu().numpy(), each, rtol=NORM, atol=0)
+    assert np.allclose(stats.cpu().numpy(), want, rtol=2 * NORM, atol=0)
+    for t, o in zip(ts, outs):
+        assert torch.equal(o, (t.float() * stats[1]).to(t.dtype))
+    ps, ms, vs = ([torch.ones_like(t, dtype=torch.float32) for t in ts] for _ in range(3))
+    g.ar_adamw_step(ps, ts, ms, vs, 0.1, 1, betas=(0.5, 0.5))
+    for p, t, m in zip(ps, ts, ms):
+        # (a gradient of -1 leaves the first moment, and so the weight, where it was; any other bf16 moves it by 1e-4 or more)
+        assert torch.equal(m, 0.5 + 0.5 * t.float()) and torch.equal(p != 1.0, m != 0.0)
+
+
+def test_short_lists_of_every_size(g):
+    """Around the sizes where a cluster grows, and where one launch becomes three."""
+    for granules in (1, 31, 32, 33, 2047, 2049, 8191, 8193, 16385, 130000, 131072, 131073, 140000):
+        t = torch.randn(granules * 8, device="cuda").bfloat16()
+        for cut in (0, 3):
+            x = t[cut:t.numel() - cut]
+            out = torch.empty(x.numel() + 8, dtype=torch.bfloat16, device="cuda")[cut:cut + x.numel()]
+            stats, norms, _ = g.ar_grad_clip([x], 1e-3, outs=[out])
+            want = torch.linalg.vector_norm(x.double()).item()
+            assert abs(stats[0].item() - want) <= want * NORM and torch.equal(norms, stats[:1])
+            assert torch.equal(out, (x.float() * stats[1]).bfloat16())

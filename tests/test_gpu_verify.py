@@ -321,3 +321,58 @@ def test_many_sequences_of_many_rows_are_skipped_alike(g):
     C.check(C.call(g, d), C.want(d))
     d["drafts"][::2] = d["target"].double().argmax(1)[torch.arange(260 * 6) + torch.arange(260).repeat_interleave(6)][::2]
     C.check(C.call(g, d, mode="greedy"), C.want(d, greedy=True))
+
+
+def test_workspaces_that_hold_anything(g):
+    """One workspace for calls of many shapes, one after the other, filled with ones, zeros, infinities or what the last
+    call left: the results do not depend on it."""
+    cases = []
+    for i, (counts, vocab, dtype, drafted) in enumerate([([3, 0, 2], 5000, "f32", True), ([5] * 150, 9000, "bf16", True),
+                                                         ([2, 9], 300, "bf16", False), ([0], 40000, "f32", False),
+                                                         ([4] * 300, 2000, "f32", False)]):
+        c = C.make(counts, vocab, dtype, seed=40 + i, drafted=drafted)
+        C.settle(c)
+        cases.append((c, C.want(c)))
+    room = max(g.ar_verify_workspace(len(c["drafts"]), len(c["draft_start"]) - 1, c["target"].shape[1]) for c, _ in cases)
+    ws = torch.empty(room // 4, device="cuda")
+    for fill in (float("nan"), 0.0, float("inf"), -float("inf"), 1.0, None, None):
+        for c, expected in cases:
+            if fill is not None:
+                ws.fill_(fill)
+            C.check(C.call(g, c, workspace=ws), expected, fill)
+
+
+def test_calls_side_by_side(g):
+    """Calls on streams of their own, each with its workspace, give what they give alone."""
+    cases = []
+    for i, counts in enumerate([[4] * 200, [6, 0, 1], [1] * 90]):
+        c = C.make(counts, 4001, "bf16", seed=50 + i)
+        C.settle(c)
+        cases.append(({k: v.cuda() for k, v in c.items()}, C.want(c)))
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[g.ar_verify_drafts(**d, stream=s) for (d, _), s in zip(cases, streams)] for _ in range(8)]
+    torch.cuda.synchronize()
+    for round_ in got:
+        for out, (_, expected) in zip(round_, cases):
+            C.check(out, expected)
+
+
+def test_two_graphs_of_one_workspace_replayed_in_turn(g):
+    c, d = C.make([3, 1, 4], 3000, seed=60), C.make([2, 2], 7001, "bf16", seed=61, drafted=False)
+    room = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for x in (c, d):
+        C.settle(x)
+        inputs = {k: None if v is None else v.cuda() for k, v in x.items()}
+        g.ar_verify_drafts(**inputs, workspace=room)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = g.ar_verify_drafts(**inputs, workspace=room)
+        graphs.append((graph, out, C.want(x), inputs))
+    for _ in range(3):
+        for graph, out, expected, _ in graphs:
+            for t in out:
+                t.fill_(7)
+            graph.replay()
+            C.check(out, expected)

@@ -42,7 +42,6 @@ namespace {
 
 constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 constexpr int kMaxRanks = 8;  // CTAs of a cluster of draw_kernel
-constexpr int kDrawCtas = 3;  // CTAs of draw_kernel an SM
 
 enum Mode : int { kLookup = 0, kDrafted = 1, kGreedy = 2 };  // drafts without distributions, with them, greedy
 
@@ -619,8 +618,9 @@ struct Shared {
   Two parts[kRowWarps];
 };
 
-template <bool XB, bool YB, int MODE>
-__global__ void __launch_bounds__(kRowThreads, kDrawCtas) draw_kernel(const __grid_constant__ VerifyParams p) {
+// CTAS: of them an SM.
+template <bool XB, bool YB, int MODE, int CTAS>
+__global__ void __launch_bounds__(kRowThreads, CTAS) draw_kernel(const __grid_constant__ VerifyParams p) {
   using X = Scores<XB>;
   using Y = Scores<YB>;
   grid_dependency_wait();
@@ -820,16 +820,24 @@ Kernel sums_of(const VerifyParams& p) {
   if (x) return y ? sums_kernel<true, true, kDrafted> : sums_kernel<true, false, kDrafted>;
   return y ? sums_kernel<false, true, kDrafted> : sums_kernel<false, false, kDrafted>;
 }
+template <int CTAS>
 Kernel draw_of(const VerifyParams& p) {
   const bool x = p.target.bf16 != 0, y = p.draft.bf16 != 0;
-  if (p.greedy) return x ? draw_kernel<true, true, kGreedy> : draw_kernel<false, false, kGreedy>;
-  if (p.draft.data == nullptr) return x ? draw_kernel<true, true, kLookup> : draw_kernel<false, false, kLookup>;
-  if (x) return y ? draw_kernel<true, true, kDrafted> : draw_kernel<true, false, kDrafted>;
-  return y ? draw_kernel<false, true, kDrafted> : draw_kernel<false, false, kDrafted>;
+  if (p.draft.data == nullptr) return x ? draw_kernel<true, true, kLookup, CTAS> : draw_kernel<false, false, kLookup, CTAS>;
+  if (x) return y ? draw_kernel<true, true, kDrafted, CTAS> : draw_kernel<true, false, kDrafted, CTAS>;
+  return y ? draw_kernel<false, true, kDrafted, CTAS> : draw_kernel<false, false, kDrafted, CTAS>;
 }
 
-constexpr int64_t kPart = 32768, kLeastPart = 4096;  // elements that a CTA of sums_kernel takes (of one row or two)
-constexpr int64_t kLeastDraw = 2048;                 // ... of draw_kernel: a round of all its warps
+// Elements that a CTA of sums_kernel takes, of one row or two. Measured, 16384 of each of two rows against 8192 and
+// 32768: 64 x 8 drafts x 131072 bf16 54.5, 58.2 and 58.4 us. At least 4096 where there are few rows, against 8192: one
+// sequence of 4 drafts x 32000 fp32 10.4 and 12.2 us, 8 of 8 drafts 12.0 and 13.4.
+constexpr int64_t kPart = 32768, kLeastPart = 4096;
+// ... of draw_kernel: a round of all its warps. (Clusters of 8 against 4: 4 x 4 drafts x 131072 bf16 13.5 and 16.9 us.)
+constexpr int64_t kLeastDraw = 2048;
+// Calls with less to read do not skip rows, which takes about 3 us: flags cleared by a launch, rows decided about.
+// Measured, skipping against not: 64 x 8 drafts x 131072 bf16 (285 MB) 50 and 64 us, 256 x 4 x 32000 (147 MB) 41.8 and
+// 43.3, 16 x 4 x 131072 (38 MB) 20.1 and 18.2, 200 x 3 looked-up drafts x 5000 (8 MB) 16.6 and 13.3.
+constexpr int64_t kSkipBytes = int64_t(96) << 20;
 
 }  // namespace
 
@@ -843,22 +851,33 @@ cudaError_t launch_verify(const VerifyParams& q, cudaStream_t stream) {
   while (p.part_bits < kVerifyPartBits && (rows << p.part_bits) < 2 * sms && (p.vocab >> p.part_bits) >= 2 * kLeastPart) ++p.part_bits;
   while (p.part_bits > 0 && (rows << p.part_bits) > 0x7fffffff) --p.part_bits;
   p.parts = 1 << p.part_bits;
-  // more rows than run at once: by their place in their sequence, and not behind a draft that fell
-  const bool waves = rows * p.parts > 4 * sms && p.n_drafts > 0 && rows / p.n_seq < 60000;
+  // more rows than run at once, and enough of them: by their place in their sequence, and not behind a draft that fell
+  const int64_t bytes = p.vocab * (rows * (p.target.bf16 ? 2 : 4) + (p.draft.data == nullptr ? 0 : p.n_drafts * (p.draft.bf16 ? 2 : 4)));
+  const bool waves = rows * p.parts > 4 * sms && bytes > kSkipBytes && p.n_drafts > 0 && rows / p.n_seq < 60000;
   p.pitch = waves ? int((rows + p.n_seq - 1) / p.n_seq) : 1;
   if (!waves) p.fallen = nullptr;
-  // a cluster a sequence, all at once where they fit
-  p.rank_bits = 0;
-  if (!p.greedy)
-    while ((1 << p.rank_bits) < kMaxRanks && (p.n_seq << p.rank_bits) * 2 <= kDrawCtas * sms && (p.vocab >> p.rank_bits) >= 2 * kLeastDraw)
-      ++p.rank_bits;
+  // a cluster a sequence, all at once where they fit: three CTAs an SM, or, with fewer registers, four where that makes
+  // the clusters larger (64 x 8 drafts x 131072 bf16 48.0 us with four, 50.8 with three; where it does not, 16 x 8 x 32000
+  // 14.5 and 13.6)
+  const auto rank_bits = [&](int64_t ctas) {
+    int bits = 0;
+    while ((1 << bits) < kMaxRanks && (p.n_seq << bits) * 2 <= ctas * sms && (p.vocab >> bits) >= 2 * kLeastDraw) ++bits;
+    return bits;
+  };
+  p.rank_bits = p.greedy ? 0 : rank_bits(3);
+  Kernel draw = p.target.bf16 ? draw_kernel<true, true, kGreedy, 4> : draw_kernel<false, false, kGreedy, 4>;
+  if (!p.greedy) {
+    const bool more = rank_bits(4) > p.rank_bits;
+    if (more) p.rank_bits = rank_bits(4);
+    draw = more ? draw_of<4>(p) : draw_of<3>(p);
+  }
   cudaError_t err = cudaSuccess;
   if (err == cudaSuccess && waves) err = launch_after(clear_kernel, p, dim3(unsigned((rows + 255) / 256)), 1, stream);
   const int64_t across = (rows + p.pitch - 1) / p.pitch;
   if (err == cudaSuccess)
     err = launch_after(sums_of(p), p, dim3(unsigned(across << p.part_bits), unsigned(p.pitch)), 1, stream);
   if (err == cudaSuccess)
-    err = launch_after(draw_of(p), p, dim3(unsigned(p.n_seq << p.rank_bits)), 1 << p.rank_bits, stream);
+    err = launch_after(draw, p, dim3(unsigned(p.n_seq << p.rank_bits)), 1 << p.rank_bits, stream);
   return err;
 }
 

@@ -24,7 +24,7 @@ CUDA_SOURCES = ["fused.cu", "fused_tma.cu", "step.cu", "pack.cu", "noalloc.cu", 
                 "ortho_steps1.cu", "ortho_steps2.cu", "grads.cu", "verify.cu"]
 CXX_SOURCES = ["api.cpp", "loss.cpp", "ortho.cpp", "grads.cpp", "verify.cpp"]
 HEADERS = ["internal.h", "common.cuh", "bulk.cuh", "loss.h", "ortho.h", "ortho_table.cuh",
-           "ortho_steps.cuh", "grads.h", "verify.h"]
+           "ortho_steps.cuh", "grads.h", "verify.h", "pairs.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # Per-file nvcc flags (none at present).

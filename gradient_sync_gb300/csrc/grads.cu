@@ -24,6 +24,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "pairs.cuh"
 
 namespace ar {
 namespace {
@@ -59,20 +60,6 @@ __device__ __forceinline__ uint4 load16(const char* p, uint64_t policy) {
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                : "l"(p), "l"(policy));
   return r;
-}
-
-// A sum as two fp32 numbers.
-struct Two {
-  float hi, lo;
-};
-__device__ __forceinline__ Two two_sum(float a, float b) {
-  const float s = a + b, z = s - a;
-  return {s, (a - (s - z)) + (b - z)};
-}
-__device__ __forceinline__ Two add(Two a, Two b) {
-  Two s = two_sum(a.hi, b.hi);
-  const float lo = s.lo + (a.lo + b.lo), hi = s.hi + lo;
-  return {hi, lo - (hi - s.hi)};
 }
 
 // A sum of squares v * 2^(176 band), or, of maxima, a magnitude (band 0). An

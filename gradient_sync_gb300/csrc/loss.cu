@@ -44,6 +44,7 @@
 
 #include "bulk.cuh"
 #include "common.cuh"
+#include "pairs.cuh"
 
 namespace ar {
 namespace {
@@ -54,41 +55,6 @@ namespace {
 // 8 x 16384 fp32 long; longer ones are read twice.
 constexpr int kVecs = 8;
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Two fp32 operations an instruction.
-struct Pair {
-  uint64_t v;
-};
-__device__ __forceinline__ Pair pair_of(float lo, float hi) {
-  Pair r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 floats_of(Pair a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-  return r;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  Pair r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ Pair add2(Pair a, Pair b) {
-  Pair r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-  Pair r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
 // The pairs of a vector: 4 of bf16, 2 of fp32.
 template <bool BF16>
 __device__ __forceinline__ Pair pair_at(const uint4& r, int i) {
@@ -144,15 +110,6 @@ __device__ __forceinline__ Lse lse_warp_at_max(Lse v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
   return {c, s};
-}
-
-// A sum of two floats, for the few operations of a row that need more than 24 bits.
-struct Two {
-  float hi, lo;
-};
-__device__ __forceinline__ Two two_sum(float a, float b) {
-  const float s = a + b, t = s - a;
-  return {s, (a - (s - t)) + (b - t)};
 }
 
 // lp = (x_y k - c - log2 s) ln 2. What cancels is subtracted exactly.

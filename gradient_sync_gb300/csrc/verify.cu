@@ -36,6 +36,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "pairs.cuh"
 
 namespace ar {
 namespace {
@@ -45,55 +46,11 @@ constexpr int kMaxRanks = 8;  // CTAs of a cluster of draw_kernel
 
 enum Mode : int { kLookup = 0, kDrafted = 1, kGreedy = 2 };  // drafts without distributions, with them, greedy
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Two fp32 operations an instruction.
-struct Pair {
-  uint64_t v;
-};
-__device__ __forceinline__ Pair pair_of(float lo, float hi) {
-  Pair r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 floats_of(Pair a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-  return r;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  Pair r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ Pair add2(Pair a, Pair b) {
-  Pair r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
 __device__ __forceinline__ Pair exp2_pair(Pair a) {
   const float2 y = floats_of(a);
   return pair_of(exp2_approx(y.x), exp2_approx(y.y));
 }
 
-// A sum as two fp32 numbers: about 46 bits.
-struct Two {
-  float hi, lo;
-};
-__device__ __forceinline__ Two two_sum(float a, float b) {
-  const float s = a + b, z = s - a;
-  return {s, (a - (s - z)) + (b - z)};
-}
-__device__ __forceinline__ Two add(Two a, Two b) {
-  Two s = two_sum(a.hi, b.hi);
-  const float lo = s.lo + (a.lo + b.lo);
-  const float hi = s.hi + lo;
-  return {hi, lo - (hi - s.hi)};
-}
 __device__ __forceinline__ bool above(Two a, Two b) {
   const Two d = add(a, {-b.hi, -b.lo});
   return d.hi > 0.0f || (d.hi == 0.0f && d.lo > 0.0f);

@@ -761,14 +761,15 @@ def ar_grad_clip(grads, max_norm: float, outs=None, kind="l2", eps: float = 1e-6
     return stats, norms, (grads if to is None else to).tensors
 
 
-def ar_adamw_step(params, grads, exp_avgs, exp_avg_sqs, lr: float, step, betas=(0.9, 0.999), eps: float = 1e-8,
+def ar_adamw_step(params, grads, exp_avgs, exp_avg_sqs, lr, step, betas=(0.9, 0.999), eps: float = 1e-8,
                   weight_decay: float = 0.0, grad_scale: float = 1.0, clip=None, masters=None, params_out=None,
                   exp_avgs_out=None, exp_avg_sqs_out=None, masters_out=None, stream=None):
     """One AdamW step on lists of tensors or TensorLists (see include/ar.h), in place unless *_out
     lists are given.
 
     `params` and `grads` float32 or bfloat16, moments float32. `step` counts from 1: an int, or a
-    device int64 tensor of one element that is read when the step runs. `clip`: the stats of
+    device int64 tensor of one element that is read when the step runs; `lr` a float, or a device
+    float32 tensor of one element (for captured steps). `clip`: the stats of
     ar_grad_norm (same grad_scale). `masters`: float32 weights behind the parameters, None for a
     parameter that has none."""
     import torch
@@ -780,10 +781,12 @@ def ar_adamw_step(params, grads, exp_avgs, exp_avg_sqs, lr: float, step, betas=(
     w, wo = _tensors(masters, "masters", p), _tensors(masters_out, "masters_out", p)
     po = _tensors(params_out, "params_out", p)
     mo, vo = _tensors(exp_avgs_out, "exp_avgs_out", p), _tensors(exp_avg_sqs_out, "exp_avg_sqs_out", p)
-    at = 0
+    step_at = lr_at = 0
     if isinstance(step, torch.Tensor):
-        at, step = _vector(step.reshape(-1), torch.int64, 1, "step"), 0
-    desc = _lib.ArAdamwDesc(lr, betas[0], betas[1], eps, weight_decay, grad_scale, int(step), at)
+        step_at, step = _vector(step.reshape(-1), torch.int64, 1, "step"), 0
+    if isinstance(lr, torch.Tensor):
+        lr_at, lr = _vector(lr.reshape(-1), torch.float32, 1, "lr"), 0.0
+    desc = _lib.ArAdamwDesc(lr, betas[0], betas[1], eps, weight_decay, grad_scale, int(step), step_at, lr_at)
     scale = None if clip is None else _vector(clip, torch.float32, 4, "clip")
     c = [None if x is None else x.c for x in (p, g, m, v, w, po, mo, vo, wo)]
     _check(_lib.load().ar_adamw_step(desc, len(p), *c, scale, _stream(stream)), "ar_adamw_step")

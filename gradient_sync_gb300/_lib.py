@@ -70,7 +70,7 @@ class ArNormDesc(ctypes.Structure):
 class ArAdamwDesc(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("grad_scale", c_float),
-                ("step", ctypes.c_int64), ("device_step", c_void_p)]
+                ("step", ctypes.c_int64), ("device_step", c_void_p), ("device_lr", c_void_p)]
 
 
 class ArScoreRows(ctypes.Structure):

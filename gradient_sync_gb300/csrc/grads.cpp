@@ -185,6 +185,7 @@ ar_status ar_adamw_step(const ar_adamw_desc* desc, int n_tensors, const ar_tenso
       !std::isfinite(desc->grad_scale))
     return AR_EINVAL;
   if (desc->device_step == nullptr ? desc->step < 1 : !aligned(desc->device_step, 8)) return AR_EINVAL;
+  if (desc->device_lr != nullptr && !aligned(desc->device_lr, 4)) return AR_EINVAL;
   if (clip != nullptr && !aligned(clip, 4)) return AR_EINVAL;
   if (masters == nullptr && masters_out != nullptr) return AR_EINVAL;
   if (params_out == nullptr) params_out = params;
@@ -240,14 +241,18 @@ ar_status ar_adamw_step(const ar_adamw_desc* desc, int n_tensors, const ar_tenso
     if (e[i].p_out != nullptr) ranges.add(range(e[i].p_out, e[i].count * (e[i].p_bf16 ? 2 : 4), true));
   if (clip != nullptr) ranges.add(range(clip, 16, false));
   if (desc->device_step != nullptr) ranges.add(range(desc->device_step, 8, false));
+  if (desc->device_lr != nullptr) ranges.add(range(desc->device_lr, 4, false));
   if (!ranges.apart()) return AR_EINVAL;
   if ((s = device_ready()) != AR_OK) return s;
   AdamJob job = {};
   job.rates = {float(desc->beta1), float(desc->beta2), float(1.0 - desc->beta1), float(1.0 - desc->beta2), 0.0f, 0.0f,
-               float(desc->eps), float(1.0 - desc->lr * desc->weight_decay)};
-  adam_rates(desc->lr, desc->beta1, desc->beta2, std::max<int64_t>(desc->step, 1), job.rates);
+               float(desc->eps), 0.0f};
+  job.step = std::max<int64_t>(desc->step, 1);
+  adam_rates(desc->lr, desc->beta1, desc->beta2, desc->weight_decay, job.step, job.rates);
   job.device_step = desc->device_step;
+  job.device_lr = desc->device_lr;
   job.lr = desc->lr;
+  job.weight_decay = desc->weight_decay;
   job.beta1 = desc->beta1;
   job.beta2 = desc->beta2;
   job.clip = clip;

@@ -612,11 +612,12 @@ __global__ void __launch_bounds__(kAdamThreads, kAdamCtas) adamw_kernel(const __
   grid_dependency_wait();
   grid_dependents_launch();
   AdamStep step = {job.rates, job.grad_scale, false};
-  if (job.device_step != nullptr) {
+  if (job.device_step != nullptr || job.device_lr != nullptr) {
     __shared__ AdamRates rates;
     if (threadIdx.x == 0) {
       rates = job.rates;
-      adam_rates(job.lr, job.beta1, job.beta2, max(*job.device_step, int64_t(1)), rates);
+      adam_rates(job.device_lr != nullptr ? double(*job.device_lr) : job.lr, job.beta1, job.beta2, job.weight_decay,
+                 job.device_step != nullptr ? max(*job.device_step, int64_t(1)) : job.step, rates);
     }
     __syncthreads();
     step.r = rates;

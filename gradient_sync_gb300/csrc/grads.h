@@ -87,9 +87,11 @@ struct AdamRates {
 };
 
 struct AdamJob {
-  AdamRates rates;             // for a step that the host knows
+  AdamRates rates;             // for a step and a learning rate that the host knows
   const int64_t* device_step;  // null: it does
-  double lr, beta1, beta2;     // for one that it does not
+  const float* device_lr;      // null: it does
+  int64_t step;                // for those that it does not
+  double lr, beta1, beta2, weight_decay;
   const float* clip;           // null: none
   float grad_scale;
   bool in_place;               // every output is its input
@@ -97,11 +99,12 @@ struct AdamJob {
 
 constexpr int kAdamTile = 4096;  // elements
 
-// 1 - beta^t and what a step makes of it.
-__host__ __device__ inline void adam_rates(double lr, double beta1, double beta2, int64_t t, AdamRates& r) {
+// What a step makes of 1 - beta^t and of the learning rate.
+__host__ __device__ inline void adam_rates(double lr, double beta1, double beta2, double weight_decay, int64_t t, AdamRates& r) {
   const double c1 = -expm1(double(t) * log(beta1)), c2 = -expm1(double(t) * log(beta2));
   r.rate = float(lr / c1);
   r.inv_root = float(1.0 / sqrt(c2));
+  r.keep = float(1.0 - lr * weight_decay);
 }
 
 cudaError_t launch_grad_norm(const GradTensor* t, int n, bool clip, const GradJob& job, cudaStream_t stream);

@@ -25,7 +25,7 @@
 //
 // What bounds it, one GB300: 64 sequences of 8 drafts x 131072 bf16, a third of the drafts
 // standing: sums 37 us for the 155 MB of 285 that are not skipped, 51 us (5.5 TB/s, 0.81 of the
-// copy bandwidth) where all are read; the draw 13 us, latency. One sequence of 4 drafts x 32000
+// copy bandwidth) where all are read; the draw 10 us, latency. One sequence of 4 drafts x 32000
 // fp32: 10 us in a graph of calls, two kernels of 3 and 6 us, latency.
 // Taken apart and left: rows held in shared memory by clusters that decide and draw
 // themselves (99 us for the batch: barriers of a cluster take 0.6 us each, five a row, and

@@ -286,6 +286,26 @@ def test_adamw_steps_and_betas(g, t, betas):
     check_adam(before, (*dev, None), None, t, 0.1, betas, 1e-8, 0.0, 1.0)
 
 
+def test_adamw_rates_on_the_device(g):
+    """A captured step whose number and learning rate change between replays: each is that of the formula."""
+    ps, gs, ms, vs, _ = adam_state([(500,), (33,)], "f32", "f32", False)
+    lr, t = torch.empty(1, device="cuda"), torch.empty((), dtype=torch.int64, device="cuda")
+    new = [[torch.empty_like(a) for a in x] for x in (ps, ms, vs)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.ar_adamw_step(ps, gs, ms, vs, lr, t, (0.9, 0.99), weight_decay=0.2, params_out=new[0], exp_avgs_out=new[1],
+                        exp_avg_sqs_out=new[2])
+    for rate, step in ((0.1, 1), (0.003, 40), (1e-5, 7)):
+        lr.fill_(rate)
+        t.fill_(step)
+        graph.replay()
+        check_adam((ps, gs, ms, vs, None), (*new, None), None, step, float(np.float32(rate)), (0.9, 0.99), 1e-8, 0.2, 1.0)
+    # the rate alone
+    g.ar_adamw_step(ps, gs, ms, vs, lr, 7, (0.9, 0.99), weight_decay=0.2, params_out=new[0], exp_avgs_out=new[1],
+                    exp_avg_sqs_out=new[2])
+    check_adam((ps, gs, ms, vs, None), (*new, None), None, 7, float(np.float32(1e-5)), (0.9, 0.99), 1e-8, 0.2, 1.0)
+
+
 def test_adamw_skips_a_step_that_is_not_finite(g):
     for master in (False, True):
         ps, gs, ms, vs, ws = adam_state([(100,), (4097,), (33,)], "bf16", "bf16", master)

@@ -83,7 +83,7 @@ LISTS = ("params", "grads", "exp_avgs", "exp_avg_sqs", "masters", "params_out", 
 
 
 def adam(g, n=None, clip=0, **kw):
-    d = dict(lr=0.1, beta1=0.9, beta2=0.99, eps=1e-8, decay=0.0, scale=1.0, step=1, device=0)
+    d = dict(lr=0.1, beta1=0.9, beta2=0.99, eps=1e-8, decay=0.0, scale=1.0, step=1, device=0, rate=0)
     lists = {k: [((i + 1) * A, 10, 0), ((i + 1) * A + 4096, 7, 0)] for i, k in enumerate(LISTS)}
     d.update({k: v for k, v in kw.items() if k in d})
     lists.update({k: v for k, v in kw.items() if k in lists})
@@ -94,7 +94,7 @@ def adam(g, n=None, clip=0, **kw):
 
 BAD_ADAM = [dict(lr=NAN), dict(lr=INF), dict(beta1=-0.1), dict(beta1=1.0), dict(beta2=1.0), dict(beta2=NAN), dict(eps=-1.0),
             dict(eps=INF), dict(decay=NAN), dict(scale=INF), dict(step=0), dict(step=-4), dict(device=12 * A + 4),
-            dict(clip=12 * A + 2), dict(n=0), dict(masters=None),
+            dict(rate=12 * A + 2), dict(rate=7 * A), dict(clip=12 * A + 2), dict(n=0), dict(masters=None),
             *[{k: [(20 * A, 10, 0), (21 * A, 8, 0)]} for k in LISTS],      # another count
             *[{k: [(20 * A, 10, 0), (0, 7, 0)]} for k in LISTS],           # missing
             *[{k: [(20 * A + 2, 10, 0), (21 * A, 7, 0)]} for k in LISTS],  # misaligned

@@ -706,13 +706,16 @@ def _tensors(x, what: str, like: TensorList | None = None):
     return x
 
 
-def _here(device):
-    """Refuses tensors of another device than the one that the call would run on."""
-    if device.type == "cuda":
-        import torch
+def _queue(stream, device) -> int:
+    """The stream of a call on tensors of a device, which has to be the current one."""
+    if device.type != "cuda":
+        return _stream(stream)
+    import torch
 
-        if device.index != torch._C._cuda_getDevice():
-            raise ValueError(f"tensors on {device}, but the current device is cuda:{torch._C._cuda_getDevice()}")
+    here = torch._C._cuda_getDevice()
+    if device.index != here:
+        raise ValueError(f"tensors on {device}, but the current device is cuda:{here}")
+    return torch._C._cuda_getCurrentRawStream(here) if stream is None else _stream(stream)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -729,7 +732,6 @@ def ar_grad_workspace(grads) -> int:
 
 def _norm_call(grads, max_norm, kind, eps, grad_scale, stats, norms, workspace, stream):
     grads = _tensors(grads, "grads")
-    _here(grads.device)
     n, like = len(grads), grads.like
     stats, stats_at = _output(stats, 4, like, "stats", stream)
     norms, norms_at = _output(norms, n, like, "norms", stream)
@@ -745,7 +747,8 @@ def ar_grad_norm(grads, max_norm: float = float("inf"), kind="l2", eps: float = 
     the device; `ar_adamw_step(clip=stats)` reads them there."""
     grads, n, desc, stats, stats_at, norms, norms_at, workspace, room = _norm_call(
         grads, max_norm, kind, eps, grad_scale, stats, norms, workspace, stream)
-    _check(_lib.load().ar_grad_norm(grads.c, n, desc, stats_at, norms_at, room, _stream(stream)), "ar_grad_norm")
+    _check(_lib.load().ar_grad_norm(grads.c, n, desc, stats_at, norms_at, room, _queue(stream, grads.device)),
+           "ar_grad_norm")
     return stats, norms
 
 
@@ -757,7 +760,7 @@ def ar_grad_clip(grads, max_norm: float, outs=None, kind="l2", eps: float = 1e-6
         grads, max_norm, kind, eps, grad_scale, stats, norms, workspace, stream)
     to = _tensors(outs, "outs", grads)
     _check(_lib.load().ar_grad_clip(grads.c, n, None if to is None else to.c, desc, stats_at, norms_at, room,
-                                    _stream(stream)), "ar_grad_clip")
+                                    _queue(stream, grads.device)), "ar_grad_clip")
     return stats, norms, (grads if to is None else to).tensors
 
 
@@ -775,7 +778,6 @@ def ar_adamw_step(params, grads, exp_avgs, exp_avg_sqs, lr, step, betas=(0.9, 0.
     import torch
 
     p = _tensors(params, "params")
-    _here(p.device)
     g = _tensors(grads, "grads", p)
     m, v = _tensors(exp_avgs, "exp_avgs", p), _tensors(exp_avg_sqs, "exp_avg_sqs", p)
     w, wo = _tensors(masters, "masters", p), _tensors(masters_out, "masters_out", p)
@@ -789,7 +791,7 @@ def ar_adamw_step(params, grads, exp_avgs, exp_avg_sqs, lr, step, betas=(0.9, 0.
     desc = _lib.ArAdamwDesc(lr, betas[0], betas[1], eps, weight_decay, grad_scale, int(step), step_at, lr_at)
     scale = None if clip is None else _vector(clip, torch.float32, 4, "clip")
     c = [None if x is None else x.c for x in (p, g, m, v, w, po, mo, vo, wo)]
-    _check(_lib.load().ar_adamw_step(desc, len(p), *c, scale, _stream(stream)), "ar_adamw_step")
+    _check(_lib.load().ar_adamw_step(desc, len(p), *c, scale, _queue(stream, p.device)), "ar_adamw_step")
 
 
 # ---------------------------------------------------------------- drafts
@@ -818,7 +820,6 @@ def ar_verify_drafts(target, drafts, uniforms=None, draft_start=None, draft_logi
     import torch
 
     ld = _row_major(target, "target")
-    _here(target.device)
     rows, vocab = target.shape
     n_drafts = drafts.shape[0] if drafts.dim() == 1 else -1
     n_seq = rows - n_drafts
@@ -842,7 +843,8 @@ def ar_verify_drafts(target, drafts, uniforms=None, draft_start=None, draft_logi
     tokens, tokens_at = _output(tokens, rows, target, "tokens", stream, torch.int64)
     logp, logp_at = _output(logp, rows, target, "logp", stream)
     workspace, room = _room(workspace, ar_verify_workspace(n_drafts, n_seq, vocab), target, stream)
-    _check(_lib.load().ar_verify_drafts(d, accepted_at, tokens_at, logp_at, room, _stream(stream)), "ar_verify_drafts")
+    _check(_lib.load().ar_verify_drafts(d, accepted_at, tokens_at, logp_at, room, _queue(stream, target.device)),
+           "ar_verify_drafts")
     return accepted, tokens, logp
 
 

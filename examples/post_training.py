@@ -8,7 +8,7 @@ bucket, and the orthogonalised step updates the weights:
     ar_token_logp                     log-probabilities under the old and the reference policy
     ar_policy_loss / ar_preference_loss  the loss and the gradient of the logits, in one call
     BucketedReducer                   the sum over the ranks' gradients
-    ar_grad_clip                      with --max-norm: the global norm, and the clipped gradients
+    ar_grad_norm                      with --max-norm: the global norm, whose coefficient the steps read
     ar_muon_step                      momentum, orthogonalisation, weight update
     ar_adamw_step                     with --adamw: the step of embedding and head
 
@@ -167,13 +167,13 @@ def train(objective="policy", steps=12, ranks=4, answers=64, length=24, vocab=51
             for t in reversed(range(len(policy.weights))):
                 reducer.ready(t)
             reducer.finish()
-            if max_norm is not None:
-                g.ar_grad_clip(grads[0], max_norm)
+            clip = None if max_norm is None else g.ar_grad_norm(grads[0], max_norm)[0]
             g.ar_muon_step(plan, of(matrices, policy.weights), of(matrices, grads[0]), momenta, lr=lr,
-                           workspace=workspace)
+                           workspace=workspace, clip=clip)
             updates += 1
             if others:
-                g.ar_adamw_step(of(others, policy.weights), of(others, grads[0]), *moments, lr=0.1 * lr, step=updates)
+                g.ar_adamw_step(of(others, policy.weights), of(others, grads[0]), *moments, lr=0.1 * lr, step=updates,
+                                clip=clip)
     return rewards
 
 

@@ -602,17 +602,24 @@ def ar_orthogonalize(plan: OrthoPlan, matrices, outs=None, workspace=None, strea
 
 def ar_muon_step(plan: OrthoPlan, params, grads, momenta, lr: float, momentum: float = 0.95, weight_decay: float = 0.0,
                  nesterov: bool = True, adjust="shape", grad_scale: float = 1.0, params_out=None, momenta_out=None,
-                 workspace=None, stream=None):
+                 workspace=None, stream=None, clip=None):
     """One step of the orthogonalised optimiser on every matrix of the plan (see
     include/ar.h); `params` and `momenta` (fp32) are updated in place unless
-    `params_out` / `momenta_out` are given."""
+    `params_out` / `momenta_out` are given. `clip`: the stats of ar_grad_norm
+    (same grad_scale)."""
     p, g = _matrices(plan, params, plan.out_dtype, "params"), _matrices(plan, grads, plan.in_dtype, "grads")
     m = _matrices(plan, momenta, AR_F32, "momenta")
     po, mo = _matrices(plan, params_out, plan.out_dtype, "params_out"), _matrices(plan, momenta_out, AR_F32, "momenta_out")
     workspace, room = _room(workspace, ar_ortho_workspace(plan), params[0], stream)
     d = _lib.ArMuonDesc(float(lr), float(momentum), float(weight_decay), int(bool(nesterov)),
                         ADJUSTS.get(adjust, adjust), float(grad_scale))
-    _check(_lib.load().ar_muon_step(plan.handle, d, p, g, m, po, mo, room, _stream(stream)), "ar_muon_step")
+    if clip is None:
+        _check(_lib.load().ar_muon_step(plan.handle, d, p, g, m, po, mo, room, _stream(stream)), "ar_muon_step")
+        return
+    import torch
+
+    _check(_lib.load().ar_muon_step_clipped(plan.handle, d, p, g, m, po, mo, _vector(clip, torch.float32, 4, "clip"), room,
+                                            _stream(stream)), "ar_muon_step_clipped")
 
 
 # ---------------------------------------------------------------- gradients

@@ -128,6 +128,8 @@ SIGNATURES = {
     "ar_orthogonalize": (c_int, [c_void_p, MATRIXP, MATRIXP, c_void_p, c_void_p]),
     "ar_muon_step": (c_int, [c_void_p, ctypes.POINTER(ArMuonDesc), MATRIXP, MATRIXP, MATRIXP, MATRIXP, MATRIXP,
                              c_void_p, c_void_p]),
+    "ar_muon_step_clipped": (c_int, [c_void_p, ctypes.POINTER(ArMuonDesc), MATRIXP, MATRIXP, MATRIXP, MATRIXP, MATRIXP,
+                                     c_void_p, c_void_p, c_void_p]),
     "ar_grad_workspace": (c_int, [c_int, SIZEP]),
     "ar_grad_norm": (c_int, [TENSORP, c_int, ctypes.POINTER(ArNormDesc), c_void_p, c_void_p, c_void_p, c_void_p]),
     "ar_grad_clip": (c_int, [TENSORP, c_int, TENSORP, ctypes.POINTER(ArNormDesc), c_void_p, c_void_p, c_void_p,

@@ -219,7 +219,7 @@ ar_status ar_orthogonalize(const ar_ortho_plan_t* plan, const ar_matrix* in, con
   if (!apart(std::move(ranges))) return AR_EINVAL;
   const ar_status s = device_ready();
   if (s != AR_OK) return s;
-  const OrthoHyper hyper = {0.0f, 1.0f, 1.0f, 0, 0};
+  const OrthoHyper hyper = {0.0f, 1.0f, 1.0f, 0, 0, nullptr};
   return from_cuda(launch_ortho(*plan, io.data(), hyper, static_cast<char*>(workspace), static_cast<cudaStream_t>(stream)));
 } catch (const std::bad_alloc&) {
   return AR_ENOMEM;
@@ -227,13 +227,20 @@ ar_status ar_orthogonalize(const ar_ortho_plan_t* plan, const ar_matrix* in, con
 
 ar_status ar_muon_step(const ar_ortho_plan_t* plan, const ar_muon_desc* desc, const ar_matrix* params,
                        const ar_matrix* grads, const ar_matrix* momenta, const ar_matrix* params_out,
-                       const ar_matrix* momenta_out, void* workspace, void* stream) try {
+                       const ar_matrix* momenta_out, void* workspace, void* stream) {
+  return ar_muon_step_clipped(plan, desc, params, grads, momenta, params_out, momenta_out, nullptr, workspace, stream);
+}
+
+ar_status ar_muon_step_clipped(const ar_ortho_plan_t* plan, const ar_muon_desc* desc, const ar_matrix* params,
+                               const ar_matrix* grads, const ar_matrix* momenta, const ar_matrix* params_out,
+                               const ar_matrix* momenta_out, const float* clip, void* workspace, void* stream) try {
   if (plan == nullptr || desc == nullptr || params == nullptr || grads == nullptr || momenta == nullptr ||
       guard(workspace) != AR_OK)
     return AR_EINVAL;
   if (!std::isfinite(desc->lr) || !std::isfinite(desc->momentum) || !std::isfinite(desc->weight_decay) ||
       !std::isfinite(desc->grad_scale) || desc->adjust < AR_ADJUST_NONE || desc->adjust > AR_ADJUST_RMS)
     return AR_EINVAL;
+  if (clip != nullptr && reinterpret_cast<uintptr_t>(clip) % 4 != 0) return AR_EINVAL;
   if (params_out == nullptr) params_out = params;
   if (momenta_out == nullptr) momenta_out = momenta;
   const int n = int(plan->mats.size());
@@ -269,11 +276,12 @@ ar_status ar_muon_step(const ar_ortho_plan_t* plan, const ar_muon_desc* desc, co
     q.alpha = float(-double(desc->lr) * adjust);
     set_access(q, c, we);
   }
+  if (clip != nullptr) ranges.push_back({uintptr_t(clip), uintptr_t(clip) + 16, 0, 0, false});
   if (!apart(std::move(ranges))) return AR_EINVAL;
   const ar_status s = device_ready();
   if (s != AR_OK) return s;
   const OrthoHyper hyper = {desc->momentum, desc->grad_scale, float(1.0 - double(desc->lr) * double(desc->weight_decay)), 1,
-                            desc->nesterov != 0};
+                            desc->nesterov != 0, clip};
   return from_cuda(launch_ortho(*plan, io.data(), hyper, static_cast<char*>(workspace), static_cast<cudaStream_t>(stream)));
 } catch (const std::bad_alloc&) {
   return AR_ENOMEM;

@@ -127,6 +127,13 @@ __device__ __forceinline__ void load8(const void* base, int64_t e, int n, bool v
   }
 }
 
+// What gradients are multiplied by; NaN: they are not finite somewhere and count as 0, whatever they hold.
+__device__ __forceinline__ float gradient_scale(const OrthoHyper& h) {
+  if (h.clip == nullptr) return h.grad_scale;
+  return h.clip[3] != 0.0f ? h.clip[1] * h.grad_scale : __int_as_float(0x7fffffff);
+}
+__device__ __forceinline__ float scaled(float g, float scale) { return scale == scale ? g * scale : 0.0f; }
+
 // One CTA a chunk of kOrthoChunk consecutive elements of one matrix. With
 // momentum: M' = mu M + s G, and the update is M' or s G + mu M'.
 template <bool BF16>
@@ -140,6 +147,7 @@ __global__ void __launch_bounds__(256) squares_kernel(const __grid_constant__ Or
   const int64_t total = int64_t(mat.m) * mat.n;
   if (item == 0)  // the products' counters
     for (int k = threadIdx.x; k <= p.n_mat; k += 256) reinterpret_cast<unsigned int*>(p.ws + p.sync_off)[k] = 0;
+  const float scale = gradient_scale(p.hyper);
   const int64_t lo = int64_t(item - p.start[0][i]) * kOrthoChunk, hi = lo + kOrthoChunk < total ? lo + kOrthoChunk : total;
   Squares sum;
   if (io.vec_in) {  // eight elements of one row at a time
@@ -153,7 +161,7 @@ __global__ void __launch_bounds__(256) squares_kernel(const __grid_constant__ Or
         load8<false>(io.m, r * io.m_ld + c, 8, true, mom);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          u[k] *= p.hyper.grad_scale;
+          u[k] = scaled(u[k], scale);
           mom[k] = fmaf(p.hyper.mu, mom[k], u[k]);
           u[k] = p.hyper.nesterov ? fmaf(p.hyper.mu, mom[k], u[k]) : mom[k];
         }
@@ -168,7 +176,7 @@ __global__ void __launch_bounds__(256) squares_kernel(const __grid_constant__ Or
       const int64_t r = io.flat ? 0 : e / cols, c = e - r * cols;
       float u = load_elem<BF16>(io.g, r * io.g_ld + c);
       if (p.hyper.muon) {
-        u *= p.hyper.grad_scale;
+        u = scaled(u, scale);
         const float mom = fmaf(p.hyper.mu, io.m[r * io.m_ld + c], u);
         io.m_out[r * io.m_out_ld + c] = mom;
         u = p.hyper.nesterov ? fmaf(p.hyper.mu, mom, u) : mom;
@@ -198,6 +206,7 @@ __global__ void __launch_bounds__(256, 4) pack_kernel(const __grid_constant__ Or
   const OrthoMat& mat = p.mat[i];
   const OrthoIo& io = p.io[i];
 
+  const float by = gradient_scale(p.hyper);
   // eight elements of row r of the caller's matrix, from column c; n of them exist
   auto update = [&](int64_t r, int64_t c, int n, float (&u)[8]) {
     const bool vec = io.vec_in && n >= 8;
@@ -210,7 +219,7 @@ __global__ void __launch_bounds__(256, 4) pack_kernel(const __grid_constant__ Or
       float grad[8];
       load8<BF16>(io.g, r * io.g_ld + c, n, vec, grad);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] = fmaf(p.hyper.mu, u[k], grad[k] * p.hyper.grad_scale);
+      for (int k = 0; k < 8; ++k) u[k] = fmaf(p.hyper.mu, u[k], scaled(grad[k], by));
     }
   };
   const int local = item - p.start[0][i], rb = local / mat.nb, cb = local - rb * mat.nb;

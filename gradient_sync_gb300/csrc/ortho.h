@@ -45,6 +45,7 @@ struct OrthoIo {
 struct OrthoHyper {
   float mu, grad_scale, keep;  // keep: 1 - lr * weight decay
   int muon, nesterov;
+  const float* clip;  // statistics of a gradient norm (null: none): [1] multiplies gradients too, [3] = 0: they count as 0
 };
 
 struct OrthoPoly {

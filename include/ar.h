@@ -728,6 +728,14 @@ ar_status ar_muon_step(const ar_ortho_plan_t* plan, const ar_muon_desc* desc, co
                        const ar_matrix* grads, const ar_matrix* momenta, const ar_matrix* params_out,
                        const ar_matrix* momenta_out, void* workspace, void* stream);
 
+/* The same with the clipping coefficient of a gradient norm: clip (device, NULL:
+ * none) are the stats of ar_grad_norm below with the same grad_scale. G = c *
+ * grad_scale * gradient, in fp32; where an element of the list was not finite,
+ * G is 0: momentum and weights only decay. */
+ar_status ar_muon_step_clipped(const ar_ortho_plan_t* plan, const ar_muon_desc* desc, const ar_matrix* params,
+                               const ar_matrix* grads, const ar_matrix* momenta, const ar_matrix* params_out,
+                               const ar_matrix* momenta_out, const float* clip, void* workspace, void* stream);
+
 /* ---------------------------------------------------------------- gradients
  * Between the exchange and the weights: the global norm of many gradient
  * tensors, the coefficient that clips it, and the AdamW step, for parameters
@@ -894,8 +902,8 @@ ar_status ar_verify_drafts(const ar_verify_desc* desc, int64_t* accepted, int64_
  * "Collective communication"). From then on the executing calls
  * (ar_execute, ar_execute_host, ar_execute_noalloc, ar_bind,
  * ar_execute_bound, ar_bucket_allreduce, ar_token_logp, ar_policy_loss,
- * ar_preference_loss, ar_orthogonalize, ar_muon_step, ar_grad_norm,
- * ar_grad_clip, ar_adamw_step, ar_verify_drafts) on that device return AR_ETIMEOUT
+ * ar_preference_loss, ar_orthogonalize, ar_muon_step, ar_muon_step_clipped,
+ * ar_grad_norm, ar_grad_clip, ar_adamw_step, ar_verify_drafts) on that device return AR_ETIMEOUT
  * and enqueue nothing, until ar_device_status(1) clears the word. */
 
 /* Read (and clear, if clear != 0) the calling device's sticky status word.

@@ -214,3 +214,21 @@ def test_verify_tensors(g):
                       ("logp", Device(torch.zeros(4))), ("workspace", Device(torch.zeros(8, dtype=torch.uint8)))):
         with pytest.raises(ValueError, match=name):
             g.ar_verify_drafts(**{**ok, name: bad})
+
+
+def test_clip_of_the_orthogonalised_step(g):
+    plan = g.ar_ortho_plan([(4, 8)])
+    lib, d = g._lib.load(), g._lib.ArMuonDesc(0.1, 0.9, 0.0, 1, 0, 1.0)
+
+    def call(clip, ws=9 * A, plan=plan.handle, n=3):
+        m = [(g._lib.ArMatrix * 1)(g._lib.ArMatrix((i + 1) * A, 8)) for i in range(3)]
+        return lib.ar_muon_step_clipped(plan, d, *m, None, None, clip, ws, None)
+
+    assert call(5 * A + 2) == g.AR_EINVAL                   # misaligned
+    for at in (A, 3 * A + 4, 9 * A + 64):                   # weights, momentum, workspace
+        assert call(at) == g.AR_EINVAL
+    assert call(5 * A, ws=0) == g.AR_EINVAL and call(5 * A, plan=None) == g.AR_EINVAL
+    x = [Device(torch.zeros(4, 8))]
+    with pytest.raises(ValueError, match="clip"):
+        g.ar_muon_step(plan, x, x, x, lr=0.1, clip=Device(torch.zeros(3)),
+                       workspace=Device(torch.zeros(1 << 22, dtype=torch.uint8)), stream=0)

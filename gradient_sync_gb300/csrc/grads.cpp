@@ -78,6 +78,12 @@ struct Ranges {
   }
 };
 
+// A number as two of fp32.
+void halves(double v, float& hi, float& low) {
+  hi = float(v);
+  low = std::isfinite(hi) ? float(v - double(hi)) : 0.0f;
+}
+
 ar_status device_ready() {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return AR_ECUDA;
@@ -117,10 +123,6 @@ ar_status grad_norm(const ar_tensor* grads, int n, const ar_tensor* outs, bool c
   if ((s = device_ready()) != AR_OK) return s;
   GradJob job = {};
   job.kind = desc->kind;
-  const auto halves = [](double v, float& hi, float& low) {
-    hi = float(v);
-    low = std::isfinite(hi) ? float(v - double(hi)) : 0.0f;
-  };
   halves(desc->max_norm, job.max_norm, job.max_norm_low);
   halves(desc->eps, job.eps, job.eps_low);
   job.grad_scale = desc->grad_scale;
@@ -248,13 +250,16 @@ ar_status ar_adamw_step(const ar_adamw_desc* desc, int n_tensors, const ar_tenso
   job.rates = {float(desc->beta1), float(desc->beta2), float(1.0 - desc->beta1), float(1.0 - desc->beta2), 0.0f, 0.0f,
                float(desc->eps), 0.0f};
   job.step = std::max<int64_t>(desc->step, 1);
-  adam_rates(desc->lr, desc->beta1, desc->beta2, desc->weight_decay, job.step, job.rates);
+  const double log1 = std::log(desc->beta1), log2 = std::log(desc->beta2);  // (-inf for a beta of 0)
+  job.rates.rate = float(desc->lr / -std::expm1(double(job.step) * log1));
+  job.rates.inv_root = float(1.0 / std::sqrt(-std::expm1(double(job.step) * log2)));
+  job.rates.keep = float(1.0 - desc->lr * desc->weight_decay);
   job.device_step = desc->device_step;
   job.device_lr = desc->device_lr;
-  job.lr = desc->lr;
-  job.weight_decay = desc->weight_decay;
-  job.beta1 = desc->beta1;
-  job.beta2 = desc->beta2;
+  job.lr = float(desc->lr);
+  job.weight_decay = float(desc->weight_decay);
+  halves(log1, job.log1, job.log1_low);
+  halves(log2, job.log2, job.log2_low);
   job.clip = clip;
   job.grad_scale = desc->grad_scale;
   job.in_place = in_place;

@@ -607,20 +607,34 @@ __device__ __forceinline__ void adam_one(const AdamEntry& e, int64_t x, const Ad
   if (e.p_out != nullptr) store1(e.p_out, x, e.p_bf16, w);
 }
 
+// 1 - beta^t from log beta, to 2^-23 of itself or so.
+__device__ __forceinline__ float one_less_power(int64_t t, float log_hi, float log_low) {
+  if (log_hi == -INFINITY) return 1.0f;
+  const float hi = float(t), low = float(t - int64_t(hi)), p = hi * log_hi;
+  const float rest = fmaf(hi, log_hi, -p) + (hi * log_low + low * log_hi), e = expm1f(p);
+  return -(e + rest * (1.0f + e));
+}
+
 template <int CAP>
 __global__ void __launch_bounds__(kAdamThreads, kAdamCtas) adamw_kernel(const __grid_constant__ AdamTable<CAP> t, AdamJob job) {
   grid_dependency_wait();
   grid_dependents_launch();
   AdamStep step = {job.rates, job.grad_scale, false};
   if (job.device_step != nullptr || job.device_lr != nullptr) {
-    __shared__ AdamRates rates;
+    // In fp32 by one thread. 131 M elements, bf16 with masters: 518 us, as with the host's rates (517); in fp64 663;
+    // in fp32 by every thread 543, and the spills that this brings take the host's to 521.
+    __shared__ float rate, inv_root, keep;
     if (threadIdx.x == 0) {
-      rates = job.rates;
-      adam_rates(job.device_lr != nullptr ? double(*job.device_lr) : job.lr, job.beta1, job.beta2, job.weight_decay,
-                 job.device_step != nullptr ? max(*job.device_step, int64_t(1)) : job.step, rates);
+      const int64_t steps = job.device_step != nullptr ? max(*job.device_step, int64_t(1)) : job.step;
+      const float lr = job.device_lr != nullptr ? *job.device_lr : job.lr;
+      rate = lr / one_less_power(steps, job.log1, job.log1_low);
+      inv_root = 1.0f / sqrtf(one_less_power(steps, job.log2, job.log2_low));
+      keep = fmaf(-lr, job.weight_decay, 1.0f);
     }
     __syncthreads();
-    step.r = rates;
+    step.r.rate = rate;
+    step.r.inv_root = inv_root;
+    step.r.keep = keep;
   }
   if (job.clip != nullptr) {
     step.factor = job.clip[1] * job.grad_scale;

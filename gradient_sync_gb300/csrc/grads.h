@@ -91,21 +91,13 @@ struct AdamJob {
   const int64_t* device_step;  // null: it does
   const float* device_lr;      // null: it does
   int64_t step;                // for those that it does not
-  double lr, beta1, beta2, weight_decay;
+  float lr, weight_decay, log1, log1_low, log2, log2_low;  // log beta as two numbers
   const float* clip;           // null: none
   float grad_scale;
   bool in_place;               // every output is its input
 };
 
 constexpr int kAdamTile = 4096;  // elements
-
-// What a step makes of 1 - beta^t and of the learning rate.
-__host__ __device__ inline void adam_rates(double lr, double beta1, double beta2, double weight_decay, int64_t t, AdamRates& r) {
-  const double c1 = -expm1(double(t) * log(beta1)), c2 = -expm1(double(t) * log(beta2));
-  r.rate = float(lr / c1);
-  r.inv_root = float(1.0 / sqrt(c2));
-  r.keep = float(1.0 - lr * weight_decay);
-}
 
 cudaError_t launch_grad_norm(const GradTensor* t, int n, bool clip, const GradJob& job, cudaStream_t stream);
 cudaError_t launch_adamw(const AdamEntry* e, int n, const AdamJob& job, cudaStream_t stream);

@@ -803,7 +803,9 @@ typedef struct {
   int64_t step;              /* t >= 1, where device_step is NULL */
   const int64_t* device_step; /* device: t is read there when the kernels run (a
                                  captured step advances it itself); t < 1 counts as 1 */
-  const float* device_lr;     /* device: the learning rate is read there instead */
+  const float* device_lr;     /* device: the learning rate is read there instead.
+                                 With either, the factors of the step are worked
+                                 out in fp32 (to some 2^-22), else in 64 bits */
 } ar_adamw_desc;
 
 /* One AdamW step on n_tensors tensors, in fp32:

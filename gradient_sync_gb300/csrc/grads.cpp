@@ -225,7 +225,7 @@ ar_status ar_adamw_step(const ar_adamw_desc* desc, int n_tensors, const ar_tenso
     ph.add(wo.data, w.dtype == AR_BF16);
     if (has_master) ph.add(po.data, p.dtype == AR_BF16);
     e[i].phase = ph.value();
-    if (m.data != mo.data || v.data != vo.data || w.data != wo.data) in_place = false;
+    if (m.data != mo.data || v.data != vo.data || w.data != wo.data || p.data != po.data) in_place = false;
   }
   Ranges ranges(size_t(9 * n + 2));
   for (int i = 0; i < n; ++i) ranges.add(range(grads[i], false));

@@ -815,8 +815,8 @@ typedef struct {
  * clip (device): the stats of ar_grad_norm or ar_grad_clip with the same
  * grad_scale (after ar_grad_clip the outs are scaled already: NULL then);
  * where it says that an element was not finite, the step is skipped: every
- * output is its input (in place nothing is written; elsewhere, a parameter
- * beside a master is that one, rounded).
+ * output is its input. (With every output in place nothing is written; with any
+ * elsewhere all are, and a parameter beside a master is that one, rounded.)
  * params fp32 or bf16, each as it is; moments fp32. masters (NULL, or a list in
  * which a tensor without a master has data NULL): fp32 weights W that are
  * updated in the parameters' place; the parameter itself is not read then, and

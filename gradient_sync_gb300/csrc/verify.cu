@@ -189,7 +189,7 @@ __device__ __forceinline__ float max8(const float (&x)[8]) {
 // Sums that the first group's shift does not serve: with the thread's maximum.
 template <class S>
 __device__ __noinline__ Sum careful_sum(const S s, const Piece p, int start, int step, float k) {
-  float top = -INFINITY, sum = 0.0f, x[8];
+  float top = -INFINITY, x[8];
   bool nan = false;
   for (int g = p.lo + start; g < p.hi; g += step) {
     s.load(8 * g + p.first, x);
@@ -200,13 +200,14 @@ __device__ __noinline__ Sum careful_sum(const S s, const Piece p, int start, int
   if (top * k >= kFraction) return {kOdd, INFINITY};
   if (top * k <= -kFraction) return {kLow, 0.5f};
   const float c = ceilf(top * k);
+  Two sum = {0.0f, 0.0f};
   for (int g = p.lo + start; g < p.hi; g += step) {
     s.load(8 * g + p.first, x);
     float t = 0.0f;
     for (int j = 0; j < 8; ++j) t += exp2_approx(fmaf(x[j], k, -c));
-    sum += t;
+    sum = add(sum, {t, 0.0f});
   }
-  return normalized(int(c), sum);
+  return normalized(int(c), sum.hi);
 }
 
 // The sum over every step-th group from the start-th, in one pass: the shift is the first group's. TOP: and the

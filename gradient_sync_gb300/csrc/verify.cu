@@ -210,8 +210,10 @@ __device__ __noinline__ Sum careful_sum(const S s, const Piece p, int start, int
   return normalized(int(c), sum.hi);
 }
 
-// The sum over every step-th group from the start-th, in one pass: the shift is the first group's. TOP: and the
-// largest score with its first place.
+// The sum over every step-th group from the start-th, in one pass: the shift is the first group's. Scores far above it
+// have exponents of up to 100, of which fp32 leaves 2^-18. (A batch taken again with its own maximum as the shift:
+// 64 x 8 drafts x 131072 bf16 49.8 us for 48.1, at a temperature of 0.2 55 for 44.) TOP: and the largest score with its
+// first place.
 template <bool TOP, class S>
 __device__ __forceinline__ Sum fast_sum(const S& s, const Piece& p, int start, int step, float k, Top& top) {
   constexpr int kDeep = 8 / S::kVecs;  // groups of 8 loads in flight
@@ -265,7 +267,9 @@ __device__ __forceinline__ Sum fast_sum(const S& s, const Piece& p, int start, i
     for (int j = 7; j >= 0; --j)
       if (y[j] == top.x) top.at = 8 * best + p.first + j;
   }
-  if (sum.hi > 7.9e-31f && sum.hi < 1.2e30f) return normalized(int(c), sum.hi);
+  // A term that the shift was taken from is above 1/2: less is the sum behind a first group of masked scores, whose
+  // terms may be below fp32's range.
+  if (sum.hi > 0.25f && sum.hi < 1.2e30f) return normalized(int(c), sum.hi);
   return careful_sum(s, p, start, step, k);
 }
 

@@ -843,9 +843,12 @@ ar_status ar_adamw_step(const ar_adamw_desc* desc, int n_tensors, const ar_tenso
  *   w = p_a where a = K_s: the first i whose w_0 + .. + w_i passes u * sum(w)
  * (the speculative sampling of Leviathan et al. 2023 and Chen et al. 2023). p and
  * q are softmaxes of logits / temperature. Their terms are fp32 exponentials,
- * each off by up to about 2^-20 of itself, and 0 below 2^-126 of the sum; sums
- * beyond 64 terms are pairs of fp32 numbers, so that a draw's borders are where
- * those terms put them. Results do not depend on timing.                       */
+ * each off by up to about 2^-20 of itself, or 2^-18 in rows with logits more than
+ * 22 temperature apart, and 0 below 2^-124 of the sum. The sum of a row is made of
+ * some hundred sums of a thread each, of up to 64 terms in fp32 and pairs of fp32
+ * numbers beyond those, which are joined in fp32: off by 2^-20 more. In a draw
+ * sums beyond 64 terms are pairs throughout, so that its borders are where those
+ * terms put them. Results do not depend on timing.                             */
 typedef enum {
   AR_VERIFY_SAMPLE = 0, /* as above; without draft logits q_j is 1 at x_j */
   AR_VERIFY_GREEDY = 1  /* draft j stands while it is the first largest logit of its

@@ -606,7 +606,8 @@ def ar_muon_step(plan: OrthoPlan, params, grads, momenta, lr: float, momentum: f
     """One step of the orthogonalised optimiser on every matrix of the plan (see
     include/ar.h); `params` and `momenta` (fp32) are updated in place unless
     `params_out` / `momenta_out` are given. `clip`: the stats of ar_grad_norm
-    (same grad_scale)."""
+    (same grad_scale); gradients that are not finite somewhere count as 0, and the step goes on
+    along the old momentum, where ar_adamw_step skips its own."""
     p, g = _matrices(plan, params, plan.out_dtype, "params"), _matrices(plan, grads, plan.in_dtype, "grads")
     m = _matrices(plan, momenta, AR_F32, "momenta")
     po, mo = _matrices(plan, params_out, plan.out_dtype, "params_out"), _matrices(plan, momenta_out, AR_F32, "momenta_out")
@@ -780,7 +781,7 @@ def ar_adamw_step(params, grads, exp_avgs, exp_avg_sqs, lr, step, betas=(0.9, 0.
     `params` and `grads` float32 or bfloat16, moments float32. `step` counts from 1: an int, or a
     device int64 tensor of one element that is read when the step runs; `lr` a float, or a device
     float32 tensor of one element (for captured steps). `clip`: the stats of
-    ar_grad_norm (same grad_scale). `masters`: float32 weights behind the parameters, None for a
+    ar_grad_norm (same grad_scale), by which the step is skipped where gradients are not finite. `masters`: float32 weights behind the parameters, None for a
     parameter that has none."""
     import torch
 

@@ -730,8 +730,11 @@ ar_status ar_muon_step(const ar_ortho_plan_t* plan, const ar_muon_desc* desc, co
 
 /* The same with the clipping coefficient of a gradient norm: clip (device, NULL:
  * none) are the stats of ar_grad_norm below with the same grad_scale. G = c *
- * grad_scale * gradient, in fp32; where an element of the list was not finite,
- * G is 0: momentum and weights only decay. */
+ * grad_scale * gradient, in fp32. Where an element of the list was not finite,
+ * G is 0 and the step goes on: M' = mu M, and the weights move by a step of
+ * the usual length along that old momentum (without momentum they only decay).
+ * ar_adamw_step with the same stats is skipped instead. A caller who wants
+ * neither step reads stats[3]. */
 ar_status ar_muon_step_clipped(const ar_ortho_plan_t* plan, const ar_muon_desc* desc, const ar_matrix* params,
                                const ar_matrix* grads, const ar_matrix* momenta, const ar_matrix* params_out,
                                const ar_matrix* momenta_out, const float* clip, void* workspace, void* stream);
@@ -789,8 +792,8 @@ ar_status ar_grad_norm(const ar_tensor* grads, int n_tensors, const ar_norm_desc
 
 /* The same, and outs[i] = c * grad_scale * grads[i], rounded to its type
  * (one fp32 product by the fp32 factor); zeros where an element anywhere is
- * not finite, so that a step with such gradients adds nothing to moments and
- * weights but their decay. outs: the same counts and types; NULL, or an out
+ * not finite. A step on those zeros is none on the gradients, but goes on along
+ * the moments of earlier ones. outs: the same counts and types; NULL, or an out
  * at its gradient's own address: in place (where the factor is 1, nothing is
  * written then). Otherwise no out overlaps another one or any gradient. (A
  * tensor named twice counts twice in ar_grad_norm, and is refused here.) */

@@ -642,8 +642,9 @@ def _dense(t) -> bool:
 
 class TensorList:
     """Tensors of the calls below, marshalled once. Pass it in place of a list when the same
-    tensors are used again and again, as an optimiser does every step: the per-call cost is then
-    independent of their number. It keeps the tensors alive; they may be written to, not moved.
+    tensors are used again and again, as an optimiser does every step: this binding's cost per call is
+    then independent of their number (the library still checks every tensor's address and size and lays
+    out their table). It keeps the tensors alive; they may be written to, not moved.
 
     Tensors are float32 or bfloat16 CUDA tensors of one device whose elements lie one behind the other
     (any order of the dimensions). None stands for a tensor that is not there (masters only)."""

@@ -42,7 +42,7 @@ __device__ __forceinline__ uint4 load16(const char* p) {
 
 // The same with a priority for staying in the L2. Of a list that is to be clipped, the norm keeps the last granules of
 // every stretch, kKept bytes in all, and the scaling, which goes through a stretch from its end, lets them go: 67 M fp32
-// elements 131 -> 125 us, in place 123 -> 118. (28, 55, 80 and 110 MB kept, before the scaling let go of lines: 128, 124.5,
+// elements 131 -> 125 us, in place 123 -> 118, 9 M 20.2 -> 18.6. (28, 55, 80 and 110 MB kept, before the scaling let go of lines: 128, 124.5,
 // 123.5 and 124.7 us.) Lines have the priority until it is taken from them, whatever reads them later: with it, six passes
 // over other 80 MB took 129 us behind any such call, 105 without. It is taken where nothing is scaled too, which is 4 us
 // of a call in place that does not clip.
@@ -513,8 +513,8 @@ __device__ __forceinline__ void scale_stretch(const Table& t, int64_t lo, int64_
   }
 }
 
-// The scaled gradients, stretch by stretch as the norm read them. Bound by HBM: 67 M fp32 elements 79 us with cold
-// caches, 6.8 TB/s; the clipping of them 123 us in all. (A batch of loads a warp, CTAs from the end of the list on:
+// The scaled gradients, stretch by stretch as the norm read them. Bound by HBM: 67 M fp32 elements 84 us with cold
+// caches, 6.4 TB/s; the clipping of them 125 us in all. (A batch of loads a warp, CTAs from the end of the list on:
 // 136 us in place of 129, before the L2 was told what to keep.)
 template <int CAP>
 __global__ void __launch_bounds__(kNormThreads, 2) scale_kernel(const __grid_constant__ GradTable<CAP> t, GradJob job) {
@@ -598,7 +598,7 @@ __device__ __forceinline__ void store1(void* p, int64_t e, bool bf16, float v) {
 }
 
 // A CTA a tile of 4096 elements: 16 a thread, all loads before the first store. Bound by HBM: 131 M parameters (bf16
-// with fp32 masters, 28 bytes each) with their norm 574 us, 1.01 of the copy bandwidth; 29 M fp32 in 203 uneven tensors
+// with fp32 masters, 28 bytes each) with their norm 576 us, 1.01 of the copy bandwidth; 29 M fp32 in 203 uneven tensors
 // 116 us in the kernel, 7.0 TB/s. (Persistent CTAs 671 us for the first, tiles of 2048 595, 8 elements a thread 675.)
 struct AdamStep {
   AdamRates r;

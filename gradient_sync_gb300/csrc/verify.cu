@@ -23,10 +23,13 @@
 // 2^-22 of itself, and by half a last place of its exponent x k - c. Sums beyond 64 terms, and
 // borders, are pairs of fp32 numbers; the draft's weight is subtracted in one fused operation.
 //
-// What bounds it, one GB300: 64 sequences of 8 drafts x 131072 bf16, a third of the drafts
-// standing: sums 37 us for the 155 MB of 285 that are not skipped, 51 us (5.5 TB/s, 0.81 of the
-// copy bandwidth) where all are read; the draw 10 us, latency. One sequence of 4 drafts x 32000
-// fp32: 10 us in a graph of calls, two kernels of 3 and 6 us, latency.
+// What bounds it, one GB300, calls in a graph: 64 sequences of 8 drafts x 131072 bf16, a third of the
+// drafts standing, 47.4 us for the 149 MB of 285 that are not skipped and a draw: latency; 68 us where
+// all stand and all is read. By themselves, caches cold: sums 38.8 us (3.9 TB/s; 56.3 us, 5.1 TB/s, where all
+// is read), draw 19 us, half of it instructions fetched for the first time. One sequence of 4 drafts
+// x 32000 fp32: 10.3 us, two kernels, latency. Draft rows at another alignment than the target's are
+// read by elements (contiguous rows of 131073 tokens 85 us for 48), and threads whose scores are all masked go
+// through their groups twice (all but 50 tokens of a row at -inf: 70 us for 48).
 // Taken apart and left: rows held in shared memory by clusters that decide and draw
 // themselves (99 us for the batch: barriers of a cluster take 0.6 us each, five a row, and
 // rows that fall in vain are drawn from); fp64 for borders (an operation takes a warp some 200
